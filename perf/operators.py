@@ -212,13 +212,11 @@ def prepare(case, seed):
 def _workspace(gb, s):
     """The scratch that a program keeps for its calls."""
     op = s["op"]
-    if op == "append":
+    if op in ("append", "evict"):
         return None
     if op == "decode":
         n = gb.attn_paged_decode_f16_workspace_size(s["B"], s["Hq"], s["Hkv"], s["nq"], s["hi"],
                                                     s["D"], s["weights"] is not None)
-    elif op == "evict":
-        n = gb.kv_paged_evict_workspace_size(s["B"], s["Hkv"], s["hi"], s["budget"])
     elif op == "diff_decode":
         n = gb.attn_diff_paged_decode_f16_workspace_size(s["B"], s["Hq"], s["Hkv"], s["nq"],
                                                          s["hi"], 128)
@@ -249,7 +247,7 @@ def _run_own(s):
         new_lens, kept = gb.kv_paged_evict(s["k_pages"], s["v_pages"], s["weights"], s["table"],
                                            s["kv_lens"], s["budget"], sink=s["sink"],
                                            recent=s["recent"], dst_table=s["dst_table"],
-                                           max_kv_len=s["hi"], workspace=ws)
+                                           max_kv_len=s["hi"])
         return {"k_pages": s["k_pages"], "v_pages": s["v_pages"], "weights": s["weights"],
                 "new_lens": new_lens, "kept": kept}
     if op == "decode":
