@@ -23,41 +23,41 @@ EPS = 1e-5
 def listed():
     return [
         # one decoding step of a busy server: one token for each of 64 sequences
-        {"name": "append, one token", "op": "append", "B": 64, "n": 1, "Hkv": 8, "D": 128,
+        {"name": "append one token", "op": "append", "B": 64, "n": 1, "Hkv": 8, "D": 128,
          "page": 16, "lo": 300, "hi": 6000, "ragged": False, "weights": True},
         # prompts of four requests enter the cache
-        {"name": "append, prompts", "op": "append", "B": 4, "n": 8192, "Hkv": 8, "D": 128,
+        {"name": "append prompts", "op": "append", "B": 4, "n": 8192, "Hkv": 8, "D": 128,
          "page": 64, "lo": 8192, "hi": 9001, "ragged": True, "weights": True},
         # one short conversation: latency
-        {"name": "decode, one short sequence", "op": "decode", "B": 1, "Hq": 32, "Hkv": 8,
+        {"name": "decode one short sequence", "op": "decode", "B": 1, "Hq": 32, "Hkv": 8,
          "D": 128, "nq": 1, "page": 16, "lo": 511, "hi": 511, "weights": False},
         # an ordinary batch of conversations whose caches are kept within a budget
-        {"name": "decode, batch with weights", "op": "decode", "B": 32, "Hq": 32, "Hkv": 8,
+        {"name": "decode batch with weights", "op": "decode", "B": 32, "Hq": 32, "Hkv": 8,
          "D": 128, "nq": 1, "page": 16, "lo": 257, "hi": 8191, "weights": True},
         # long documents, the head layout and lengths of the benchmark's E4M3 decode
-        {"name": "decode, long caches", "op": "decode", "B": 4, "Hq": 6, "Hkv": 1, "D": 256,
+        {"name": "decode long caches", "op": "decode", "B": 4, "Hq": 6, "Hkv": 1, "D": 256,
          "nq": 1, "page": 32, "lo": 65571, "hi": 131072, "weights": False},
         # caches grown past their budget by one page or more of new tokens
-        {"name": "evict, after some tokens", "op": "evict", "B": 16, "Hkv": 8, "D": 128,
+        {"name": "evict after some tokens", "op": "evict", "B": 16, "Hkv": 8, "D": 128,
          "page": 16, "lo": 1030, "hi": 1152, "budget": 1024, "sink": 4, "recent": 255},
         # long prompts cut down to what was attended to
-        {"name": "evict, after long prompts", "op": "evict", "B": 4, "Hkv": 8, "D": 128,
+        {"name": "evict after long prompts", "op": "evict", "B": 4, "Hkv": 8, "D": 128,
          "page": 64, "lo": 20011, "hi": 32768, "budget": 8192, "sink": 4, "recent": 1024},
         # two short prompts of different lengths, padded to one batch
-        {"name": "diff prompt, short", "op": "diff_prompt", "B": 2, "Hq": 8, "Hkv": 4, "Sq": 333,
+        {"name": "diff prompt short", "op": "diff_prompt", "B": 2, "Hq": 8, "Hkv": 4, "Sq": 333,
          "Skv": 333, "causal": True, "ragged": True, "norm": True, "layer": 3},
         # a long prompt
-        {"name": "diff prompt, long", "op": "diff_prompt", "B": 1, "Hq": 16, "Hkv": 16, "Sq": 8192,
+        {"name": "diff prompt long", "op": "diff_prompt", "B": 1, "Hq": 16, "Hkv": 16, "Sq": 8192,
          "Skv": 8192, "causal": True, "ragged": False, "norm": True, "layer": 12},
         # the next piece of a long document against what came before it
-        {"name": "diff prompt, piece of a long one", "op": "diff_prompt", "B": 1, "Hq": 16,
+        {"name": "diff prompt piece of a long one", "op": "diff_prompt", "B": 1, "Hq": 16,
          "Hkv": 4, "Sq": 500, "Skv": 32500, "causal": True, "ragged": False, "norm": True,
          "layer": 12},
         # one short conversation: latency
-        {"name": "diff decode, one sequence", "op": "diff_decode", "B": 1, "Hq": 16, "Hkv": 4,
+        {"name": "diff decode one sequence", "op": "diff_decode", "B": 1, "Hq": 16, "Hkv": 4,
          "nq": 1, "page": 16, "lo": 1501, "hi": 1501, "norm": True, "layer": 0},
         # an ordinary batch of conversations
-        {"name": "diff decode, batch", "op": "diff_decode", "B": 16, "Hq": 16, "Hkv": 4, "nq": 1,
+        {"name": "diff decode batch", "op": "diff_decode", "B": 16, "Hq": 16, "Hkv": 4, "nq": 1,
          "page": 32, "lo": 1000, "hi": 16001, "norm": True, "layer": 20},
     ]
 
