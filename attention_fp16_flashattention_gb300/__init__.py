@@ -42,6 +42,16 @@ _SIGNATURES = {
     "attn_paged_decode_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "attn_paged_decode_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i,
                                    _i, _i, _f, _f, _f, _vp, _sz, _vp]),
+    "kv_paged_append_f16": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _vp, _i,
+                                 _i, _i, _vp]),
+    "attn_paged_decode_f16_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "attn_paged_decode_f16_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
+                                       _i, _i, _i, _i, _f, _vp, _sz, _vp]),
+    "kv_paged_evict": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
+                            _i, _i, _i, _i, _vp]),
+    "attn_diff_paged_decode_f16_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
+    "attn_diff_paged_decode_f16_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _vp, _f, _vp, _vp,
+                                            _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]),
     "vsa_select_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "vsa_select_blocks": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "vsa_sparse_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
@@ -351,6 +361,221 @@ def attn_paged_decode_fwd(q, k_pages, v_pages, page_table, kv_lens, k_scale, v_s
                                       workspace.numel() * workspace.element_size(),
                                       _stream(stream))
     _check("attn_paged_decode_fwd", rc)
+    return o
+
+
+def _need_shape(t, name, shape):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+
+
+def _same_device(**tensors):
+    """Every tensor given on the current device: the call's stream and kernels run there."""
+    import torch
+    dev = torch.cuda.current_device()
+    for name, t in tensors.items():
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+
+
+def _new_tensor(shape, dtype, device, stream):
+    """A tensor this module allocates for a call on `stream` (None: the current stream), taken
+    from that stream's memory so that nothing queued on another stream still uses it."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(nbytes, device, stream):
+    """Workspace bytes for one call on `stream`."""
+    import torch
+    return _new_tensor(max(int(nbytes), 16), torch.uint8, device, stream)
+
+
+def _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, Hkv, D):
+    """Checks an FP16 page pool with its table; returns (pages, page size, max pages)."""
+    import torch
+    _need(k_pages, "k_pages", torch.float16, 4)
+    _need(v_pages, "v_pages", torch.float16, 4)
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(kv_lens, "kv_lens", torch.int32, 1)
+    P, ps, h, d = k_pages.shape
+    if tuple(v_pages.shape) != tuple(k_pages.shape) or d != D or (Hkv is not None and h != Hkv):
+        raise ValueError("k_pages and v_pages must be [P, page, Hkv, D] matching the tokens")
+    if page_table.shape[0] != B or kv_lens.shape[0] != B:
+        raise ValueError("page_table and kv_lens need one row per sequence")
+    return P, ps, page_table.shape[1]
+
+
+def kv_paged_append_f16(k_new, v_new, k_pages, v_pages, page_table, kv_lens, new_lens=None,
+                        weights=None, stream=None):
+    """Append new tokens to paged FP16 caches, in place.  k_new, v_new [B,Hkv,n,D] FP16 (views
+    with a contiguous last dimension and equal strides); pages [P,page,Hkv,D] FP16; page_table
+    int32 [B,max_pages]; kv_lens int32 [B] (device): lengths after the call.  new_lens int32 [B]
+    (device) appends only the first rows of each sequence; weights FP32 [P,Hkv,page] gets zeros
+    at the new slots."""
+    import torch
+    _need_view(k_new, "k_new", torch.float16)
+    _need_view(v_new, "v_new", torch.float16)
+    B, Hkv, n, D = k_new.shape
+    if tuple(v_new.shape) != tuple(k_new.shape) or v_new.stride() != k_new.stride():
+        raise ValueError("k_new and v_new must have the same shape and strides")
+    P, ps, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, Hkv, D)
+    if new_lens is not None:
+        _need(new_lens, "new_lens", torch.int32, 1)
+        _need_shape(new_lens, "new_lens", (B,))
+    if weights is not None:
+        _need(weights, "weights", torch.float32, 3)
+        _need_shape(weights, "weights", (P, Hkv, ps))
+    _same_device(k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages,
+                 page_table=page_table, kv_lens=kv_lens, new_lens=new_lens, weights=weights)
+    rc = load().kv_paged_append_f16(_ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages),
+                                    _ptr(page_table), _ptr(kv_lens), _ptr(new_lens), _ptr(weights),
+                                    B, Hkv, n, D, _strides(k_new), P, ps, max_pages,
+                                    _stream(stream))
+    _check("kv_paged_append_f16", rc)
+    return k_pages, v_pages
+
+
+def attn_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len, D, weights=False):
+    return int(load().attn_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len, D,
+                                                           1 if weights else 0))
+
+
+def attn_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, max_kv_len=None, o=None,
+                              lse=None, weights=None, scale=None, workspace=None, stream=None):
+    """Decode over paged FP16 caches. q [B,Hq,nq,D] FP16; pages [P,page,Hkv,D] FP16; page_table
+    int32 [B,max_pages]; kv_lens int32 [B] (device).  weights FP32 [P,Hkv,page] grows by the
+    attention every cached token receives (what kv_paged_evict ranks by).  max_kv_len defaults to
+    max_pages * page_size (no device read)."""
+    import torch
+    _need(q, "q", torch.float16, 4)
+    B, Hq, nq, D = q.shape
+    P, ps, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, None, D)
+    Hkv = k_pages.shape[2]
+    max_kv_len = max_pages * ps if max_kv_len is None else int(max_kv_len)
+    o = _new_tensor(q.shape, torch.float16, q.device, stream) if o is None else o
+    _need(o, "o", torch.float16, 4)
+    _need_shape(o, "o", q.shape)
+    if lse is not None:
+        _need(lse, "lse", torch.float32)
+        _need_shape(lse, "lse", (B, Hq, nq))
+    if weights is not None:
+        _need(weights, "weights", torch.float32, 3)
+        _need_shape(weights, "weights", (P, Hkv, ps))
+    if workspace is None:
+        workspace = _scratch(attn_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len, D,
+                                                                  weights is not None),
+                             q.device, stream)
+    _same_device(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_lens=kv_lens,
+                 o=o, lse=lse, weights=weights, workspace=workspace)
+    rc = load().attn_paged_decode_f16_fwd(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
+                                          _ptr(kv_lens), _ptr(o), _ptr(lse), _ptr(weights), B, Hq,
+                                          Hkv, nq, D, P, ps, max_pages, max_kv_len,
+                                          _scale(scale, D), _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(),
+                                          _stream(stream))
+    _check("attn_paged_decode_f16_fwd", rc)
+    return o
+
+
+def kv_paged_evict(k_pages, v_pages, weights, page_table, kv_lens, budget, sink=0, recent=0,
+                   dst_table=None, max_kv_len=None, new_lens=None, kept=None, stream=None):
+    """Evict the tokens of paged caches (FP16 or uint8 E4M3 pages) that received the least
+    attention: every KV head keeps its first `sink` tokens, its last `recent` and the heaviest of
+    the rest, `budget` in all, in slots 0.. of dst_table's pages (None: in place).  Returns
+    (new_lens int32 [B], kept int32 [B,Hkv,budget]: old slots, -1 past the new length)."""
+    import torch
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in (torch.float16, torch.uint8):
+        raise ValueError("k_pages must be a float16 or uint8 tensor")
+    _need(k_pages, "k_pages", k_pages.dtype, 4)
+    _need(v_pages, "v_pages", k_pages.dtype, 4)
+    _need(weights, "weights", torch.float32, 3)
+    _need(page_table, "page_table", torch.int32, 2)
+    _need(kv_lens, "kv_lens", torch.int32, 1)
+    P, ps, Hkv, D = k_pages.shape
+    B, max_pages = page_table.shape
+    _need_shape(v_pages, "v_pages", k_pages.shape)
+    _need_shape(weights, "weights", (P, Hkv, ps))
+    _need_shape(kv_lens, "kv_lens", (B,))
+    dst = page_table if dst_table is None else dst_table
+    _need(dst, "dst_table", torch.int32, 2)
+    if dst.shape[0] != B:
+        raise ValueError("dst_table needs one row per sequence")
+    max_kv_len = max_pages * ps if max_kv_len is None else int(max_kv_len)
+    budget = int(budget)
+    if budget <= 0:
+        raise ValueError("budget must be positive")
+    dev = k_pages.device
+    if new_lens is None:
+        new_lens = _new_tensor((B,), torch.int32, dev, stream)
+    if kept is None:
+        kept = _new_tensor((B, Hkv, budget), torch.int32, dev, stream)
+    _need(new_lens, "new_lens", torch.int32, 1)
+    _need_shape(new_lens, "new_lens", (B,))
+    _need(kept, "kept", torch.int32, 3)
+    _need_shape(kept, "kept", (B, Hkv, budget))
+    _same_device(k_pages=k_pages, v_pages=v_pages, weights=weights, page_table=page_table,
+                 kv_lens=kv_lens, dst_table=dst, new_lens=new_lens, kept=kept)
+    rc = load().kv_paged_evict(_ptr(k_pages), _ptr(v_pages), _ptr(weights), _ptr(page_table),
+                               _ptr(dst), _ptr(kv_lens), _ptr(new_lens), _ptr(kept), B, Hkv, D,
+                               k_pages.element_size(), P, ps, max_pages, dst.shape[1], max_kv_len,
+                               budget, int(sink), int(recent), _stream(stream))
+    _check("kv_paged_evict", rc)
+    return new_lens, kept
+
+
+def _need_diff(lambda_vecs, norm_weight, Hq, D):
+    """Checks the learned tensors of differential heads; returns lambda_heads (1 or Hq)."""
+    import torch
+    _need(lambda_vecs, "lambda_vecs", torch.float32)
+    heads = lambda_vecs.shape[1] if lambda_vecs.dim() == 3 else 1
+    if tuple(lambda_vecs.shape) not in ((4, D // 2), (4, 1, D // 2), (4, Hq, D // 2)):
+        raise ValueError("lambda_vecs must be [4, D/2], [4, 1, D/2] or [4, Hq, D/2]")
+    if norm_weight is not None:
+        _need(norm_weight, "norm_weight", torch.float32, 1)
+        _need_shape(norm_weight, "norm_weight", (D,))
+    return heads
+
+
+def attn_diff_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len, D):
+    return int(load().attn_diff_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len, D))
+
+
+def attn_diff_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, lambda_vecs,
+                                   lambda_init, norm_weight=None, eps=1e-5, max_kv_len=None,
+                                   o=None, lse=None, scale=None, workspace=None, stream=None):
+    """Differential attention of the newest tokens over paged FP16 caches: q [B,Hq,nq,128] and
+    the cached keys hold two halves of 64, one per softmax map.  lambda_vecs FP32 [4,Hq or 1,64]
+    (lq1, lk1, lq2, lk2); norm_weight FP32 [128] or None; lse FP32 [B,Hq,2,nq].  scale defaults to
+    1/sqrt(64)."""
+    import torch
+    _need(q, "q", torch.float16, 4)
+    B, Hq, nq, D = q.shape
+    P, ps, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, None, D)
+    Hkv = k_pages.shape[2]
+    heads = _need_diff(lambda_vecs, norm_weight, Hq, D)
+    max_kv_len = max_pages * ps if max_kv_len is None else int(max_kv_len)
+    o = _new_tensor(q.shape, torch.float16, q.device, stream) if o is None else o
+    _need(o, "o", torch.float16, 4)
+    _need_shape(o, "o", q.shape)
+    if lse is not None:
+        _need(lse, "lse", torch.float32)
+        _need_shape(lse, "lse", (B, Hq, 2, nq))
+    if workspace is None:
+        workspace = _scratch(attn_diff_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len,
+                                                                       D), q.device, stream)
+    _same_device(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_lens=kv_lens,
+                 lambda_vecs=lambda_vecs, norm_weight=norm_weight, o=o, lse=lse,
+                 workspace=workspace)
+    rc = load().attn_diff_paged_decode_f16_fwd(
+        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(kv_lens), _ptr(lambda_vecs),
+        heads, float(lambda_init), _ptr(norm_weight), float(eps), _ptr(o), _ptr(lse), B, Hq, Hkv,
+        nq, D, P, ps, max_pages, max_kv_len, _scale(scale, D // 2), _ptr(workspace),
+        workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("attn_diff_paged_decode_f16_fwd", rc)
     return o
 
 

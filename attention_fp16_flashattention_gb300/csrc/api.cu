@@ -103,6 +103,20 @@ int encode_tmap_f16_mask(CUtensorMap* map, const void* base, uint64_t skv, uint6
     return r == CUDA_SUCCESS ? GBATTN_OK : GBATTN_ERR_CUDA;
 }
 
+int encode_tmap_f16_pages(CUtensorMap* map, const void* base, uint64_t D, uint64_t hkv,
+                          uint64_t rows, uint32_t box_rows) {
+    if (load_encoder() != GBATTN_OK) return GBATTN_ERR_CUDA;
+    cuuint64_t dims[3] = {D, hkv, rows};
+    cuuint64_t strides[2] = {D * 2, D * hkv * 2};   // bytes, dims 1 and 2
+    cuuint32_t box[3] = {64, 1, box_rows};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims,
+                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                          CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? GBATTN_OK : GBATTN_ERR_CUDA;
+}
+
 int encode_tmap_u8_pages(CUtensorMap* map, const void* base, uint64_t D, uint64_t hkv,
                          uint64_t rows, uint32_t box_rows) {
     if (load_encoder() != GBATTN_OK) return GBATTN_ERR_CUDA;

@@ -1,0 +1,494 @@
+// The paged KV cache around the decode kernels: new tokens are appended to the
+// pages, and tokens that received little attention are evicted.  The pages name
+// the cache and its page table ("Integrate FP32 v37 prefill and exact E4M3
+// bridge", Implementation: paged cache, live length); how it is filled and kept
+// within a budget is this library's own.
+//
+// Both are copies: nothing but bytes moves, so HBM bounds them.
+#include <cooperative_groups.h>
+#include <cuda_fp16.h>
+
+#include <mutex>
+
+#include "host.h"
+#include "ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace gbattn {
+namespace {
+
+// ---------------------------------------------------------------- append
+
+struct AppendArgs {
+    const uint4 *k, *v;          // new rows, 16-byte chunks
+    uint4 *k_pages, *v_pages;
+    const int32_t *table, *kv_lens, *new_lens;
+    float* weights;              // [num_phys][Hkv][ps] or null
+    uint32_t* status;
+    long long k_sb, k_sh, k_sr;  // source strides in chunks (k and v share them)
+    int n, Hkv, chunk_bits, num_phys, ps, max_pages;
+};
+
+constexpr int kAppendThreads = 256;
+constexpr int kAppendUnroll = 4;   // chunks of K and of V in flight per thread
+
+// One thread moves 16-byte chunk c of head h of new token i (chunks of one token are
+// contiguous in the page: h and c are the fast indexes), kAppendUnroll of them
+// blockDim apart.
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendArgs a) {
+    const int b = blockIdx.y;
+    const int len = a.kv_lens[b];
+    const int count = a.new_lens ? a.new_lens[b] : a.n;
+    if (count < 0 || count > a.n || len < count ||
+        len > static_cast<long long>(a.max_pages) * a.ps) {
+        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(a.status, kDevBadLength);
+        return;
+    }
+    const int row_chunks = a.Hkv << a.chunk_bits;
+    const long long total = static_cast<long long>(count) * row_chunks;
+    long long x = static_cast<long long>(blockIdx.x) * (kAppendThreads * kAppendUnroll) + threadIdx.x;
+    uint4 kv[kAppendUnroll], vv[kAppendUnroll];
+    long long dst[kAppendUnroll];
+#pragma unroll
+    for (int u = 0; u < kAppendUnroll; ++u, x += kAppendThreads) {
+        dst[u] = -1;
+        if (x >= total) continue;
+        const int i = static_cast<int>(x / row_chunks);
+        const int hc = static_cast<int>(x - static_cast<long long>(i) * row_chunks);
+        const int h = hc >> a.chunk_bits, c = hc & ((1 << a.chunk_bits) - 1);
+        const int token = len - count + i;
+        const int page = a.table[static_cast<long long>(b) * a.max_pages + token / a.ps];
+        if (page < 0 || page >= a.num_phys) {
+            atomicOr(a.status, kDevBadPage);
+            continue;
+        }
+        const long long slot = token % a.ps;
+        const long long src = b * a.k_sb + h * a.k_sh + i * a.k_sr + c;
+        kv[u] = a.k[src];
+        vv[u] = a.v[src];
+        dst[u] = (static_cast<long long>(page) * a.ps + slot) * row_chunks + hc;
+        if (a.weights && c == 0)
+            a.weights[(static_cast<long long>(page) * a.Hkv + h) * a.ps + slot] = 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kAppendUnroll; ++u) {
+        if (dst[u] < 0) continue;
+        a.k_pages[dst[u]] = kv[u];
+        a.v_pages[dst[u]] = vv[u];
+    }
+}
+
+// ---------------------------------------------------------------- eviction
+//
+// One cluster of 1..8 CTAs takes one (sequence, KV head).  Of its L > budget slots
+// the first `sink` and the last `recent` stay, and of the middle the M = budget -
+// sink - recent heaviest.  The M-th largest weight is found by radix selection on
+// order-preserving 32-bit keys, eight bits a pass: each CTA counts its part of the
+// slots (keys held in shared memory) into 256 bins, the cluster's CTAs read each
+// other's bins.  Keys above it are kept, and of those equal to it the first slots
+// up to M.  Prefix counts over warps and CTAs give every kept slot its place, in
+// slot order, and the rows move there.
+//
+// In place a row's new slot j is never above its old one, so rows may move in
+// rounds of consecutive j: a round's reads end (cluster barrier) before its
+// writes begin, and a write of this round lands below every later round's reads.
+
+constexpr int kEvictThreads = 512;
+constexpr int kEvictWarps = kEvictThreads / 32;
+constexpr int kEvictRows = 4;            // rows in flight per thread
+constexpr int kEvictMaxCluster = 8;
+constexpr int kEvictMaxKeys = 24576;     // keys held per CTA (96 KB: two CTAs per SM)
+
+struct EvictArgs {
+    uint4 *k_pages, *v_pages;
+    float* weights;             // [num_phys][Hkv][ps]
+    const int32_t *table, *dst_table, *kv_lens;
+    int32_t *new_lens, *kept;   // [B], [B][Hkv][budget]
+    uint32_t* status;
+    int Hkv, chunk_bits, num_phys, ps, max_pages, dst_pages, max_kv, budget, sink, recent;
+    int in_place, keys;         // keys: capacity of the CTA's key array
+};
+
+// Larger key = larger weight; NaN is below everything, -0 equals 0.
+__device__ __forceinline__ uint32_t weight_key(float w) {
+    if (w != w) return 0u;
+    const uint32_t u = __float_as_uint(w == 0.0f ? 0.0f : w);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictArgs a) {
+    extern __shared__ uint32_t s_keys[];
+    __shared__ uint32_t s_hist[2][256];
+    __shared__ uint32_t s_total[256];
+    __shared__ uint32_t s_pick[2];                      // digit, keys still wanted at it
+    __shared__ uint2 s_warp[kEvictWarps], s_cta;        // (above, equal) counts
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = static_cast<int>(cluster.num_blocks());
+    const int rank = static_cast<int>(cluster.block_rank());
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const long long stream = blockIdx.x / C;
+    const int b = static_cast<int>(stream / a.Hkv), h = static_cast<int>(stream - static_cast<long long>(b) * a.Hkv);
+    const int32_t* table = a.table + static_cast<long long>(b) * a.max_pages;
+    const int32_t* dst_table = a.dst_table + static_cast<long long>(b) * a.dst_pages;
+    int32_t* kept = a.kept + stream * a.budget;
+    const int L = a.kv_lens[b];
+    const int first = rank * kEvictThreads + tid, step = C * kEvictThreads;
+
+    // ---- a sequence whose length or pages are out of range stays as it is
+    bool bad = L < 0 || L > a.max_kv;
+    const int n = bad ? 0 : min(L, a.budget);
+    if (bad) {
+        if (first == 0) atomicOr(a.status, kDevBadLength);
+    } else {
+        bool bad_page = false;
+        for (int p = tid; p < (L + a.ps - 1) / a.ps; p += kEvictThreads)
+            bad_page |= table[p] < 0 || table[p] >= a.num_phys;
+        if (!a.in_place)
+            for (int p = tid; p < (n + a.ps - 1) / a.ps; p += kEvictThreads)
+                bad_page |= dst_table[p] < 0 || dst_table[p] >= a.num_phys;
+        bad = __syncthreads_or(bad_page) != 0;
+        if (bad && first == 0) atomicOr(a.status, kDevBadPage);
+    }
+    if (h == 0 && first == 0) a.new_lens[b] = bad ? L : n;
+    for (int j = (bad ? 0 : n) + first; j < a.budget; j += step) kept[j] = -1;
+    if (bad) return;   // the same answer in every CTA of the cluster
+
+    auto weight_at = [&](int t) -> float* {
+        return a.weights + (static_cast<long long>(table[t / a.ps]) * a.Hkv + h) * a.ps + t % a.ps;
+    };
+    if (L <= a.budget) {
+        for (int j = first; j < n; j += step) kept[j] = j;
+        if (a.in_place) return;
+    } else {
+        for (int j = first; j < a.sink; j += step) kept[j] = j;
+        for (int j = first; j < a.recent; j += step) kept[n - a.recent + j] = L - a.recent + j;
+        const int want = n - a.sink - a.recent;   // M
+        if (want > 0) {
+            // this CTA's part [lo, hi) of the middle slots
+            const int mid = L - a.sink - a.recent;
+            const int per = (mid + C - 1) / C;
+            const int lo = min(rank * per, mid), hi = min(lo + per, mid);
+            auto key_at = [&](int i) -> uint32_t {   // i relative to lo
+                return i < a.keys ? s_keys[i] : weight_key(*weight_at(a.sink + lo + i));
+            };
+            for (int i = tid; i < min(hi - lo, a.keys); i += kEvictThreads)
+                s_keys[i] = weight_key(*weight_at(a.sink + lo + i));
+            uint32_t chosen = 0, left = static_cast<uint32_t>(want);
+#pragma unroll 1
+            for (int pass = 0; pass < 4; ++pass) {
+                const int shift = 24 - 8 * pass;
+                uint32_t* hist = s_hist[pass & 1];
+                if (tid < 256) hist[tid] = 0;
+                __syncthreads();
+                for (int i = tid; i < hi - lo; i += kEvictThreads) {
+                    const uint32_t key = key_at(i);
+                    if (pass == 0 || (key >> (shift + 8)) == chosen)
+                        atomicAdd(&hist[(key >> shift) & 255u], 1u);
+                }
+                cluster.sync();
+                if (tid < 256) {
+                    uint32_t sum = 0;
+                    for (int r = 0; r < C; ++r) sum += cluster.map_shared_rank(hist, r)[tid];
+                    s_total[tid] = sum;
+                }
+                __syncthreads();
+                if (warp == 0) {   // the bin that holds the left-th largest: eight bins a lane
+                    uint32_t own = 0;
+                    for (int e = 0; e < 8; ++e) own += s_total[255 - (8 * lane + e)];
+                    uint32_t incl = own;
+#pragma unroll
+                    for (int sh = 1; sh < 32; sh <<= 1) {
+                        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, sh);
+                        if (lane >= sh) incl += y;
+                    }
+                    uint32_t above = incl - own;
+                    if (above < left && left <= incl) {
+                        int e = 0;
+                        while (above + s_total[255 - (8 * lane + e)] < left)
+                            above += s_total[255 - (8 * lane + e++)];
+                        s_pick[0] = 255 - (8 * lane + e);
+                        s_pick[1] = left - above;
+                    }
+                }
+                __syncthreads();
+                chosen = (chosen << 8) | s_pick[0];
+                left = s_pick[1];
+            }
+            // ---- places: a warp takes consecutive slots; (above, equal) counts before it
+            const int wper = ((hi - lo + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
+            const int w0 = min(warp * wper, hi - lo), w1 = min(w0 + wper, hi - lo);
+            uint32_t above = 0, equal = 0;
+            for (int i0 = w0; i0 < w1; i0 += 32) {
+                const int i = i0 + lane;
+                const uint32_t key = i < w1 ? key_at(i) : 0u;
+                above += __popc(__ballot_sync(0xffffffffu, i < w1 && key > chosen));
+                equal += __popc(__ballot_sync(0xffffffffu, i < w1 && key == chosen));
+            }
+            if (lane == 0) s_warp[warp] = make_uint2(above, equal);
+            __syncthreads();
+            above = equal = 0;
+            for (int k = 0; k < kEvictWarps; ++k) {
+                if (k == warp) break;
+                above += s_warp[k].x;
+                equal += s_warp[k].y;
+            }
+            if (tid == kEvictThreads - 1)
+                s_cta = make_uint2(above + s_warp[warp].x, equal + s_warp[warp].y);
+            cluster.sync();
+            for (int r = 0; r < rank; ++r) {
+                const uint2 t = *cluster.map_shared_rank(&s_cta, r);
+                above += t.x;
+                equal += t.y;
+            }
+            const uint32_t below = (1u << lane) - 1u;
+            for (int i0 = w0; i0 < w1; i0 += 32) {
+                const int i = i0 + lane;
+                const uint32_t key = i < w1 ? key_at(i) : 0u;
+                const uint32_t ma = __ballot_sync(0xffffffffu, i < w1 && key > chosen);
+                const uint32_t me = __ballot_sync(0xffffffffu, i < w1 && key == chosen);
+                const uint32_t eq = equal + __popc(me & below);
+                if (i < w1 && (key > chosen || (key == chosen && eq < left)))
+                    kept[a.sink + above + __popc(ma & below) + min(eq, left)] = a.sink + lo + i;
+                above += __popc(ma);
+                equal += __popc(me);
+            }
+        }
+    }
+    cluster.sync();   // kept[] is complete; nobody reads another CTA's shared memory any more
+
+    // ---- the rows: a thread moves one 16-byte chunk of K and of V of kEvictRows rows a round
+    const int chunks = 1 << a.chunk_bits;
+    const int rows_step = kEvictThreads >> a.chunk_bits;   // rows the CTA's threads cover at once
+    const int per_round = rows_step * kEvictRows;
+    const int c = tid & (chunks - 1), r0 = tid >> a.chunk_bits;
+    const long long row_chunks = static_cast<long long>(a.Hkv) << a.chunk_bits;
+    for (int base = 0; base < n; base += C * per_round) {
+        uint4 kr[kEvictRows], vr[kEvictRows];
+        float wr[kEvictRows];
+        int to[kEvictRows];
+#pragma unroll
+        for (int u = 0; u < kEvictRows; ++u) {
+            const int j = base + rank * per_round + u * rows_step + r0;
+            to[u] = -1;
+            if (j >= n) continue;
+            const int t = __ldcg(kept + j);
+            if (a.in_place && t == j) continue;
+            to[u] = j;
+            const long long page = table[t / a.ps];
+            const int slot = t % a.ps;
+            const long long at = (page * a.ps + slot) * row_chunks + (h << a.chunk_bits) + c;
+            kr[u] = a.k_pages[at];
+            vr[u] = a.v_pages[at];
+            if (c == 0) wr[u] = a.weights[(page * a.Hkv + h) * a.ps + slot];
+        }
+        if (a.in_place) cluster.sync();
+#pragma unroll
+        for (int u = 0; u < kEvictRows; ++u) {
+            if (to[u] < 0) continue;
+            const long long page = dst_table[to[u] / a.ps];
+            const int slot = to[u] % a.ps;
+            const long long at = (page * a.ps + slot) * row_chunks + (h << a.chunk_bits) + c;
+            a.k_pages[at] = kr[u];
+            a.v_pages[at] = vr[u];
+            if (c == 0) a.weights[(page * a.Hkv + h) * a.ps + slot] = wr[u];
+        }
+    }
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+// log2 of the 16-byte chunks of one row of D elements, or -1.
+int row_chunk_bits(int D, int elem) {
+    if ((D != 64 && D != 128 && D != 256) || (elem != 1 && elem != 2)) return -1;
+    int bits = 0;
+    while ((16 << bits) < D * elem) ++bits;
+    return bits;
+}
+
+bool pool_supported(int num_phys, int ps) {
+    return ps >= 16 && (ps & (ps - 1)) == 0 && static_cast<long long>(num_phys) * ps <= 0x7FFFFFFFLL;
+}
+
+struct Range {
+    const void* p;
+    size_t n;
+};
+
+// Whether any of the outputs overlaps an input or another output.
+template <int NI, int NO>
+bool any_overlap(const Range (&in)[NI], const Range (&out)[NO]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+    }
+    return false;
+}
+
+}  // namespace
+}  // namespace gbattn
+
+using namespace gbattn;
+
+extern "C" int kv_paged_append_f16(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                                   const int32_t* page_table, const int32_t* kv_lens,
+                                   const int32_t* new_lens, float* weights, int B, int Hkv, int n,
+                                   int D, const int64_t* new_strides, int num_phys_pages,
+                                   int page_size, int max_pages, void* stream) {
+    CallRange nvtx_range("kv_paged_append_f16");
+    if (!k_new || !v_new || !k_pages || !v_pages || !page_table || !kv_lens) return GBATTN_ERR_NULL;
+    if (B <= 0 || Hkv <= 0 || n <= 0 || num_phys_pages <= 0 || page_size <= 0 || max_pages <= 0)
+        return GBATTN_ERR_SHAPE;
+    const int bits = row_chunk_bits(D, 2);
+    if (bits < 0 || !pool_supported(num_phys_pages, page_size)) return GBATTN_ERR_UNSUPPORTED;
+    if (B > 65535 || static_cast<long long>(Hkv) * n > (1LL << 40) / D ||
+        static_cast<long long>(Hkv) > (1 << 24))
+        return GBATTN_ERR_SHAPE;
+    Strides st;
+    if (!make_strides(new_strides, B, Hkv, n, D, false, &st)) return GBATTN_ERR_SHAPE;
+    if (!aligned16(k_new) || !aligned16(v_new) || !aligned16(k_pages) || !aligned16(v_pages) ||
+        misaligned4(page_table) || misaligned4(kv_lens) || misaligned4(new_lens) ||
+        misaligned4(weights))
+        return GBATTN_ERR_ALIGN;
+    const size_t nb = strided_bytes(st, B, Hkv, n, D);
+    const size_t slots = static_cast<size_t>(num_phys_pages) * page_size * Hkv;
+    const Range in[] = {{k_new, nb},
+                        {v_new, nb},
+                        {page_table, static_cast<size_t>(B) * max_pages * 4},
+                        {kv_lens, static_cast<size_t>(B) * 4},
+                        {new_lens, static_cast<size_t>(B) * 4}};
+    const Range out[] = {{k_pages, slots * D * 2}, {v_pages, slots * D * 2}, {weights, slots * 4}};
+    if (any_overlap(in, out)) return GBATTN_ERR_ALIAS;
+    DeviceState dev;
+    const int rc = current_device(&dev);
+    if (rc != GBATTN_OK) return rc;
+    AppendArgs a{};
+    a.k = static_cast<const uint4*>(k_new);
+    a.v = static_cast<const uint4*>(v_new);
+    a.k_pages = static_cast<uint4*>(k_pages);
+    a.v_pages = static_cast<uint4*>(v_pages);
+    a.table = page_table;
+    a.kv_lens = kv_lens;
+    a.new_lens = new_lens;
+    a.weights = weights;
+    a.status = dev.status;
+    a.k_sb = st.b / 8;
+    a.k_sh = st.h / 8;
+    a.k_sr = st.r / 8;
+    a.n = n;
+    a.Hkv = Hkv;
+    a.chunk_bits = bits;
+    a.num_phys = num_phys_pages;
+    a.ps = page_size;
+    a.max_pages = max_pages;
+    const long long per_block = kAppendThreads * kAppendUnroll;
+    const long long blocks = ((static_cast<long long>(n) * Hkv << bits) + per_block - 1) / per_block;
+    if (blocks > 0x7FFFFFFFLL) return GBATTN_ERR_SHAPE;
+    kv_append_kernel<<<dim3(static_cast<unsigned>(blocks), B), kAppendThreads, 0,
+                       static_cast<cudaStream_t>(stream)>>>(a);
+    count_launches(1);
+    return launch_status();
+}
+
+extern "C" int kv_paged_evict(void* k_pages, void* v_pages, float* weights,
+                              const int32_t* page_table, const int32_t* dst_table,
+                              const int32_t* kv_lens, int32_t* new_lens, int32_t* kept, int B,
+                              int Hkv, int D, int elem_size, int num_phys_pages, int page_size,
+                              int max_pages, int dst_pages, int max_kv_len, int budget, int sink,
+                              int recent, void* stream) {
+    CallRange nvtx_range("kv_paged_evict");
+    if (!k_pages || !v_pages || !weights || !page_table || !dst_table || !kv_lens || !new_lens ||
+        !kept)
+        return GBATTN_ERR_NULL;
+    if (B <= 0 || Hkv <= 0 || num_phys_pages <= 0 || page_size <= 0 || max_pages <= 0 ||
+        dst_pages <= 0 || max_kv_len <= 0 || budget <= 0 || sink < 0 || recent < 0 ||
+        static_cast<long long>(sink) + recent > budget ||
+        static_cast<long long>(max_kv_len) > static_cast<long long>(max_pages) * page_size)
+        return GBATTN_ERR_SHAPE;
+    const bool in_place = dst_table == page_table;
+    if (in_place && dst_pages != max_pages) return GBATTN_ERR_SHAPE;
+    const int most = budget < max_kv_len ? budget : max_kv_len;
+    if (static_cast<long long>(most) > static_cast<long long>(dst_pages) * page_size)
+        return GBATTN_ERR_SHAPE;
+    const int bits = row_chunk_bits(D, elem_size);
+    if (bits < 0 || !pool_supported(num_phys_pages, page_size)) return GBATTN_ERR_UNSUPPORTED;
+    const long long streams = static_cast<long long>(B) * Hkv;
+    if (streams > 0x7FFFFFFFLL / kEvictMaxCluster || Hkv > (1 << 24)) return GBATTN_ERR_SHAPE;
+    if (!aligned16(k_pages) || !aligned16(v_pages) || misaligned4(weights) ||
+        misaligned4(page_table) || misaligned4(dst_table) || misaligned4(kv_lens) ||
+        misaligned4(new_lens) || misaligned4(kept))
+        return GBATTN_ERR_ALIGN;
+    const size_t slots = static_cast<size_t>(num_phys_pages) * page_size * Hkv;
+    const size_t rows = slots * D * elem_size;
+    const Range in[] = {{page_table, static_cast<size_t>(B) * max_pages * 4},
+                        {dst_table, static_cast<size_t>(B) * dst_pages * 4},
+                        {kv_lens, static_cast<size_t>(B) * 4}};
+    const Range out[] = {{k_pages, rows},
+                         {v_pages, rows},
+                         {weights, slots * 4},
+                         {new_lens, static_cast<size_t>(B) * 4},
+                         {kept, static_cast<size_t>(streams) * budget * 4}};
+    if (any_overlap(in, out)) return GBATTN_ERR_ALIAS;
+    DeviceState dev;
+    const int rc = current_device(&dev);
+    if (rc != GBATTN_OK) return rc;
+
+    // The largest cluster with which every CTA of the grid is resident at once (two per SM).
+    int C = kEvictMaxCluster;
+    while (C > 1 && streams * C > 2LL * dev.num_sms) C /= 2;
+    EvictArgs a{};
+    a.k_pages = static_cast<uint4*>(k_pages);
+    a.v_pages = static_cast<uint4*>(v_pages);
+    a.weights = weights;
+    a.table = page_table;
+    a.dst_table = dst_table;
+    a.kv_lens = kv_lens;
+    a.new_lens = new_lens;
+    a.kept = kept;
+    a.status = dev.status;
+    a.Hkv = Hkv;
+    a.chunk_bits = bits;
+    a.num_phys = num_phys_pages;
+    a.ps = page_size;
+    a.max_pages = max_pages;
+    a.dst_pages = dst_pages;
+    a.max_kv = max_kv_len;
+    a.budget = budget;
+    a.sink = sink;
+    a.recent = recent;
+    a.in_place = in_place ? 1 : 0;
+    const int need = (max_kv_len + C - 1) / C;
+    a.keys = need < kEvictMaxKeys ? need : kEvictMaxKeys;
+    static std::once_flag once[64];
+    static int attr_rc[64];
+    if (dev.device < 0 || dev.device >= 64) return GBATTN_ERR_CUDA;
+    std::call_once(once[dev.device], [&] {
+        attr_rc[dev.device] = cudaFuncSetAttribute(kv_evict_kernel,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kEvictMaxKeys * 4) == cudaSuccess
+                                  ? GBATTN_OK
+                                  : GBATTN_ERR_CUDA;
+    });
+    if (attr_rc[dev.device] != GBATTN_OK) return attr_rc[dev.device];
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(streams * C));
+    cfg.blockDim = dim3(kEvictThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(a.keys) * 4;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_kernel, a);
+    count_launches(1);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return GBATTN_ERR_CUDA;
+    }
+    return launch_status();
+}

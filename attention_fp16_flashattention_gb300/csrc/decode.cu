@@ -34,6 +34,7 @@
 #include "e4m3.cuh"
 #include "host.h"
 #include "ptx.cuh"
+#include "tiles.cuh"
 
 namespace gbattn {
 namespace {
@@ -84,20 +85,6 @@ struct DecodeArgs {
     __half2 ks2, vs2;
 };
 
-__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                          uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-    uint32_t y;
-    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
-    return y;
-}
-
 template <int kMode>
 __device__ __forceinline__ uint32_t cvt_scaled(uint32_t two_bytes, __half2 s2, float s) {
     const uint32_t h = e4m3x2_to_f16x2(two_bytes);
@@ -116,39 +103,6 @@ __device__ __forceinline__ int pv_col(int j, int g) { return 128 * (j >> 3) + 16
 // Tiles of one stream of a sequence (0 for a rejected length).
 __device__ __forceinline__ uint32_t seq_tiles(int len, int nq, int max_kv) {
     return (len >= nq && len <= max_kv) ? static_cast<uint32_t>((len + kTile - 1) / kTile) : 0u;
-}
-
-// First tile of warp w when W warps share U tiles.
-__device__ __forceinline__ uint32_t warp_start(uint32_t w, uint32_t W, uint32_t U) {
-    return static_cast<uint32_t>(static_cast<unsigned long long>(w) * U / W);
-}
-
-// The warp whose range holds tile u (the last w with warp_start(w) <= u).
-__device__ __forceinline__ uint32_t warp_of(uint32_t u, uint32_t W, uint32_t U) {
-    return static_cast<uint32_t>(((static_cast<unsigned long long>(u) + 1) * W - 1) / U);
-}
-
-// Where tile u lives: sequence b, stream within the sequence (hk * row_groups +
-// rg), tile t within the stream, and the stream's tile range.
-struct TileLoc {
-    int b, sis, t;
-    uint32_t s_end;
-};
-
-__device__ __forceinline__ TileLoc locate(uint32_t u, const uint32_t* prefix, int B, int per_seq) {
-    int lo = 0, hi = B - 1;   // largest b with prefix[b] <= u
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (prefix[mid] <= u) lo = mid; else hi = mid - 1;
-    }
-    TileLoc L;
-    L.b = lo;
-    const uint32_t T = (prefix[lo + 1] - prefix[lo]) / per_seq;
-    const uint32_t off = u - prefix[lo];
-    L.sis = static_cast<int>(off / T);
-    L.t = static_cast<int>(off - L.sis * T);
-    L.s_end = prefix[lo] + (L.sis + 1) * T;
-    return L;
 }
 
 template <int D, int kMode>

@@ -1,0 +1,951 @@
+// Decode attention over a paged FP16 KV cache, with the attention weight every
+// cached token receives added up for eviction, and its differential form.  The
+// FP16 counterpart of the E4M3 decode in decode.cu ("Integrate FP32 v37 prefill
+// and exact E4M3 bridge", Validation: decode of long caches with shared-KV heads).
+//
+// Mathematics.  Row r of a (sequence, KV head) is one query of one head of the
+// group; x[r][t] = scale q_r . k_t over the tokens it sees, p = softmax(x),
+// o_r = sum_t p[r][t] v_t.  In the differential form a query head has two rows,
+// q's halves q1 and q2 against k's halves: the rows are [q1 | 0] and [0 | q2], so
+// both maps are ordinary rows of the same kernel over the same cached bytes, and
+// the merge takes o1 - lambda o2 (diff.cuh).
+//
+// What bounds it: the cache's bytes, 4 D per token and KV head read once, against
+// 4 D FLOPs per row.  So the split is the E4M3 decode's (tiles.cuh): every warp of
+// a persistent grid takes an equal contiguous range of 16-token tiles whatever the
+// lengths, runs its own TMA ring (about 192 KB in flight per SM), and writes the
+// partial (max, sum, O) of each stream its range meets; a merge kernel joins them.
+//   * S^T = K Q^T and O^T += V^T P^T on mma.sync m16n8k16: tokens (QK) and head
+//     width (PV) fill M, the query rows N (8, or 16 where a group has more).  K and
+//     V fragments come from the swizzled stage by ldmatrix (V transposed).
+//   * Probabilities enter the PV product as two FP16 halves, hi = RNE(p) and
+//     lo = RNE(p - hi), about 22 bits: one FP16 value alone would add an error as
+//     large as the output's own rounding, and the extra MMAs are hidden behind the
+//     loads.  Softmax state is FP32 in log2 units; the reference max moves only when
+//     a score passes it by more than 2^8.
+//   * With `weights` the warps also store their scores (FP32, 1/16 of the cache's
+//     bytes at D = 128 and four rows); when the merge has the rows' final max and
+//     sum, a third kernel adds sum_r 2^(x - max) / sum to every token's weight.
+//     Every (token, KV head) is added to once per call, so the result does not
+//     depend on any order unless two sequences share a page.
+#include <cuda_fp16.h>
+#include <mutex>
+
+#include "diff.cuh"
+#include "host.h"
+#include "ptx.cuh"
+#include "tiles.cuh"
+
+namespace gbattn {
+namespace {
+
+constexpr int kTile = 16;        // tokens per tile (one MMA M block)
+constexpr int kMaxSeqs = 4096;   // sequences per launch (prefix table in shared memory)
+constexpr float kRescale = 8.0f;
+constexpr float kLn2 = 0.69314718055994531f;
+
+template <int D>
+struct Cfg {
+    static constexpr int kWarps = D == 256 ? 4 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kStages = D == 64 ? 6 : 3;            // 192 KB per CTA at every width
+    static constexpr int kBoxes = D / 64;                      // 64-column boxes of a row
+    static constexpr int kBox = kTile * 128;                   // bytes of one TMA box
+    static constexpr int kStageBytes = 2 * kBoxes * kBox;      // K boxes, then V boxes
+    static constexpr int kSteps = D / 16;                      // QK k-steps, PV d-blocks
+    static constexpr int kRing = kWarps * kStages * kStageBytes;
+    static constexpr int kBarBytes = kWarps * kStages * 8;
+    static constexpr int kSmem = kRing + kBarBytes + 4 * (kMaxSeqs + 1) + 16 + 1024;
+};
+
+struct DecodeF16Args {
+    const __half* q;
+    const int32_t* table;
+    const int32_t* kv_lens;
+    float* part_o;        // [record][R][D], unnormalised (R = 8 NB rows)
+    float2* part_ml;      // [record][R]: (max in log2 units, sum)
+    uint32_t* prefix_out; // [B + 1]: tiles of all streams of the sequences before b
+    float* scores;        // [tile][pitch][16] log2-unit scores, or null
+    uint32_t* status;
+    uint64_t wait_limit;
+    int fault;   // test hook: 1 = no stage is loaded, 2 = loads stop after two ring rounds
+    int B, Hq, Hkv, nq, G, row_groups, pitch, num_phys, ps, max_pages, max_kv;
+    int maps;             // 1, or 2: row r is map r % 2 of query r / 2
+    float sl2;            // softmax scale * log2(e)
+};
+
+__device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
+
+// Tiles of one stream of a sequence (0 for a rejected length).
+__device__ __forceinline__ uint32_t seq_tiles(int len, int max_kv) {
+    return (len >= 0 && len <= max_kv) ? static_cast<uint32_t>((len + kTile - 1) / kTile) : 0u;
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+    decode_f16_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                      DecodeF16Args a) {
+    using C = Cfg<D>;
+    constexpr int R = 8 * NB;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t warp_sums[C::kWarps];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing);
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + C::kRing + C::kBarBytes);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + kMaxSeqs + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int per_seq = a.Hkv * a.row_groups;
+
+    // ---- tile prefix over sequences (block-wide scan of per-sequence tile counts)
+    {
+        const int per = (a.B + C::kThreads) / C::kThreads;   // entries 0..B over the threads
+        const int b0 = threadIdx.x * per;
+        uint32_t sum = 0;
+        for (int b = b0; b < min(b0 + per, a.B); ++b) {
+            const int len = a.kv_lens[b];
+            if ((len < 0 || len > a.max_kv) && blockIdx.x == 0) atomicOr(a.status, kDevBadLength);
+            const uint32_t n = seq_tiles(len, a.max_kv) * static_cast<uint32_t>(per_seq);
+            prefix[b] = n;   // this thread's own entries; turned into the prefix below
+            sum += n;
+        }
+        uint32_t incl = sum;
+#pragma unroll
+        for (int sh = 1; sh < 32; sh <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, incl, sh);
+            if (lane >= sh) incl += y;
+        }
+        if (lane == 31) warp_sums[warp] = incl;
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < C::kWarps * C::kStages; ++s) mbar_init(&bars[s], 1);
+            *abort_flag = 0;
+            mbar_init_fence();
+        }
+        __syncthreads();
+        uint32_t run = incl - sum;
+        for (int w = 0; w < warp; ++w) run += warp_sums[w];
+        for (int b = b0; b < min(b0 + per, a.B + 1); ++b) {
+            const uint32_t n = b < a.B ? prefix[b] : 0u;
+            prefix[b] = run;   // prefix[B] = total
+            run += n;
+        }
+        __syncthreads();
+        if (blockIdx.x == 0)
+            for (int b = threadIdx.x; b <= a.B; b += C::kThreads) a.prefix_out[b] = prefix[b];
+    }
+    // The merge grid may start launching now; it waits for this grid to finish.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t U = prefix[a.B];
+    const uint32_t W = gridDim.x * C::kWarps;
+    const uint32_t w = blockIdx.x * C::kWarps + warp;
+    const uint32_t u_beg = warp_start(w, W, U), u_end = warp_start(w + 1, W, U);
+    if (u_beg >= u_end) return;
+
+    const WaitCtl wc{a.wait_limit, a.status, abort_flag};
+    uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
+    uint64_t* full = bars + warp * C::kStages;
+    if (lane == 0) {
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+    }
+
+    // First cache row ([page * ps + slot] space) of tile u and its KV head, packed
+    // as (head, row) in 64 bits.
+    auto tile_src = [&](uint32_t u) -> long long {
+        if (u >= u_end) return 0;
+        const TileLoc L = locate(u, prefix, a.B, per_seq);
+        const int tok = L.t * kTile;
+        int page = a.table[static_cast<long long>(L.b) * a.max_pages + tok / a.ps];
+        if (page < 0 || page >= a.num_phys) {
+            atomicOr(a.status, kDevBadPage);
+            page = 0;
+        }
+        const int hk = L.sis / a.row_groups;
+        return (static_cast<long long>(hk) << 32) | static_cast<uint32_t>(page * a.ps + tok % a.ps);
+    };
+    auto issue = [&](uint32_t k, long long src) {   // stage k of this warp's range
+        if (elect_one()) {
+            const int slot = k % C::kStages;
+            uint8_t* dst = ring + slot * C::kStageBytes;
+            const int row = static_cast<int>(src & 0xFFFFFFFFLL), hk = static_cast<int>(src >> 32);
+            mbar_arrive_expect_tx(&full[slot], C::kStageBytes);
+#pragma unroll
+            for (int h = 0; h < C::kBoxes; ++h) {
+                tma_load_3d(dst + h * C::kBox, &tk, &full[slot], 64 * h, hk, row);
+                tma_load_3d(dst + (C::kBoxes + h) * C::kBox, &tv, &full[slot], 64 * h, hk, row);
+            }
+        }
+        __syncwarp();
+    };
+
+    const uint32_t n_tiles = u_end - u_beg;
+    // test hook: the waits for stages never loaded run out (bounded) mid-range
+    const uint32_t n_load = a.fault == 1 ? 0u
+                            : a.fault == 2 ? min(n_tiles, static_cast<uint32_t>(2 * C::kStages))
+                                           : n_tiles;
+    long long src_cur = tile_src(u_beg + lane);          // tiles 0..31 of the range, one per lane
+    long long src_next = tile_src(u_beg + 32 + lane);    // tiles 32..63
+    uint32_t issued = 0;
+    for (; issued < static_cast<uint32_t>(C::kStages - 1) && issued < n_load; ++issued)
+        issue(issued, __shfl_sync(0xffffffffu, src_cur, issued));
+
+    const int g = lane >> 2, c = lane & 3;
+    const int grp = a.Hq / a.Hkv;
+    float o[NB][C::kSteps][4];
+    float m_ref[NB][2], l_sum[NB][2];
+    uint32_t qf[NB][C::kSteps][2];
+    TileLoc L = locate(u_beg, prefix, a.B, per_seq);
+    int kv_len = 0, lim[NB][2], first_masked = 0;
+    long long rec_id = 0;
+    // Start of a stream segment: state reset and the Q operand of the stream's rows.
+    auto begin_stream = [&]() {
+        kv_len = a.kv_lens[L.b];
+        const int hk = L.sis / a.row_groups, rg = L.sis - hk * a.row_groups;
+        rec_id = static_cast<long long>(w) + static_cast<long long>(L.b) * per_seq + L.sis;
+        first_masked = kv_len - a.nq + 1;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = rg * R + 8 * n + 2 * c + e;
+                lim[n][e] = r < a.G ? kv_len - a.nq + (r / a.maps) % a.nq : kv_len - 1;
+                m_ref[n][e] = -INFINITY;
+                l_sum[n][e] = 0.0f;
+            }
+            const int r = rg * R + 8 * n + g;
+            const int rq = r / a.maps, sub = r - rq * a.maps;   // query of the group, map
+            const __half* qp = nullptr;
+            if (r < a.G)
+                qp = a.q + ((static_cast<long long>(L.b) * a.Hq + hk * grp + rq / a.nq) * a.nq +
+                            rq % a.nq) * D;
+#pragma unroll
+            for (int st = 0; st < C::kSteps; ++st) {
+                uint32_t x0 = 0, x1 = 0;
+                // map 0 holds q's first half and zeros, map 1 zeros and its second half
+                if (qp && (a.maps == 1 || (st >= C::kSteps / 2) == (sub == 1))) {
+                    x0 = *reinterpret_cast<const uint32_t*>(qp + 16 * st + 2 * c);
+                    x1 = *reinterpret_cast<const uint32_t*>(qp + 16 * st + 8 + 2 * c);
+                }
+                qf[n][st][0] = x0;
+                qf[n][st][1] = x1;
+            }
+#pragma unroll
+            for (int j = 0; j < C::kSteps; ++j)
+                o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.0f;
+        }
+    };
+    begin_stream();
+
+    // ldmatrix lane addresses within a box: K rows (tokens) lane % 16, column chunk
+    // lane / 16; V rows (lane % 8) + 8 (lane / 16), chunk (lane / 8) % 2.
+    const int k_row = lane & 15, k_ch = lane >> 4;
+    const int v_row = (lane & 7) + ((lane >> 4) << 3), v_ch = (lane >> 3) & 1;
+
+    bool aborted = false;
+    for (uint32_t k = 0; k < n_tiles; ++k) {
+        // keep the ring kStages - 1 tiles ahead
+        if (issued < n_load) {
+            if ((issued & 31u) == 0) {
+                src_cur = src_next;
+                src_next = tile_src(u_beg + issued + 32 + lane);
+            }
+            issue(issued, __shfl_sync(0xffffffffu, src_cur, issued & 31u));
+            ++issued;
+        }
+        const int slot = k % C::kStages;
+        if (!wait_warp(&full[slot], (k / C::kStages) & 1, wc)) {
+            aborted = true;
+            break;
+        }
+        const uint32_t kst = smem_addr(ring + slot * C::kStageBytes);
+        const uint32_t vst = kst + C::kBoxes * C::kBox;
+        const int tb = L.t * kTile;   // first token of the tile
+
+        // ---- S^T = K Q^T: 16 tokens (rows) x R query rows
+        float acc[NB][2][4];
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) acc[n][x][0] = acc[n][x][1] = acc[n][x][2] = acc[n][x][3] = 0.0f;
+#pragma unroll
+        for (int st = 0; st < C::kSteps; ++st) {
+            uint32_t f[4];
+            const int ch = 2 * (st & 3) + k_ch;
+            ldmatrix_x4(f, kst + (st >> 2) * C::kBox + k_row * 128 + ((ch ^ (k_row & 7)) << 4));
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+                mma_16816(acc[n][st & 1], f[0], f[1], f[2], f[3], qf[n][st][0], qf[n][st][1]);
+        }
+        uint32_t ph[NB][2], pl[NB][2];   // P^T operands: hi and lo halves
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            // x[0]: token g, query 2c; x[1]: token g, query 2c+1; x[2], x[3]: token g+8.
+            float x[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = (acc[n][0][e] + acc[n][1][e]) * a.sl2;
+            if (tb + kTile > first_masked) {
+                const int t0 = tb + g, t1 = tb + g + 8;
+                if (t0 > lim[n][0]) x[0] = -INFINITY;
+                if (t0 > lim[n][1]) x[1] = -INFINITY;
+                if (t1 > lim[n][0]) x[2] = -INFINITY;
+                if (t1 > lim[n][1]) x[3] = -INFINITY;
+            }
+            if (a.scores) {
+                const int r0 = 8 * n + 2 * c;
+                const int real = min(R, a.G - (L.sis % a.row_groups) * R);
+                float* sp = a.scores + (static_cast<long long>(u_beg + k) * a.pitch + r0) * kTile + g;
+                if (r0 < real) {
+                    sp[0] = x[0];
+                    sp[8] = x[2];
+                }
+                if (r0 + 1 < real) {
+                    sp[kTile] = x[1];
+                    sp[kTile + 8] = x[3];
+                }
+            }
+            // ---- online softmax for this lane's query columns 2c, 2c+1
+            float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
+#pragma unroll
+            for (int sh = 4; sh < 32; sh <<= 1) {
+                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
+                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
+            }
+            const bool up0 = mx0 > m_ref[n][0] + kRescale, up1 = mx1 > m_ref[n][1] + kRescale;
+            if (__any_sync(0xffffffffu, up0 || up1)) {
+                const float n0 = up0 ? mx0 : m_ref[n][0], n1 = up1 ? mx1 : m_ref[n][1];
+                const float al0 = up0 ? fast_exp2(m_ref[n][0] - n0) : 1.0f;
+                const float al1 = up1 ? fast_exp2(m_ref[n][1] - n1) : 1.0f;
+                m_ref[n][0] = n0;
+                m_ref[n][1] = n1;
+                l_sum[n][0] *= al0;
+                l_sum[n][1] *= al1;
+#pragma unroll
+                for (int j = 0; j < C::kSteps; ++j) {
+                    o[n][j][0] *= al0;
+                    o[n][j][2] *= al0;
+                    o[n][j][1] *= al1;
+                    o[n][j][3] *= al1;
+                }
+            }
+            const float mu0 = m_ref[n][0] == -INFINITY ? 0.0f : m_ref[n][0];
+            const float mu1 = m_ref[n][1] == -INFINITY ? 0.0f : m_ref[n][1];
+            const float p0 = fast_exp2(x[0] - mu0), p1 = fast_exp2(x[1] - mu1);
+            const float p2 = fast_exp2(x[2] - mu0), p3 = fast_exp2(x[3] - mu1);
+            l_sum[n][0] += p0 + p2;
+            l_sum[n][1] += p1 + p3;
+            const __half2 h01 = __floats2half2_rn(p0, p1), h23 = __floats2half2_rn(p2, p3);
+            const float2 f01 = __half22float2(h01), f23 = __half22float2(h23);
+            const __half2 l01 = __floats2half2_rn(p0 - f01.x, p1 - f01.y);
+            const __half2 l23 = __floats2half2_rn(p2 - f23.x, p3 - f23.y);
+            ph[n][0] = movmatrix_trans(h2_bits(h01));
+            ph[n][1] = movmatrix_trans(h2_bits(h23));
+            pl[n][0] = movmatrix_trans(h2_bits(l01));
+            pl[n][1] = movmatrix_trans(h2_bits(l23));
+        }
+        // ---- O^T += V^T P^T: d-block j, rows d = 16 j + g (+ 8)
+        auto pv = [&](uint32_t m01, uint32_t m89) {
+#pragma unroll
+            for (int j = 0; j < C::kSteps; ++j) {
+                uint32_t f[4];
+                const int ch = 2 * (j & 3) + v_ch;
+                ldmatrix_x4_trans(f, vst + (j >> 2) * C::kBox + v_row * 128 +
+                                         ((ch ^ (v_row & 7)) << 4));
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    mma_16816(o[n][j], f[0] & m01, f[1] & m01, f[2] & m89, f[3] & m89, ph[n][0],
+                              ph[n][1]);
+                    mma_16816(o[n][j], f[0] & m01, f[1] & m01, f[2] & m89, f[3] & m89, pl[n][0],
+                              pl[n][1]);
+                }
+            }
+        };
+        if (tb + kTile > kv_len) {   // slots past the cache end may hold anything, NaN too
+            const int t0 = tb + 2 * c;
+            const uint32_t m01 = (t0 < kv_len ? 0xFFFFu : 0u) | (t0 + 1 < kv_len ? 0xFFFF0000u : 0u);
+            const uint32_t m89 = (t0 + 8 < kv_len ? 0xFFFFu : 0u) | (t0 + 9 < kv_len ? 0xFFFF0000u : 0u);
+            pv(m01, m89);
+        } else {
+            pv(0xFFFFFFFFu, 0xFFFFFFFFu);
+        }
+
+        // ---- end of a stream segment: write the partial record, move on
+        const uint32_t u = u_beg + k;
+        if (u + 1 == L.s_end || k + 1 == n_tiles) {
+            const int rbase = (L.sis % a.row_groups) * R;   // query rows of padding are skipped
+            float* po = a.part_o + rec_id * R * D;
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+                float ls0 = l_sum[n][0], ls1 = l_sum[n][1];
+#pragma unroll
+                for (int sh = 4; sh < 32; sh <<= 1) {
+                    ls0 += __shfl_xor_sync(0xffffffffu, ls0, sh);
+                    ls1 += __shfl_xor_sync(0xffffffffu, ls1, sh);
+                }
+                const int r0 = 8 * n + 2 * c;
+                const bool real0 = rbase + r0 < a.G, real1 = rbase + r0 + 1 < a.G;
+#pragma unroll
+                for (int j = 0; j < C::kSteps; ++j) {
+                    const int d = 16 * j + g;
+                    if (real0) {
+                        po[r0 * D + d] = o[n][j][0];
+                        po[r0 * D + d + 8] = o[n][j][2];
+                    }
+                    if (real1) {
+                        po[(r0 + 1) * D + d] = o[n][j][1];
+                        po[(r0 + 1) * D + d + 8] = o[n][j][3];
+                    }
+                }
+                if (g == 0) {
+                    if (real0) a.part_ml[rec_id * R + r0] = make_float2(m_ref[n][0], ls0);
+                    if (real1) a.part_ml[rec_id * R + r0 + 1] = make_float2(m_ref[n][1], ls1);
+                }
+            }
+            if (k + 1 < n_tiles) {
+                L = locate(u + 1, prefix, a.B, per_seq);
+                begin_stream();
+            }
+        } else {
+            ++L.t;
+        }
+    }
+    if (aborted) {
+        // Stages already issued must land before the CTA's shared memory goes away.
+        if (lane == 0) {
+            for (uint32_t k = issued > C::kStages ? issued - C::kStages : 0; k < issued; ++k) {
+                const uint64_t t0 = global_timer_ns();
+                while (!mbar_try_wait(&full[k % C::kStages], (k / C::kStages) & 1))
+                    if (global_timer_ns() - t0 > a.wait_limit) break;
+            }
+        }
+        __syncwarp();
+    }
+}
+
+// Joins the partial records of every query row: with m_r, l_r the max (log2
+// units) and sum of record r, M = max_r m_r, L = sum_r 2^(m_r - M) l_r,
+// O = sum_r 2^(m_r - M) O_r / L and lse = (M + log2 L) ln 2; the records of a row
+// are those of the warps whose tile ranges meet its stream.  One CTA takes one
+// query of one head, its warps every blockDim/32-th record (kBatch in flight each,
+// a lane on D/32 columns); the differential form gives each map half the warps
+// and ends with diff.cuh's combination.  A row that sees nothing gets O = 0,
+// lse = -inf.
+struct MergeArgs {
+    const float* part_o;
+    const float2* part_ml;
+    const uint32_t* prefix;
+    int B, Hq, Hkv, nq, row_groups, R;
+    uint32_t W;
+    __half* o;
+    float* lse;       // [B][Hq][maps][nq] or null
+    float2* row_ml;   // [B][Hkv][G]: (M, 1 / L) for the weights kernel, or null
+    DiffArgs diff;
+};
+
+constexpr int kMergeMaxWarps = 16;
+
+template <int D, bool kDiff>
+__global__ void __launch_bounds__(32 * kMergeMaxWarps)
+    decode_f16_merge_kernel(const MergeArgs a) {
+    constexpr int V = D / 32;
+    constexpr int kMaps = kDiff ? 2 : 1;
+    constexpr int kBatch = 8;
+    __shared__ float s_o[kMergeMaxWarps][D];
+    __shared__ float2 s_ml[kMergeMaxWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const long long row = blockIdx.x;
+    const int per_b = a.Hq * a.nq;
+    const int b = static_cast<int>(row / per_b);
+    const int within = static_cast<int>(row - static_cast<long long>(b) * per_b);
+    const int head = within / a.nq, i = within - head * a.nq;
+    const int grp = a.Hq / a.Hkv;
+    const int hk = head / grp;
+    const int map = kDiff ? warp & 1 : 0;
+    const int r = ((head - hk * grp) * a.nq + i) * kMaps + map;
+    const int rg = r / a.R, n = r - rg * a.R;
+    const int per_seq = a.Hkv * a.row_groups;
+    float lambda = 0.0f;
+    if (kDiff && warp == 0) lambda = diff_lambda(a.diff, head, D / 2, lane);
+    // Launched as a programmatic dependent of the decode grid: wait for its
+    // prefix table and records before reading them.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t U = a.prefix[a.B];
+    const uint32_t T = (a.prefix[b + 1] - a.prefix[b]) / per_seq;
+    uint32_t w0 = 1, w1 = 0;   // empty unless the sequence has tiles
+    long long s_index = 0;
+    if (T > 0) {
+        const int sis = hk * a.row_groups + rg;
+        const uint32_t u0 = a.prefix[b] + sis * T;
+        w0 = warp_of(u0, a.W, U);
+        w1 = warp_of(u0 + T - 1, a.W, U);
+        s_index = static_cast<long long>(b) * per_seq + sis;
+    }
+    // With at least as many tiles as warps every warp range is non-empty, and
+    // the per-record emptiness test (two 64-bit divisions) is skipped.
+    const bool all_busy = U >= a.W;
+    const int lanes = warps / kMaps, wl = kDiff ? warp >> 1 : warp;
+    float mx = -INFINITY, lw = 0.0f, acc[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) acc[e] = 0.0f;
+    for (uint32_t wb = w0 + wl; wb <= w1; wb += lanes * kBatch) {
+        float2 ml[kBatch];
+        float v[kBatch][V];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            const uint32_t w = wb + lanes * j;
+            ml[j] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[j][e] = 0.0f;
+            if (w <= w1 &&
+                (all_busy || warp_start(w, a.W, U) < warp_start(w + 1, a.W, U))) {
+                const long long rec = (w + s_index) * a.R + n;
+                ml[j] = a.part_ml[rec];
+                const float* p = a.part_o + rec * D + lane * V;
+                if constexpr (V == 2) {
+                    const float2 t = *reinterpret_cast<const float2*>(p);
+                    v[j][0] = t.x;
+                    v[j][1] = t.y;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < V; e += 4) {
+                        const float4 t = *reinterpret_cast<const float4*>(p + e);
+                        v[j][e] = t.x;
+                        v[j][e + 1] = t.y;
+                        v[j][e + 2] = t.z;
+                        v[j][e + 3] = t.w;
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            if (ml[j].x > mx) {   // a larger max: rescale what this warp holds
+                const float sc = mx == -INFINITY ? 0.0f : exp2f(mx - ml[j].x);
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] *= sc;
+                lw *= sc;
+                mx = ml[j].x;
+            }
+            // a record whose row saw nothing has max -inf and weight 0; a NaN sum stays NaN
+            const float wt = ml[j].x == -INFINITY ? (ml[j].y == 0.0f ? 0.0f : 1.0f)
+                                                  : exp2f(ml[j].x - mx);
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] += wt * v[j][e];
+            lw += wt * ml[j].y;
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) s_o[warp][lane * V + e] = acc[e];
+    if (lane == 0) s_ml[warp] = make_float2(mx, lw);
+    __syncthreads();
+    if (warp != 0) return;
+    float out[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] = 0.0f;
+#pragma unroll
+    for (int mp = 0; mp < kMaps; ++mp) {
+        float M = -INFINITY, Ls = 0.0f, so[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) so[e] = 0.0f;
+        for (int k = mp; k < warps; k += kMaps) M = fmaxf(M, s_ml[k].x);
+        for (int k = mp; k < warps; k += kMaps) {
+            const float2 ml = s_ml[k];
+            const float wt = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - M);
+            Ls += wt * ml.y;
+#pragma unroll
+            for (int e = 0; e < V; ++e) so[e] += wt * s_o[k][lane * V + e];
+        }
+        const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
+        const float f = mp == 0 ? inv : -lambda * inv;
+#pragma unroll
+        for (int e = 0; e < V; ++e) out[e] += so[e] * f;
+        if (lane == 0) {
+            if (a.lse)
+                a.lse[((static_cast<long long>(b) * a.Hq + head) * kMaps + mp) * a.nq + i] =
+                    Ls == 0.0f ? -INFINITY : (M + log2f(Ls)) * kLn2;
+            if (!kDiff && a.row_ml)
+                a.row_ml[(static_cast<long long>(b) * a.Hkv + hk) * (grp * a.nq) + r] =
+                    make_float2(M, inv);
+        }
+    }
+    if (kDiff && a.diff.norm) {
+        float sq = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) sq += out[e] * out[e];
+        const float rn = rsqrtf(warp_sum(sq) * (1.0f / D) + a.diff.eps) * (1.0f - a.diff.init);
+#pragma unroll
+        for (int e = 0; e < V; ++e) out[e] *= rn * a.diff.norm[lane * V + e];
+    }
+    __half* op = a.o + row * D + lane * V;
+    if constexpr (V == 2) {
+        *reinterpret_cast<uint32_t*>(op) = pack_half2(out[0], out[1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; e += 4)
+            *reinterpret_cast<uint2*>(op + e) =
+                make_uint2(pack_half2(out[e], out[e + 1]), pack_half2(out[e + 2], out[e + 3]));
+    }
+}
+
+// weights[slot] += sum over the group's rows of 2^(x - M) / L for every cached
+// token.  A half-warp takes a tile (one token a lane) and every row group's scores
+// of it; the sum runs in row order in one thread and reaches memory by one atomic
+// add per (token, KV head).
+struct WeightArgs {
+    const float* scores;
+    const float2* row_ml;
+    const uint32_t* prefix;
+    const int32_t* table;
+    const int32_t* kv_lens;
+    float* weights;   // [num_phys][Hkv][ps]
+    int B, Hkv, G, row_groups, R, pitch, num_phys, ps, max_pages;
+};
+
+__global__ void __launch_bounds__(256) decode_f16_weights_kernel(const WeightArgs a) {
+    // A programmatic dependent of the merge, which itself waited for the decode.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int per_seq = a.Hkv * a.row_groups;
+    const uint32_t tiles = a.prefix[a.B] / a.row_groups;   // (sequence, KV head, tile) triples
+    const uint32_t step = gridDim.x * 16;
+    const int tok = threadIdx.x & 15;
+    for (uint32_t x = blockIdx.x * 16 + (threadIdx.x >> 4); x < tiles; x += step) {
+        int lo = 0, hi = a.B - 1;   // largest b whose first triple is <= x
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (a.prefix[mid] / a.row_groups <= x) lo = mid; else hi = mid - 1;
+        }
+        const uint32_t first = a.prefix[lo];
+        const uint32_t T = (a.prefix[lo + 1] - first) / per_seq;
+        const uint32_t off = x - first / a.row_groups;
+        const int hk = static_cast<int>(off / T), t = static_cast<int>(off - hk * T);
+        const int token = t * kTile + tok;
+        if (token >= a.kv_lens[lo]) continue;
+        const float2* ml = a.row_ml + (static_cast<long long>(lo) * a.Hkv + hk) * a.G;
+        float sum = 0.0f;
+        for (int rg = 0; rg < a.row_groups; ++rg) {
+            const long long u = first + static_cast<long long>(hk * a.row_groups + rg) * T + t;
+            const float* sp = a.scores + u * a.pitch * kTile + tok;
+            const int real = min(a.R, a.G - rg * a.R);
+            for (int r = 0; r < real; ++r) {
+                const float s = sp[r * kTile];
+                const float2 m = ml[rg * a.R + r];
+                sum += s == -INFINITY ? 0.0f : fast_exp2(s - m.x) * m.y;
+            }
+        }
+        const int page = a.table[static_cast<long long>(lo) * a.max_pages + token / a.ps];
+        if (page < 0 || page >= a.num_phys) continue;   // flagged by the decode kernel
+        atomicAdd(a.weights + (static_cast<long long>(page) * a.Hkv + hk) * a.ps + token % a.ps, sum);
+    }
+}
+
+int rows_per_group(int G) { return G <= 8 ? 8 : 16; }
+
+int warps_of(int D) { return D == 256 ? 4 : 8; }
+
+size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
+
+// Workspace: partial records for W warps plus one per stream boundary, the
+// (B + 1)-entry tile prefix and, for the weights, every row's (max, 1 / sum) and
+// the scores of every tile that max_kv_len allows.
+struct Layout {
+    size_t o, ml, prefix, row_ml, scores, total;
+};
+
+Layout decode_layout(long long warps, int B, int Hkv, int G, int max_kv, int D, bool weights) {
+    const int R = rows_per_group(G), rgs = (G + R - 1) / R;
+    const size_t streams = static_cast<size_t>(B) * Hkv * rgs;
+    const size_t recs = static_cast<size_t>(warps) + streams;
+    Layout l{};
+    size_t at = 0;
+    l.o = at;
+    at += recs * R * D * 4;
+    l.ml = at;
+    at += recs * R * 8;
+    l.prefix = at;
+    at += round16((static_cast<size_t>(B) + 1) * 4);
+    l.row_ml = at;
+    if (weights) at += round16(static_cast<size_t>(B) * Hkv * G * 8);
+    l.scores = at;
+    if (weights) at += streams * ((max_kv + kTile - 1) / kTile) * (rgs > 1 ? R : G) * kTile * 4;
+    l.total = at + 16;
+    return l;
+}
+
+int sm_count_or_default() {
+    DeviceState d;
+    return current_device(&d) == GBATTN_OK ? d.num_sms : 152;
+}
+
+size_t decode_workspace_size(int B, int Hq, int Hkv, int nq, int max_kv, int D, int maps,
+                             bool weights) {
+    if (B <= 0 || Hq <= 0 || Hkv <= 0 || nq <= 0 || max_kv <= 0 || D <= 0 || Hq % Hkv != 0) return 0;
+    const long long G = static_cast<long long>(Hq / Hkv) * nq * maps;
+    if (G > 0x7FFFFFFFLL) return 0;
+    return decode_layout(static_cast<long long>(sm_count_or_default()) * warps_of(D), B, Hkv,
+                         static_cast<int>(G), max_kv, D, weights).total;
+}
+
+template <int D, int NB>
+int launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, int ctas, const DecodeF16Args& a,
+                  cudaStream_t s) {
+    static std::once_flag once[64];
+    static int rc[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GBATTN_ERR_CUDA;
+    std::call_once(once[dev], [&] {
+        rc[dev] = cudaFuncSetAttribute(decode_f16_kernel<D, NB>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       Cfg<D>::kSmem) == cudaSuccess
+                      ? GBATTN_OK
+                      : GBATTN_ERR_CUDA;
+    });
+    if (rc[dev] != GBATTN_OK) return rc[dev];
+    decode_f16_kernel<D, NB><<<ctas, Cfg<D>::kThreads, Cfg<D>::kSmem, s>>>(tk, tv, a);
+    count_launches(1);
+    return launch_status();
+}
+
+template <int D>
+int launch_decode_rows(int R, const CUtensorMap& tk, const CUtensorMap& tv, int ctas,
+                       const DecodeF16Args& a, cudaStream_t s) {
+    return R == 8 ? launch_decode<D, 1>(tk, tv, ctas, a, s) : launch_decode<D, 2>(tk, tv, ctas, a, s);
+}
+
+// A launch whose CTAs may be placed while the grid before it on the stream still
+// runs; the kernel waits for that grid itself (griddepcontrol.wait).
+template <typename Args>
+int launch_dependent(void (*kernel)(Args), dim3 grid, int threads, cudaStream_t s, const Args& args) {
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args);
+    count_launches(1);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return GBATTN_ERR_CUDA;
+    }
+    return launch_status();
+}
+
+struct DecodeCall {
+    const void *q, *k_pages, *v_pages;
+    const int32_t *page_table, *kv_lens;
+    void* o;
+    float *lse, *weights;
+    int B, Hq, Hkv, nq, D, num_phys, ps, max_pages, max_kv;
+    float scale;
+    void* workspace;
+    size_t workspace_bytes;
+    void* stream;
+    const DiffArgs* diff;   // null: ordinary attention
+};
+
+int run_decode(const DecodeCall& c) {
+    if (!c.q || !c.k_pages || !c.v_pages || !c.page_table || !c.kv_lens || !c.o)
+        return GBATTN_ERR_NULL;
+    if (c.diff && !c.diff->vecs) return GBATTN_ERR_NULL;
+    if (c.B <= 0 || c.Hq <= 0 || c.Hkv <= 0 || c.nq <= 0 || c.num_phys <= 0 || c.ps <= 0 ||
+        c.max_pages <= 0 || c.max_kv <= 0)
+        return GBATTN_ERR_SHAPE;
+    if (c.Hq % c.Hkv != 0 ||
+        static_cast<long long>(c.max_kv) > static_cast<long long>(c.max_pages) * c.ps)
+        return GBATTN_ERR_SHAPE;
+    if (c.diff && c.diff->heads != 1 && c.diff->heads != c.Hq) return GBATTN_ERR_SHAPE;
+    if (c.diff ? c.D != 128 : (c.D != 64 && c.D != 128 && c.D != 256)) return GBATTN_ERR_UNSUPPORTED;
+    if (c.ps < kTile || (c.ps & (c.ps - 1)) != 0 ||
+        static_cast<long long>(c.num_phys) * c.ps > 0x7FFFFFFFLL)
+        return GBATTN_ERR_UNSUPPORTED;
+    if (c.B > kMaxSeqs) return GBATTN_ERR_UNSUPPORTED;
+    const int maps = c.diff ? 2 : 1;
+    const long long rows = static_cast<long long>(c.B) * c.Hq * c.nq;
+    const long long G64 = static_cast<long long>(c.Hq / c.Hkv) * c.nq * maps;
+    if (rows * maps > 0x7FFFFFFFLL || G64 > 0x7FFFFFFFLL) return GBATTN_ERR_SHAPE;
+    const int G = static_cast<int>(G64);
+    const int R = rows_per_group(G), rgs = (G + R - 1) / R;
+    const long long streams = static_cast<long long>(c.B) * c.Hkv * rgs;
+    if (streams > 0x7FFFFFFFLL ||
+        streams * ((static_cast<long long>(c.max_kv) + kTile - 1) / kTile) > 0x7FFFFFFFLL)
+        return GBATTN_ERR_SHAPE;
+    if (!finite_positive(c.scale)) return GBATTN_ERR_SCALE;
+    if (c.diff && (!(fabsf(c.diff->init) <= 3.402823466e38f) ||
+                   (c.diff->norm && !finite_positive(c.diff->eps))))
+        return GBATTN_ERR_SCALE;
+    auto misaligned4 = [](const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; };
+    if (!aligned16(c.q) || !aligned16(c.k_pages) || !aligned16(c.v_pages) || !aligned16(c.o) ||
+        !aligned16(c.workspace) || misaligned4(c.page_table) || misaligned4(c.kv_lens) ||
+        misaligned4(c.lse) || misaligned4(c.weights) ||
+        (c.diff && (misaligned4(c.diff->vecs) || misaligned4(c.diff->norm))))
+        return GBATTN_ERR_ALIGN;
+    struct Range { const void* p; size_t n; };
+    const size_t slots = static_cast<size_t>(c.num_phys) * c.ps * c.Hkv;
+    const Range in[] = {{c.q, static_cast<size_t>(rows) * c.D * 2},
+                        {c.k_pages, slots * c.D * 2},
+                        {c.v_pages, slots * c.D * 2},
+                        {c.page_table, static_cast<size_t>(c.B) * c.max_pages * 4},
+                        {c.kv_lens, static_cast<size_t>(c.B) * 4},
+                        {c.diff ? c.diff->vecs : nullptr,
+                         c.diff ? static_cast<size_t>(c.diff->heads) * 4 * (c.D / 2) * 4 : 0},
+                        {c.diff ? c.diff->norm : nullptr, static_cast<size_t>(c.D) * 4}};
+    const Range out[] = {{c.o, static_cast<size_t>(rows) * c.D * 2},
+                         {c.lse, static_cast<size_t>(rows) * maps * 4},
+                         {c.weights, slots * 4}};
+    auto clash = [&](const Range& x) {
+        for (const Range& y : in)
+            if (overlaps(x.p, x.n, y.p, y.n)) return true;
+        return false;
+    };
+    for (int i = 0; i < 3; ++i) {
+        if (clash(out[i])) return GBATTN_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return GBATTN_ERR_ALIAS;
+    }
+    if (!c.workspace) return GBATTN_ERR_WORKSPACE;
+    DeviceState dev;
+    int rc = current_device(&dev);
+    if (rc != GBATTN_OK) return rc;
+
+    // One CTA per SM; fewer when the workspace holds fewer records.
+    const int cta_warps = warps_of(c.D);
+    auto layout = [&](long long ctas) {
+        return decode_layout(ctas * cta_warps, c.B, c.Hkv, G, c.max_kv, c.D, c.weights != nullptr);
+    };
+    long long ctas = dev.num_sms;
+    while (ctas > 1 && layout(ctas).total > c.workspace_bytes) --ctas;
+    const Layout lay = layout(ctas);
+    if (lay.total > c.workspace_bytes) return GBATTN_ERR_WORKSPACE;
+    const Range ws{c.workspace, lay.total};
+    if (clash(ws)) return GBATTN_ERR_ALIAS;
+    for (const Range& x : out)
+        if (overlaps(ws.p, ws.n, x.p, x.n)) return GBATTN_ERR_ALIAS;
+
+    CUtensorMap tk, tv;
+    const uint64_t total_rows = static_cast<uint64_t>(c.num_phys) * c.ps;
+    if (encode_tmap_f16_pages(&tk, c.k_pages, c.D, c.Hkv, total_rows, kTile) != GBATTN_OK ||
+        encode_tmap_f16_pages(&tv, c.v_pages, c.D, c.Hkv, total_rows, kTile) != GBATTN_OK)
+        return GBATTN_ERR_CUDA;
+
+    uint8_t* wsp = static_cast<uint8_t*>(c.workspace);
+    DecodeF16Args a{};
+    a.q = static_cast<const __half*>(c.q);
+    a.table = c.page_table;
+    a.kv_lens = c.kv_lens;
+    a.part_o = reinterpret_cast<float*>(wsp + lay.o);
+    a.part_ml = reinterpret_cast<float2*>(wsp + lay.ml);
+    a.prefix_out = reinterpret_cast<uint32_t*>(wsp + lay.prefix);
+    a.scores = c.weights ? reinterpret_cast<float*>(wsp + lay.scores) : nullptr;
+    a.status = dev.status;
+    a.wait_limit = wait_limit_ns();
+    a.fault = fault_mode();
+    a.B = c.B;
+    a.Hq = c.Hq;
+    a.Hkv = c.Hkv;
+    a.nq = c.nq;
+    a.G = G;
+    a.row_groups = rgs;
+    a.pitch = rgs > 1 ? R : G;
+    a.num_phys = c.num_phys;
+    a.ps = c.ps;
+    a.max_pages = c.max_pages;
+    a.max_kv = c.max_kv;
+    a.maps = maps;
+    a.sl2 = c.scale * 1.4426950408889634f;
+    cudaStream_t s = static_cast<cudaStream_t>(c.stream);
+    const int n = static_cast<int>(ctas);
+    rc = c.D == 64    ? launch_decode_rows<64>(R, tk, tv, n, a, s)
+         : c.D == 128 ? launch_decode_rows<128>(R, tk, tv, n, a, s)
+                      : launch_decode_rows<256>(R, tk, tv, n, a, s);
+    if (rc != GBATTN_OK) return rc;
+
+    MergeArgs m{};
+    m.part_o = a.part_o;
+    m.part_ml = a.part_ml;
+    m.prefix = a.prefix_out;
+    m.B = c.B;
+    m.Hq = c.Hq;
+    m.Hkv = c.Hkv;
+    m.nq = c.nq;
+    m.row_groups = rgs;
+    m.R = R;
+    m.W = static_cast<uint32_t>(ctas * cta_warps);
+    m.o = static_cast<__half*>(c.o);
+    m.lse = c.lse;
+    m.row_ml = c.weights ? reinterpret_cast<float2*>(wsp + lay.row_ml) : nullptr;
+    if (c.diff) m.diff = *c.diff;
+    const long long recs = m.W / streams + 2;   // records of an average row
+    const int mw = recs > 64 ? 16 : recs > 16 ? 8 : 4;
+    const dim3 mgrid(static_cast<unsigned>(rows));
+    rc = c.diff       ? launch_dependent(decode_f16_merge_kernel<128, true>, mgrid, 32 * mw, s, m)
+         : c.D == 64  ? launch_dependent(decode_f16_merge_kernel<64, false>, mgrid, 32 * mw, s, m)
+         : c.D == 128 ? launch_dependent(decode_f16_merge_kernel<128, false>, mgrid, 32 * mw, s, m)
+                      : launch_dependent(decode_f16_merge_kernel<256, false>, mgrid, 32 * mw, s, m);
+    if (rc != GBATTN_OK || !c.weights) return rc;
+
+    WeightArgs x{};
+    x.scores = a.scores;
+    x.row_ml = m.row_ml;
+    x.prefix = a.prefix_out;
+    x.table = c.page_table;
+    x.kv_lens = c.kv_lens;
+    x.weights = c.weights;
+    x.B = c.B;
+    x.Hkv = c.Hkv;
+    x.G = G;
+    x.row_groups = rgs;
+    x.R = R;
+    x.pitch = a.pitch;
+    x.num_phys = c.num_phys;
+    x.ps = c.ps;
+    x.max_pages = c.max_pages;
+    const long long tiles = static_cast<long long>(c.B) * c.Hkv * ((c.max_kv + kTile - 1) / kTile);
+    const long long want = (tiles + 15) / 16;
+    const unsigned grid = static_cast<unsigned>(want < 8LL * dev.num_sms ? want : 8LL * dev.num_sms);
+    return launch_dependent(decode_f16_weights_kernel, dim3(grid), 256, s, x);
+}
+
+}  // namespace
+}  // namespace gbattn
+
+using namespace gbattn;
+
+extern "C" size_t attn_paged_decode_f16_workspace_size(int B, int Hq, int Hkv, int nq,
+                                                       int max_kv_len, int D, int weights) {
+    return decode_workspace_size(B, Hq, Hkv, nq, max_kv_len, D, 1, weights != 0);
+}
+
+extern "C" int attn_paged_decode_f16_fwd(const void* q, const void* k_pages, const void* v_pages,
+                                         const int32_t* page_table, const int32_t* kv_lens, void* o,
+                                         float* lse, float* weights, int B, int Hq, int Hkv, int nq,
+                                         int D, int num_phys_pages, int page_size, int max_pages,
+                                         int max_kv_len, float scale, void* workspace,
+                                         size_t workspace_bytes, void* stream) {
+    CallRange nvtx_range("attn_paged_decode_f16_fwd");
+    return run_decode({q, k_pages, v_pages, page_table, kv_lens, o, lse, weights, B, Hq, Hkv, nq, D,
+                       num_phys_pages, page_size, max_pages, max_kv_len, scale, workspace,
+                       workspace_bytes, stream, nullptr});
+}
+
+extern "C" size_t attn_diff_paged_decode_f16_workspace_size(int B, int Hq, int Hkv, int nq,
+                                                            int max_kv_len, int D) {
+    return decode_workspace_size(B, Hq, Hkv, nq, max_kv_len, D, 2, false);
+}
+
+extern "C" int attn_diff_paged_decode_f16_fwd(const void* q, const void* k_pages,
+                                              const void* v_pages, const int32_t* page_table,
+                                              const int32_t* kv_lens, const float* lambda_vecs,
+                                              int lambda_heads, float lambda_init,
+                                              const float* norm_weight, float eps, void* o,
+                                              float* lse, int B, int Hq, int Hkv, int nq, int D,
+                                              int num_phys_pages, int page_size, int max_pages,
+                                              int max_kv_len, float scale, void* workspace,
+                                              size_t workspace_bytes, void* stream) {
+    CallRange nvtx_range("attn_diff_paged_decode_f16_fwd");
+    const DiffArgs diff{lambda_vecs, norm_weight, lambda_heads, lambda_init, eps};
+    return run_decode({q, k_pages, v_pages, page_table, kv_lens, o, lse, nullptr, B, Hq, Hkv, nq, D,
+                       num_phys_pages, page_size, max_pages, max_kv_len, scale, workspace,
+                       workspace_bytes, stream, &diff});
+}

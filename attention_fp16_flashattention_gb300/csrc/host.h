@@ -108,6 +108,11 @@ int encode_tmap_f16_mask(CUtensorMap* map, const void* base, uint64_t skv, uint6
 int encode_tmap_u8_pages(CUtensorMap* map, const void* base, uint64_t D, uint64_t hkv,
                          uint64_t rows, uint32_t box_rows);
 
+// The same over paged FP16 rows [rows][hkv][D], with a box of 64 columns (128
+// bytes) x 1 head x box_rows rows.
+int encode_tmap_f16_pages(CUtensorMap* map, const void* base, uint64_t D, uint64_t hkv,
+                          uint64_t rows, uint32_t box_rows);
+
 // One NVTX range per C-ABI call (its name is the entry point's), so profiler
 // timelines show which call queued which kernels.  NVTX v3 is header-only and
 // costs a branch when no tool is attached; builds with GBATTN_NVTX=0 drop it.

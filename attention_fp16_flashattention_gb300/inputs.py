@@ -38,7 +38,7 @@ import math
 import numpy as np
 
 TAGS = {"q": 1, "k": 2, "v": 3, "kpages": 4, "vpages": 5, "table": 6,
-        "qmean": 7, "kmean": 8, "qsig": 9, "ksig": 10, "rows": 11, "mask": 12}
+        "qmean": 7, "kmean": 8, "qsig": 9, "ksig": 10, "rows": 11, "mask": 12, "weights": 13, "lambda": 14, "norm": 15}
 
 
 def _rng(seed, tag):
@@ -268,6 +268,44 @@ def paged_decode_inputs(B, Hq, Hkv, nq, kv_lens, D, seed, page_size=32, spare_pa
         table[b, :n_log[b]] = perm[at:at + n_log[b]]
         at += n_log[b]
     return q, kp, vp, table, kv_lens
+
+
+def paged_f16_inputs(B, Hq, Hkv, nq, kv_lens, D, seed, page_size=32, spare_pages=0, q_std=1.0,
+                     poison=False):
+    """FP16 page-cache inputs: q [B][Hq][nq][D] ~ N(0, q_std^2), k/v pages
+    [P][page_size][Hkv][D] ~ N(0,1), page_table int32 [B][max_pages] (each sequence's pages on
+    a seeded permutation of the pool, -1 past its last page), kv_lens int32 [B], weights FP32
+    [P][Hkv][page_size] >= 0 with a long tail.  poison: NaN in every row that no sequence holds."""
+    kv_lens = np.asarray(kv_lens, dtype=np.int32)
+    n_log = [-(-int(n) // page_size) for n in kv_lens]
+    max_pages = max(max(n_log), 1)
+    P = max(sum(n_log) + spare_pages, 1)
+    q = _normal_fp16(_rng(seed, "q"), (B, Hq, nq, D), q_std)
+    kp = _normal_fp16(_rng(seed, "kpages"), (P, page_size, Hkv, D))
+    vp = _normal_fp16(_rng(seed, "vpages"), (P, page_size, Hkv, D))
+    w = np.exp(1.5 * _rng(seed, "weights").standard_normal((P, Hkv, page_size))).astype(np.float32)
+    perm = _rng(seed, "table").permutation(P).astype(np.int32)
+    table = np.full((B, max_pages), -1, dtype=np.int32)
+    at = 0
+    for b in range(B):
+        table[b, :n_log[b]] = perm[at:at + n_log[b]]
+        at += n_log[b]
+    if poison:
+        held = np.zeros((P, page_size), dtype=bool)
+        for b, n in enumerate(kv_lens):
+            t = np.arange(n)
+            held[table[b, t // page_size], t % page_size] = True
+        kp[~held] = np.nan
+        vp[~held] = np.nan
+    return q, kp, vp, table, kv_lens, w
+
+
+def diff_inputs(Hq, D, seed, heads=None, norm=True):
+    """Learned tensors of differential heads: lambda vectors FP32 [4][heads or Hq][D/2] ~
+    N(0, 0.1^2) and the norm weight FP32 [D] near one (None without norm)."""
+    vecs = 0.1 * _rng(seed, "lambda").standard_normal((4, Hq if heads is None else heads, D // 2))
+    weight = 1.0 + 0.1 * _rng(seed, "norm").standard_normal(D)
+    return vecs.astype(np.float32), weight.astype(np.float32) if norm else None
 
 
 def additive_mask(Sq, Skv, seed, hidden_keys=0.03, slope=2.0 ** -9):

@@ -16,6 +16,11 @@
  *   - decode over a paged E4M3 cache: the newest tokens of ragged sequences
  *     against their whole caches (same page, Validation: the E4M3 decode wave
  *     kernels and the 256000-input decode);
+ *   - a paged FP16 cache: new tokens appended, decode over it with the attention
+ *     weight of every cached token added up, and eviction of the tokens that
+ *     received little (the same page's paged cache, in FP16 and within a budget);
+ *   - differential attention (the difference of two softmax maps, with a learned
+ *     weight per head) for prompts and for decode over the FP16 cache;
  *   - VSA block-sparse attention: 64-token cubes, mean-pooled cube scores pick
  *     the top-k key cubes of every query cube, then attention runs over only
  *     those cubes, optionally with dense prefix tokens and padded boundary
@@ -263,6 +268,126 @@ int attn_paged_decode_fwd(const void* q, const uint8_t* k_pages, const uint8_t* 
                           int page_size, int max_pages, int max_kv_len, float k_scale,
                           float v_scale, float scale, void* workspace, size_t workspace_bytes,
                           void* stream);
+
+/*
+ * Appends new tokens to a paged FP16 KV cache.
+ * Cites: "Integrate FP32 v37 prefill and exact E4M3 bridge", Implementation (paged cache, page
+ * table, live length); the FP16 page format is the E4M3 one with FP16 elements.
+ *   k_new, v_new : [B][Hkv][n][D] FP16; new_strides: their {batch, head, row} element strides or
+ *                  NULL (dense)
+ *   k_pages,
+ *   v_pages      : [num_phys_pages][page_size][Hkv][D] FP16, written in place
+ *   page_table   : int32 [B][max_pages], row b maps logical page p of sequence b to a physical page
+ *   kv_lens      : int32 [B] on the device, cached tokens per sequence AFTER the call (the new ones
+ *                  included), as the decode of the same step takes them
+ *   new_lens     : int32 [B] on the device, how many of the n rows of each sequence are appended
+ *                  (the first ones; 0 for none), or NULL: all n
+ *   weights      : FP32 [num_phys_pages][Hkv][page_size] or NULL; the new tokens' entries become 0
+ *   New token i of sequence b goes to logical slot kv_lens[b] - new_lens[b] + i.  Everything else in
+ *   the pool stays as it is.  No two (sequence, token) pairs of one call may share a slot.
+ *   D is 64, 128 or 256; page_size a power of two >= 16; num_phys_pages * page_size < 2^31;
+ *   B <= 65535.  A sequence with new_lens[b] outside [0, n] or kv_lens[b] outside
+ *   [new_lens[b], max_pages * page_size] sets GBATTN_DEV_BAD_LENGTH and is skipped; a token whose
+ *   page is outside [0, num_phys_pages) sets GBATTN_DEV_BAD_PAGE and is skipped.
+ */
+int kv_paged_append_f16(const void* k_new, const void* v_new, void* k_pages, void* v_pages,
+                        const int32_t* page_table, const int32_t* kv_lens, const int32_t* new_lens,
+                        float* weights, int B, int Hkv, int n, int D, const int64_t* new_strides,
+                        int num_phys_pages, int page_size, int max_pages, void* stream);
+
+/*
+ * Decode attention over a paged FP16 KV cache.
+ * Cites: as attn_paged_decode_fwd, of which this is the FP16 form.
+ *   q          : [B][Hq][nq][D] FP16, the nq newest tokens of every sequence
+ *   k_pages,
+ *   v_pages    : [num_phys_pages][page_size][Hkv][D] FP16
+ *   page_table : int32 [B][max_pages] (entries past ceil(kv_lens[b] / page_size) are not read)
+ *   kv_lens    : int32 [B] on the device, cached tokens per sequence, the new ones included
+ *   o          : [B][Hq][nq][D] FP16; lse optional FP32 [B][Hq][nq] (natural log)
+ *   weights    : optional FP32 [num_phys_pages][Hkv][page_size]: the entry of every cached token
+ *                and KV head grows by the sum of its softmax probabilities over the KV head's
+ *                query heads and the nq queries (what kv_paged_evict ranks by)
+ *   Query i of sequence b sits at position kv_lens[b] - nq + i and sees the cached tokens t <= that
+ *   position; one that sees none (kv_lens[b] < nq) gets O = 0, lse = -inf.  Query head h reads KV
+ *   head h / (Hq / Hkv).  Scores, softmax and accumulation are FP32 (probabilities enter the PV
+ *   product as FP16 hi + lo halves), O is rounded to FP16 once.
+ *   Slots of a page at or past kv_lens[b] may hold anything.  Sequences may share pages; the
+ *   weights of a page that several sequences of one call share receive every sequence's addition,
+ *   in an order that may change the last bit.
+ *   D is 64, 128 or 256; page_size a power of two >= 16; Hq % Hkv == 0; B <= 4096;
+ *   max_kv_len <= max_pages * page_size; num_phys_pages * page_size < 2^31.  A length outside
+ *   [0, max_kv_len] sets GBATTN_DEV_BAD_LENGTH and yields O = 0, lse = -inf for that sequence.  An
+ *   out-of-range page-table entry sets GBATTN_DEV_BAD_PAGE (that page reads physical page 0, and
+ *   its tokens' weights stay as they are).
+ *   The work is split over the warps of a persistent grid as in attn_paged_decode_fwd, and the
+ *   workspace rules are the same: attn_paged_decode_f16_workspace_size() gives the full-speed size
+ *   (weights != 0 adds one FP32 score per query row and cached token, for max_kv_len tokens of
+ *   every sequence), a smaller one runs fewer warps, and below one CTA's worth the call returns
+ *   GBATTN_ERR_WORKSPACE.
+ */
+size_t attn_paged_decode_f16_workspace_size(int B, int Hq, int Hkv, int nq, int max_kv_len, int D,
+                                            int weights);
+int attn_paged_decode_f16_fwd(const void* q, const void* k_pages, const void* v_pages,
+                              const int32_t* page_table, const int32_t* kv_lens, void* o, float* lse,
+                              float* weights, int B, int Hq, int Hkv, int nq, int D,
+                              int num_phys_pages, int page_size, int max_pages, int max_kv_len,
+                              float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Eviction from a paged KV cache by accumulated attention weight.
+ * The pages have no counterpart: it keeps the caches that the decode calls read within a budget.
+ *   k_pages,
+ *   v_pages    : [num_phys_pages][page_size][Hkv][D], elem_size 2 (FP16) or 1 (E4M3) bytes each
+ *   weights    : FP32 [num_phys_pages][Hkv][page_size]
+ *   page_table : int32 [B][max_pages]; kv_lens: int32 [B] on the device
+ *   dst_table  : int32 [B][dst_pages], the pages that receive what is kept: page_table itself
+ *                (in place; dst_pages == max_pages) or other pages
+ *   new_lens   : int32 [B] out, min(kv_lens[b], budget); not kv_lens itself
+ *   kept       : int32 [B][Hkv][budget] out, the old slots of the kept tokens, ascending; -1 past
+ *                new_lens[b]
+ *   A sequence of at most `budget` tokens keeps them all.  Of a longer one every KV head keeps, each
+ *   for itself, its first `sink` tokens, its last `recent` and the heaviest of those between, up to
+ *   budget in all; of equal weights the lower slot is kept, a NaN weighs less than any number.  The
+ *   kept rows of K and V and their weights go to slots 0 .. new_lens[b] - 1 of dst_table's pages in
+ *   their old order.  Everything else in the pool stays as it is.
+ *   In place, a page that is moved in must belong to one sequence only.  With other pages, no page
+ *   of dst_table may be read or written for another purpose by the same call (so shared pages can be
+ *   evicted from, into fresh ones).
+ *   D is 64, 128 or 256; page_size a power of two >= 16; num_phys_pages * page_size < 2^31;
+ *   sink + recent <= budget; max_kv_len <= max_pages * page_size;
+ *   min(budget, max_kv_len) <= dst_pages * page_size.  A sequence whose length is outside
+ *   [0, max_kv_len] (GBATTN_DEV_BAD_LENGTH) or with a page that it needs outside
+ *   [0, num_phys_pages) (GBATTN_DEV_BAD_PAGE) stays as it is: new_lens[b] = kv_lens[b], kept -1.
+ */
+int kv_paged_evict(void* k_pages, void* v_pages, float* weights, const int32_t* page_table,
+                   const int32_t* dst_table, const int32_t* kv_lens, int32_t* new_lens,
+                   int32_t* kept, int B, int Hkv, int D, int elem_size, int num_phys_pages,
+                   int page_size, int max_pages, int dst_pages, int max_kv_len, int budget, int sink,
+                   int recent, void* stream);
+
+/*
+ * Differential attention of new tokens over a paged FP16 KV cache.
+ * The pages have no counterpart: a differential head is the difference of two softmax maps over one
+ * set of values.  With q = [q1 | q2] and k = [k1 | k2] (halves of d = D / 2),
+ *     O = (softmax(scale q1 k1^T) - lambda_h softmax(scale q2 k2^T)) V,
+ *     lambda_h = exp(lq1 . lk1) - exp(lq2 . lk2) + lambda_init,
+ * and with a norm weight w the head's output is normalised over its width,
+ *     O <- O / sqrt(mean(O^2) + eps) * w * (1 - lambda_init).
+ *   lambda_vecs: FP32 [4][lambda_heads][d], the learned lq1, lk1, lq2, lk2; lambda_heads is 1
+ *                (shared) or Hq.  norm_weight: FP32 [D] or NULL (no normalisation; eps unused).
+ *   lse        : optional FP32 [B][Hq][2][nq], of the two maps
+ *   scale is typically 1/sqrt(d).  Everything else as attn_paged_decode_f16_fwd; D == 128.  A query
+ *   that sees nothing gets O = 0, lse = -inf.
+ */
+size_t attn_diff_paged_decode_f16_workspace_size(int B, int Hq, int Hkv, int nq, int max_kv_len,
+                                                 int D);
+int attn_diff_paged_decode_f16_fwd(const void* q, const void* k_pages, const void* v_pages,
+                                   const int32_t* page_table, const int32_t* kv_lens,
+                                   const float* lambda_vecs, int lambda_heads, float lambda_init,
+                                   const float* norm_weight, float eps, void* o, float* lse, int B,
+                                   int Hq, int Hkv, int nq, int D, int num_phys_pages, int page_size,
+                                   int max_pages, int max_kv_len, float scale, void* workspace,
+                                   size_t workspace_bytes, void* stream);
 
 /*
  * VSA key-cube selection.

@@ -16,6 +16,9 @@ Arithmetic is float64 unless the pages fix another precision:
                   (shared-KV heads, prefix offset) and block-sparse variants.
 * ``decode``    – new query tokens attending to a paged E4M3 KV cache through
                   the bridge's FP16 values (causal among the new tokens).
+* ``paged``     – the FP16 page cache: append, decode with accumulated attention
+                  weights, eviction by them.
+* ``diff``      – differential attention (the difference of two softmax maps).
 * ``vsa``       – cube mean-pooling (FP32, as the pages fix), cube scores and
                   the top-k key-cube selection.
 
@@ -29,4 +32,4 @@ forms, invariants, library routines and brute force; no function here is
 "parity unpinned".
 """
 
-from . import fp16, e4m3, attention, decode, vsa  # noqa: F401
+from . import fp16, e4m3, attention, decode, diff, paged, vsa  # noqa: F401
