@@ -52,6 +52,9 @@ _SIGNATURES = {
     "attn_diff_paged_decode_f16_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
     "attn_diff_paged_decode_f16_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _f, _vp, _f, _vp, _vp,
                                             _i, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]),
+    "attn_diff_prefill_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
+    "attn_diff_prefill_fwd": (_i, [_vp, _vp, _vp, _vp, _i, _f, _vp, _f, _vp, _vp, _vp, _vp, _i, _i,
+                                   _i, _i, _i, _i, _vp, _vp, _vp, _f, _i, _vp, _sz, _vp]),
     "vsa_select_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "vsa_select_blocks": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "vsa_sparse_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
@@ -576,6 +579,51 @@ def attn_diff_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, lam
         nq, D, P, ps, max_pages, max_kv_len, _scale(scale, D // 2), _ptr(workspace),
         workspace.numel() * workspace.element_size(), _stream(stream))
     _check("attn_diff_paged_decode_f16_fwd", rc)
+    return o
+
+
+def attn_diff_prefill_workspace_size(B, Hq, Sq, Skv, D):
+    return int(load().attn_diff_prefill_workspace_size(B, Hq, Sq, Skv, D))
+
+
+def attn_diff_prefill_fwd(q, k, v, lambda_vecs, lambda_init, norm_weight=None, eps=1e-5,
+                          causal=True, q_lens=None, kv_lens=None, o=None, lse=None, scale=None,
+                          workspace=None, stream=None):
+    """Differential attention of prompts: q [B,Hq,Sq,128], k/v [B,Hkv,Skv,128] FP16, q and k two
+    halves of 64, one per softmax map.  Strided views with a contiguous last dimension as for
+    attn_dense_fwd.  lambda_vecs FP32 [4,Hq or 1,64] (lq1, lk1, lq2, lk2); norm_weight FP32 [128]
+    or None; q_lens, kv_lens int32 [B] (device) or None: padded batches; lse FP32 [B,Hq,2,Sq].
+    scale defaults to 1/sqrt(64)."""
+    import torch
+    for t, n in ((q, "q"), (k, "k"), (v, "v")):
+        _need_view(t, n, torch.float16)
+    B, Hq, Sq, D = q.shape
+    Hkv, Skv = k.shape[1], k.shape[2]
+    if tuple(v.shape) != tuple(k.shape) or k.shape[0] != B or k.shape[3] != D:
+        raise ValueError("k and v must be [B, Hkv, Skv, D] matching q")
+    if k.stride() != v.stride():
+        raise ValueError("k and v must have the same strides")
+    heads = _need_diff(lambda_vecs, norm_weight, Hq, D)
+    for t, n in ((q_lens, "q_lens"), (kv_lens, "kv_lens")):
+        if t is not None:
+            _need(t, n, torch.int32, 1)
+            _need_shape(t, n, (B,))
+    o = _new_tensor((B, Hq, Sq, D), torch.float16, q.device, stream) if o is None else o
+    _need_view(o, "o", torch.float16)
+    _need_shape(o, "o", (B, Hq, Sq, D))
+    if lse is not None:
+        _need(lse, "lse", torch.float32)
+        _need_shape(lse, "lse", (B, Hq, 2, Sq))
+    if workspace is None:
+        workspace = _scratch(attn_diff_prefill_workspace_size(B, Hq, Sq, Skv, D), q.device, stream)
+    _same_device(q=q, k=k, v=v, lambda_vecs=lambda_vecs, norm_weight=norm_weight, q_lens=q_lens,
+                 kv_lens=kv_lens, o=o, lse=lse, workspace=workspace)
+    rc = load().attn_diff_prefill_fwd(
+        _ptr(q), _ptr(k), _ptr(v), _ptr(lambda_vecs), heads, float(lambda_init), _ptr(norm_weight),
+        float(eps), _ptr(q_lens), _ptr(kv_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, Skv, D,
+        _strides(q), _strides(k), _strides(o), _scale(scale, D // 2), 1 if causal else 0,
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+    _check("attn_diff_prefill_fwd", rc)
     return o
 
 

@@ -390,6 +390,32 @@ int attn_diff_paged_decode_f16_fwd(const void* q, const void* k_pages, const voi
                                    size_t workspace_bytes, void* stream);
 
 /*
+ * Differential attention of prompts.
+ * The mathematics, lambda_vecs, norm_weight and eps are attn_diff_paged_decode_f16_fwd's.
+ *   q, o : [B][Hq][Sq][D] FP16   k, v : [B][Hkv][Skv][D] FP16 (k and v share kv_strides)
+ *   q_strides, kv_strides, o_strides: {batch, head, row} element strides or NULL (dense)
+ *   q_lens, kv_lens : int32 [B] on the device, or NULL: Sq, Skv.  Only the first kv_lens[b] keys
+ *          exist (what lies behind them may be anything); query i < q_lens[b] sits at position
+ *          kv_lens[b] - q_lens[b] + i and sees the keys up to it (causal = 1) or all of them
+ *          (causal = 0).  Rows that see nothing, and rows i >= q_lens[b], get O = 0, lse = -inf.
+ *   lse  : optional dense [B][Hq][2][Sq] FP32, of the two maps
+ *   scale: finite, > 0 (typically 1/sqrt(D/2))
+ *   Query head h reads KV head h / (Hq / Hkv).  D == 128; B*Hq <= 65535; Sq <= 2^22, Skv <= 2^30.
+ *   A length outside [0, Sq] or [0, Skv] sets GBATTN_DEV_BAD_LENGTH and leaves that batch entry
+ *   without queries (O = 0, lse = -inf).
+ *   With few query rows the keys are split into chunks whose FP32 partial results go to `workspace`
+ *   (32-byte aligned) and are merged; a workspace smaller than attn_diff_prefill_workspace_size()
+ *   makes the call use fewer chunks, NULL with 0 bytes one.
+ */
+size_t attn_diff_prefill_workspace_size(int B, int Hq, int Sq, int Skv, int D);
+int attn_diff_prefill_fwd(const void* q, const void* k, const void* v, const float* lambda_vecs,
+                          int lambda_heads, float lambda_init, const float* norm_weight, float eps,
+                          const int32_t* q_lens, const int32_t* kv_lens, void* o, float* lse, int B,
+                          int Hq, int Hkv, int Sq, int Skv, int D, const int64_t* q_strides,
+                          const int64_t* kv_strides, const int64_t* o_strides, float scale,
+                          int causal, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * VSA key-cube selection.
  * Cites: "Integrate H3 SM70 execution, metrics and VSA diagnostics", Purpose
  * (top-k = 64); FastVideo compare view, minimax_h3_fusions/query_pool.py and

@@ -148,3 +148,37 @@ def test_evict_refusals(lib):
     assert call(vp=A(0)) == ALIAS and call(new=A(5)) == ALIAS and call(kept=A(6)) == ALIAS
     assert call(w=A(0)) == ALIAS and call(kept=A(3)) == ALIAS
     assert call(elem=1) in (OK, CUDA) and call() in (OK, CUDA)
+
+
+def test_diff_prefill_refusals(lib):
+    names = ("q", "k", "v", "vecs", "heads", "init", "norm", "eps", "ql", "kl", "o", "lse", "B",
+             "Hq", "Hkv", "Sq", "Skv", "D", "qs", "ks", "os", "scale", "causal", "ws", "wsb",
+             "stream")
+    base = dict(zip(names, (A(0), A(1), A(2), A(3), 4, 0.5, A(4), 1e-5, A(5), A(6), A(7), A(8), 2, 4,
+                            2, 100, 200, 128, None, None, None, 0.125, 1, None, 0, None)))
+    call = caller(lib.attn_diff_prefill_fwd, names, base)
+    for n in ("q", "k", "v", "vecs", "o"):
+        assert call(**{n: None}) == NULL
+    for n in ("B", "Hq", "Hkv", "Sq", "Skv"):
+        assert call(**{n: 0}) == SHAPE and call(**{n: -1}) == SHAPE
+    assert call(Hq=5) == SHAPE and call(heads=3) == SHAPE and call(causal=2) == SHAPE
+    assert call(B=65536) == SHAPE and call(Sq=(1 << 22) + 1) == SHAPE
+    assert call(Skv=(1 << 30) + 1) == SHAPE
+    for d in (64, 256, 0):
+        assert call(D=d) == UNSUPPORTED
+    st = (ctypes.c_int64 * 3)(1, 2, 3)
+    assert call(qs=st) == SHAPE and call(ks=st) == SHAPE and call(os=st) == SHAPE
+    assert call(os=(ctypes.c_int64 * 3)(0, 128, 128)) == SHAPE          # output heads overlap
+    for s in (0.0, float("nan"), float("inf")):
+        assert call(scale=s) == SCALE and call(eps=s) == SCALE
+    assert call(init=float("nan")) == SCALE
+    for n in ("q", "k", "v", "o", "ws"):
+        assert call(**{n: MIS8}) == ALIGN
+    for n in ("vecs", "norm", "ql", "kl", "lse"):
+        assert call(**{n: MIS2}) == ALIGN
+    assert call(o=A(1)) == ALIAS and call(lse=A(4)) == ALIAS and call(lse=A(7)) == ALIAS
+    n = lib.attn_diff_prefill_workspace_size(2, 4, 100, 20000, 128)
+    assert n > 0 and call(Skv=20000, ws=A(0), wsb=n) == ALIAS           # a workspace that is used
+    assert call(ql=None, kl=None, lse=None, norm=None, eps=0.0) in (OK, CUDA)
+    assert call() in (OK, CUDA)
+    assert lib.attn_diff_prefill_workspace_size(1, 16, 8192, 8192, 128) == 0     # enough rows

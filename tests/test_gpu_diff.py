@@ -48,6 +48,135 @@ def assert_diff(o, lse, ref, norm, lambda_init, p_step, eps=1e-5):
         assert np.all(np.abs(np.where(empty, 0.0, got) - want) <= bound)
 
 
+# ---------------------------------------------------------------- prompts
+
+def prompt(B, Hq, Hkv, Sq, Skv, seed, std=1.0):
+    q = inputs._normal_fp16(np.random.default_rng([seed, 1]), (B, Hq, Sq, D), std)
+    k = inputs._normal_fp16(np.random.default_rng([seed, 2]), (B, Hkv, Skv, D))
+    v = inputs._normal_fp16(np.random.default_rng([seed, 3]), (B, Hkv, Skv, D))
+    return q, k, v
+
+
+def check_prompt(gb, q, k, v, norm=True, lambda_init=0.55, seed=61, heads=None, workspace=None, **kw):
+    B, Hq, Sq, _ = q.shape
+    vecs, weight = inputs.diff_inputs(Hq, D, seed, heads=heads, norm=norm)
+    lse = torch.full((B, Hq, 2, Sq), 7.0, device=DEV)
+    lens = {n: None if kw.get(n) is None else t(np.asarray(kw[n], dtype=np.int32))
+            for n in ("q_lens", "kv_lens")}
+    o = gb.attn_diff_prefill_fwd(t(q), t(k), t(v), t(vecs), lambda_init, norm_weight=t(weight),
+                                 causal=kw.get("causal", True), lse=lse, workspace=workspace, **lens)
+    assert gb.device_status() == 0
+    ref = OD.prefill(q, k, v, vecs, lambda_init, 0.125, weight, causal=kw.get("causal", True),
+                     q_lens=kw.get("q_lens"), kv_lens=kw.get("kv_lens"))
+    # P enters the PV product as one FP16 value: half a step, 2^-11 / 2, of each
+    assert_diff(o, lse, ref, weight, lambda_init, 2.0 ** -11)
+    return o
+
+
+@pytest.mark.parametrize("Sq,Skv", [(1, 1), (1, 129), (2, 300), (64, 64), (127, 127), (128, 128),
+                                    (129, 129), (130, 515), (257, 1000), (500, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_diff_prompt_lengths(gb, Sq, Skv, causal):
+    """One row and one key, tile edges, a prefix, and more queries than keys (rows that see none)."""
+    check_prompt(gb, *prompt(1, 2, 1, Sq, Skv, 62), causal=causal)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (6, 2), (5, 5), (8, 1)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_diff_prompt_heads(gb, Hq, Hkv, norm):
+    check_prompt(gb, *prompt(2, Hq, Hkv, 200, 333, 63), norm=norm, heads=1 if Hq == 5 else None)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+def test_diff_prompt_padded_batch(gb, causal):
+    """Ragged lengths, empty entries, and NaN in every padded row of q, k and v."""
+    q, k, v = prompt(6, 2, 1, 260, 400, 64)
+    q_lens, kv_lens = [260, 100, 0, 1, 40, 200], [400, 130, 57, 0, 17, 200]
+    for b in range(6):
+        q[b, :, q_lens[b]:] = np.nan
+        k[b, :, kv_lens[b]:] = np.nan
+        v[b, :, kv_lens[b]:] = np.inf
+    check_prompt(gb, q, k, v, q_lens=q_lens, kv_lens=kv_lens, causal=causal)
+
+
+def test_diff_prompt_split_keys(gb):
+    """Few rows against many keys: with the full workspace, with less, and with none."""
+    case = prompt(1, 2, 1, 70, 5000, 65, std=2.0)
+    n = gb.attn_diff_prefill_workspace_size(1, 2, 70, 5000, D)
+    assert n > 0
+    for size in (n, n // 2, 16):
+        ws = torch.full((size,), 0xFF, dtype=torch.uint8, device=DEV)
+        check_prompt(gb, *case, workspace=ws)
+    check_prompt(gb, *prompt(3, 2, 2, 140, 3000, 66), q_lens=[140, 3, 139], kv_lens=[3000, 900, 0])
+
+
+def test_diff_prompt_peaked_and_flat_scores(gb):
+    for std in (0.02, 6.0):
+        check_prompt(gb, *prompt(1, 2, 2, 300, 300, 67, std=std))
+
+
+def test_diff_prompt_growing_scores_rescale(gb):
+    """Keys whose scores climb from tile to tile: the running max moves in both maps."""
+    q, k, v = prompt(1, 1, 1, 128, 1024, 68)
+    q[:] = np.abs(q)
+    k *= np.linspace(0.0, 3.0, 1024)[None, None, :, None].astype(np.float16)
+    k[..., :64] = np.abs(k[..., :64])
+    check_prompt(gb, q, k, v, causal=False)
+
+
+def test_diff_prompt_strided_views(gb):
+    """Token-major q and o, k and v as slices of one packed tensor."""
+    q, k, v = prompt(2, 4, 2, 150, 150, 69)
+    want = check_prompt(gb, q, k, v)
+    tq = t(q).permute(0, 2, 1, 3).contiguous().permute(0, 2, 1, 3)
+    packed = torch.zeros((2, 150, 2, 2, D), dtype=torch.float16, device=DEV)
+    packed[:, :, 0], packed[:, :, 1] = t(k).permute(0, 2, 1, 3), t(v).permute(0, 2, 1, 3)
+    tk, tv = (packed[:, :, i].permute(0, 2, 1, 3) for i in range(2))
+    o = torch.zeros((2, 150, 4, D), dtype=torch.float16, device=DEV).permute(0, 2, 1, 3)
+    vecs, weight = inputs.diff_inputs(4, D, 61)
+    gb.attn_diff_prefill_fwd(tq, tk, tv, t(vecs), 0.55, norm_weight=t(weight), o=o)
+    assert torch.equal(o, want)
+
+
+def test_diff_prompt_bad_length_and_lost_load(gb):
+    q, k, v = prompt(2, 1, 1, 100, 100, 70)
+    vecs, _ = inputs.diff_inputs(1, D, 61)
+    bad = t(np.array([100, 101], dtype=np.int32))
+    o = gb.attn_diff_prefill_fwd(t(q), t(k), t(v), t(vecs), 0.5, kv_lens=bad)
+    assert gb.device_status() == gb.DEV_BAD_LENGTH
+    assert torch.all(o[1] == 0) and torch.any(o[0] != 0)
+    gb.set_wait_limit_ns(20_000_000)
+    try:
+        for mode in (1, 2):
+            gb.test_inject_fault(mode)
+            # one chunk (no workspace to split into): mode 2 stops after 8 of its 32 K/V tiles
+            gb.attn_diff_prefill_fwd(*(t(x) for x in prompt(1, 1, 1, 128, 2048, 71)), t(vecs), 0.5,
+                                     workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
+            assert gb.device_status() & gb.DEV_WAIT_TIMEOUT
+    finally:
+        gb.test_inject_fault(0)
+        gb.set_wait_limit_ns(1_000_000_000)
+    check_prompt(gb, q, k, v)
+
+
+def test_diff_prompt_then_decode_agree(gb):
+    """The last prompt row equals one decode step over the same keys in pages."""
+    B, Hq, Hkv, S, ps = 2, 4, 2, 290, 32
+    q, k, v = prompt(B, Hq, Hkv, S, S, 72)
+    vecs, weight = inputs.diff_inputs(Hq, D, 73)
+    o = gb.attn_diff_prefill_fwd(t(q), t(k), t(v), t(vecs), 0.4, norm_weight=t(weight))
+    P = B * 10
+    kp, vp = torch.zeros((2, P, ps, Hkv, D), dtype=torch.float16, device=DEV)
+    table = torch.randperm(P, device=DEV).to(torch.int32).reshape(B, 10).contiguous()
+    lens = t(np.full(B, S, dtype=np.int32))
+    gb.kv_paged_append_f16(t(k), t(v), kp, vp, table, lens)
+    d = gb.attn_diff_paged_decode_f16_fwd(t(q[:, :, -1:]), kp, vp, table, lens, t(vecs), 0.4,
+                                          norm_weight=t(weight))
+    ref = OD.prefill(q[:, :, -1:], k, v, vecs, 0.4, 0.125, weight)
+    assert_diff(o[:, :, -1:], None, ref, weight, 0.4, 2.0 ** -11)
+    assert_diff(d, None, ref, weight, 0.4, 2.0 ** -22)
+
+
 # ---------------------------------------------------------------- decode
 
 @pytest.mark.parametrize("Hq,Hkv,nq", [(1, 1, 1), (4, 1, 1), (8, 2, 1), (5, 1, 1), (6, 2, 3),
