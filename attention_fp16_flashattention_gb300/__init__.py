@@ -106,16 +106,24 @@ def _check(fn, rc):
 
 
 def _stream(stream):
+    """The CUDA stream handle of `stream`, or of the current device's current stream."""
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # torch.cuda.current_stream().cuda_stream without building a Stream object (3 us a call)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, name, dtype, ndim=None):
+    try:   # the usual case in one line: a call's argument checks cost as much as its launch
+        if t.is_cuda and t.dtype is dtype and t.is_contiguous() and ndim in (None, t.dim()):
+            return
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -129,6 +137,11 @@ def _need(t, name, dtype, ndim=None):
 
 def _need_view(t, name, dtype):
     """A [B, H, S, D] CUDA view whose last dimension is contiguous (any other strides)."""
+    try:
+        if t.is_cuda and t.dtype is dtype and t.dim() == 4 and t.stride(3) == 1:
+            return
+    except AttributeError:
+        pass
     import torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -368,17 +381,17 @@ def attn_paged_decode_fwd(q, k_pages, v_pages, page_table, kv_lens, k_scale, v_s
 
 
 def _need_shape(t, name, shape):
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
 
 
-def _same_device(**tensors):
+def _same_device(*tensors):
     """Every tensor given on the current device: the call's stream and kernels run there."""
     import torch
     dev = torch.cuda.current_device()
-    for name, t in tensors.items():
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
 def _new_tensor(shape, dtype, device, stream):
@@ -432,8 +445,7 @@ def kv_paged_append_f16(k_new, v_new, k_pages, v_pages, page_table, kv_lens, new
     if weights is not None:
         _need(weights, "weights", torch.float32, 3)
         _need_shape(weights, "weights", (P, Hkv, ps))
-    _same_device(k_new=k_new, v_new=v_new, k_pages=k_pages, v_pages=v_pages,
-                 page_table=page_table, kv_lens=kv_lens, new_lens=new_lens, weights=weights)
+    _same_device(k_new, v_new, k_pages, v_pages, page_table, kv_lens, new_lens, weights)
     rc = load().kv_paged_append_f16(_ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages),
                                     _ptr(page_table), _ptr(kv_lens), _ptr(new_lens), _ptr(weights),
                                     B, Hkv, n, D, _strides(k_new), P, ps, max_pages,
@@ -472,8 +484,7 @@ def attn_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, max_kv_l
         workspace = _scratch(attn_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len, D,
                                                                   weights is not None),
                              q.device, stream)
-    _same_device(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_lens=kv_lens,
-                 o=o, lse=lse, weights=weights, workspace=workspace)
+    _same_device(q, k_pages, v_pages, page_table, kv_lens, o, lse, weights, workspace)
     rc = load().attn_paged_decode_f16_fwd(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
                                           _ptr(kv_lens), _ptr(o), _ptr(lse), _ptr(weights), B, Hq,
                                           Hkv, nq, D, P, ps, max_pages, max_kv_len,
@@ -520,8 +531,7 @@ def kv_paged_evict(k_pages, v_pages, weights, page_table, kv_lens, budget, sink=
     _need_shape(new_lens, "new_lens", (B,))
     _need(kept, "kept", torch.int32, 3)
     _need_shape(kept, "kept", (B, Hkv, budget))
-    _same_device(k_pages=k_pages, v_pages=v_pages, weights=weights, page_table=page_table,
-                 kv_lens=kv_lens, dst_table=dst, new_lens=new_lens, kept=kept)
+    _same_device(k_pages, v_pages, weights, page_table, kv_lens, dst, new_lens, kept)
     rc = load().kv_paged_evict(_ptr(k_pages), _ptr(v_pages), _ptr(weights), _ptr(page_table),
                                _ptr(dst), _ptr(kv_lens), _ptr(new_lens), _ptr(kept), B, Hkv, D,
                                k_pages.element_size(), P, ps, max_pages, dst.shape[1], max_kv_len,
@@ -570,9 +580,8 @@ def attn_diff_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, lam
     if workspace is None:
         workspace = _scratch(attn_diff_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len,
                                                                        D), q.device, stream)
-    _same_device(q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, kv_lens=kv_lens,
-                 lambda_vecs=lambda_vecs, norm_weight=norm_weight, o=o, lse=lse,
-                 workspace=workspace)
+    _same_device(q, k_pages, v_pages, page_table, kv_lens, lambda_vecs, norm_weight, o, lse,
+                 workspace)
     rc = load().attn_diff_paged_decode_f16_fwd(
         _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(kv_lens), _ptr(lambda_vecs),
         heads, float(lambda_init), _ptr(norm_weight), float(eps), _ptr(o), _ptr(lse), B, Hq, Hkv,
@@ -616,8 +625,7 @@ def attn_diff_prefill_fwd(q, k, v, lambda_vecs, lambda_init, norm_weight=None, e
         _need_shape(lse, "lse", (B, Hq, 2, Sq))
     if workspace is None:
         workspace = _scratch(attn_diff_prefill_workspace_size(B, Hq, Sq, Skv, D), q.device, stream)
-    _same_device(q=q, k=k, v=v, lambda_vecs=lambda_vecs, norm_weight=norm_weight, q_lens=q_lens,
-                 kv_lens=kv_lens, o=o, lse=lse, workspace=workspace)
+    _same_device(q, k, v, lambda_vecs, norm_weight, q_lens, kv_lens, o, lse, workspace)
     rc = load().attn_diff_prefill_fwd(
         _ptr(q), _ptr(k), _ptr(v), _ptr(lambda_vecs), heads, float(lambda_init), _ptr(norm_weight),
         float(eps), _ptr(q_lens), _ptr(kv_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, Skv, D,
