@@ -13,8 +13,11 @@
 // What bounds it: the cache's bytes, 4 D per token and KV head read once, against
 // 4 D FLOPs per row.  So the split is the E4M3 decode's (tiles.cuh): every warp of
 // a persistent grid takes an equal contiguous range of 16-token tiles whatever the
-// lengths, runs its own TMA ring (about 192 KB in flight per SM), and writes the
-// partial (max, sum, O) of each stream its range meets; a merge kernel joins them.
+// lengths and runs its own TMA ring (about 192 KB in flight per SM).  The partial
+// (max, sum, O) of a stream that ends inside a warp's range goes to memory; those
+// that the ranges' ends cut are first joined over the CTA's warps in shared memory
+// (consecutive warps mostly work on one stream), so a stream leaves one record per
+// CTA it meets and not one per warp.  A merge kernel joins the records.
 //   * S^T = K Q^T and O^T += V^T P^T on mma.sync m16n8k16: tokens (QK) and head
 //     width (PV) fill M, the query rows N (8, or 16 where a group has more).  K and
 //     V fragments come from the swizzled stage by ldmatrix (V transposed).
@@ -62,8 +65,12 @@ struct DecodeF16Args {
     const __half* q;
     const int32_t* table;
     const int32_t* kv_lens;
-    float* part_o;        // [record][R][D], unnormalised (R = 8 NB rows)
-    float2* part_ml;      // [record][R]: (max in log2 units, sum)
+    // Records of R = 8 NB rows: O [R][D] unnormalised and (max in log2 units, sum) [R].
+    // Record (CTA + stream) holds what the ends of the CTA's warp ranges cut of the
+    // stream; record (tail0 + stream) what a warp finished inside its range.
+    float* part_o;
+    float2* part_ml;
+    long long tail0;
     uint32_t* prefix_out; // [B + 1]: tiles of all streams of the sequences before b
     float* scores;        // [tile][pitch][16] log2-unit scores, or null
     uint32_t* status;
@@ -81,6 +88,32 @@ __device__ __forceinline__ uint32_t seq_tiles(int len, int max_kv) {
     return (len >= 0 && len <= max_kv) ? static_cast<uint32_t>((len + kTile - 1) / kTile) : 0u;
 }
 
+// How many CTAs of a grid work on U tiles, and how many warps of each: all of them
+// when every warp gets a tile, else as many warps per CTA as every CTA can feed.
+struct Split {
+    uint32_t ctas, warps;   // warps per CTA
+};
+__device__ __forceinline__ Split split_of(uint32_t U, uint32_t grid, uint32_t cta_warps) {
+    const uint32_t per = U / grid;
+    return Split{min(grid, U), per >= cta_warps ? cta_warps : max(per, 1u)};
+}
+
+// The row sums of a lane's two query columns over the eight lanes that share them.
+__device__ __forceinline__ void quad_sum(const float (&l)[2], float (&out)[2]) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        out[e] = l[e];
+#pragma unroll
+        for (int sh = 4; sh < 32; sh <<= 1) out[e] += __shfl_xor_sync(0xffffffffu, out[e], sh);
+    }
+}
+
+// The factor of a partial (max, sum) under the joint max M.  A row that saw nothing
+// has max -inf, sum 0 and factor 0; one whose scores are all NaN keeps its NaN.
+__device__ __forceinline__ float record_weight(float2 ml, float M) {
+    return ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - M);
+}
+
 template <int D, int NB>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     decode_f16_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
@@ -89,6 +122,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     constexpr int R = 8 * NB;
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t warp_sums[C::kWarps];
+    __shared__ float2 s_ml[C::kWarps][R];      // each warp's last segment: row max and sum
+    __shared__ long long s_stream[C::kWarps];  // its stream, -1 for an idle warp
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing);
@@ -136,10 +171,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // The merge grid may start launching now; it waits for this grid to finish.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t U = prefix[a.B];
-    const uint32_t W = gridDim.x * C::kWarps;
-    const uint32_t w = blockIdx.x * C::kWarps + warp;
-    const uint32_t u_beg = warp_start(w, W, U), u_end = warp_start(w + 1, W, U);
-    if (u_beg >= u_end) return;
+    const Split sp = split_of(U, gridDim.x, C::kWarps);
+    if (blockIdx.x >= sp.ctas) return;
+    // every warp below sp.warps has at least one tile; the others wait at the end
+    const uint32_t W = sp.ctas * sp.warps;
+    const uint32_t w = blockIdx.x * sp.warps + min(static_cast<uint32_t>(warp), sp.warps - 1);
+    const bool idle = static_cast<uint32_t>(warp) >= sp.warps;
+    const uint32_t u_beg = warp_start(w, W, U), u_end = idle ? u_beg : warp_start(w + 1, W, U);
 
     const WaitCtl wc{a.wait_limit, a.status, abort_flag};
     uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
@@ -196,12 +234,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     uint32_t qf[NB][C::kSteps][2];
     TileLoc L = locate(u_beg, prefix, a.B, per_seq);
     int kv_len = 0, lim[NB][2], first_masked = 0;
-    long long rec_id = 0;
     // Start of a stream segment: state reset and the Q operand of the stream's rows.
     auto begin_stream = [&]() {
         kv_len = a.kv_lens[L.b];
         const int hk = L.sis / a.row_groups, rg = L.sis - hk * a.row_groups;
-        rec_id = static_cast<long long>(w) + static_cast<long long>(L.b) * per_seq + L.sis;
         first_masked = kv_len - a.nq + 1;
 #pragma unroll
         for (int n = 0; n < NB; ++n) {
@@ -368,42 +404,30 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             pv(0xFFFFFFFFu, 0xFFFFFFFFu);
         }
 
-        // ---- end of a stream segment: write the partial record, move on
+        // ---- the stream ends inside the range: write its record, move on
         const uint32_t u = u_beg + k;
-        if (u + 1 == L.s_end || k + 1 == n_tiles) {
+        if (u + 1 == L.s_end && k + 1 < n_tiles) {
             const int rbase = (L.sis % a.row_groups) * R;   // query rows of padding are skipped
-            float* po = a.part_o + rec_id * R * D;
+            const long long rec = a.tail0 + static_cast<long long>(L.b) * per_seq + L.sis;
+            float* po = a.part_o + rec * R * D;
 #pragma unroll
             for (int n = 0; n < NB; ++n) {
-                float ls0 = l_sum[n][0], ls1 = l_sum[n][1];
+                float ls[2];
+                quad_sum(l_sum[n], ls);
 #pragma unroll
-                for (int sh = 4; sh < 32; sh <<= 1) {
-                    ls0 += __shfl_xor_sync(0xffffffffu, ls0, sh);
-                    ls1 += __shfl_xor_sync(0xffffffffu, ls1, sh);
-                }
-                const int r0 = 8 * n + 2 * c;
-                const bool real0 = rbase + r0 < a.G, real1 = rbase + r0 + 1 < a.G;
+                for (int e = 0; e < 2; ++e) {
+                    const int r = 8 * n + 2 * c + e;
+                    if (rbase + r >= a.G) continue;
 #pragma unroll
-                for (int j = 0; j < C::kSteps; ++j) {
-                    const int d = 16 * j + g;
-                    if (real0) {
-                        po[r0 * D + d] = o[n][j][0];
-                        po[r0 * D + d + 8] = o[n][j][2];
+                    for (int j = 0; j < C::kSteps; ++j) {
+                        po[r * D + 16 * j + g] = o[n][j][e];
+                        po[r * D + 16 * j + g + 8] = o[n][j][e + 2];
                     }
-                    if (real1) {
-                        po[(r0 + 1) * D + d] = o[n][j][1];
-                        po[(r0 + 1) * D + d + 8] = o[n][j][3];
-                    }
-                }
-                if (g == 0) {
-                    if (real0) a.part_ml[rec_id * R + r0] = make_float2(m_ref[n][0], ls0);
-                    if (real1) a.part_ml[rec_id * R + r0 + 1] = make_float2(m_ref[n][1], ls1);
+                    if (g == 0) a.part_ml[rec * R + r] = make_float2(m_ref[n][e], ls[e]);
                 }
             }
-            if (k + 1 < n_tiles) {
-                L = locate(u + 1, prefix, a.B, per_seq);
-                begin_stream();
-            }
+            L = locate(u + 1, prefix, a.B, per_seq);
+            begin_stream();
         } else {
             ++L.t;
         }
@@ -419,12 +443,62 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         __syncwarp();
     }
+
+    // ---- the ranges' last segments: joined over the warps that hold the same stream.
+    // A warp's ring is its own and empty by now; rows are padded by four floats, which
+    // spreads the fragments' rows over the banks.
+    constexpr int kPitch = D + 4;
+    static_assert(R * kPitch * 4 <= C::kStages * C::kStageBytes, "segment fits the warp's ring");
+    if (lane == 0)
+        s_stream[warp] = idle ? -1 : static_cast<long long>(L.b) * per_seq + L.sis;
+    if (!idle) {
+        float* so = reinterpret_cast<float*>(ring);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+            float ls[2];
+            quad_sum(l_sum[n], ls);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * n + 2 * c + e;
+#pragma unroll
+                for (int j = 0; j < C::kSteps; ++j) {
+                    so[r * kPitch + 16 * j + g] = o[n][j][e];
+                    so[r * kPitch + 16 * j + g + 8] = o[n][j][e + 2];
+                }
+                if (g == 0) s_ml[warp][r] = make_float2(m_ref[n][e], ls[e]);
+            }
+        }
+    }
+    __syncthreads();
+    constexpr int kRingFloats = C::kStages * C::kStageBytes / 4;
+    const float* all = reinterpret_cast<const float*>(smem);
+    for (uint32_t w0 = 0, w1; w0 < sp.warps; w0 = w1) {
+        const long long stream = s_stream[w0];
+        for (w1 = w0 + 1; w1 < sp.warps && s_stream[w1] == stream; ++w1) {}
+        const long long rec = static_cast<long long>(blockIdx.x) + stream;
+        const int real = min(R, a.G - static_cast<int>(stream % a.row_groups) * R);
+        for (int x = threadIdx.x; x < real * (D / 4); x += C::kThreads) {
+            const int r = x / (D / 4), d = 4 * (x % (D / 4));
+            float M = -INFINITY, l = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (uint32_t i = w0; i < w1; ++i) M = fmaxf(M, s_ml[i][r].x);
+            for (uint32_t i = w0; i < w1; ++i) {
+                const float2 ml = s_ml[i][r];
+                const float wt = record_weight(ml, M);
+                const float4 v = *reinterpret_cast<const float4*>(all + i * kRingFloats + r * kPitch + d);
+                acc = make_float4(acc.x + wt * v.x, acc.y + wt * v.y, acc.z + wt * v.z,
+                                  acc.w + wt * v.w);
+                l += wt * ml.y;
+            }
+            *reinterpret_cast<float4*>(a.part_o + (rec * R + r) * D + d) = acc;
+            if (d == 0) a.part_ml[rec * R + r] = make_float2(M, l);
+        }
+    }
 }
 
 // Joins the partial records of every query row: with m_r, l_r the max (log2
 // units) and sum of record r, M = max_r m_r, L = sum_r 2^(m_r - M) l_r,
-// O = sum_r 2^(m_r - M) O_r / L and lse = (M + log2 L) ln 2; the records of a row
-// are those of the warps whose tile ranges meet its stream.  One CTA takes one
+// O = sum_r 2^(m_r - M) O_r / L and lse = (M + log2 L) ln 2.  One CTA takes one
 // query of one head, its warps every blockDim/32-th record (kBatch in flight each,
 // a lane on D/32 columns); the differential form gives each map half the warps
 // and ends with diff.cuh's combination.  A row that sees nothing gets O = 0,
@@ -433,8 +507,9 @@ struct MergeArgs {
     const float* part_o;
     const float2* part_ml;
     const uint32_t* prefix;
+    long long tail0;
     int B, Hq, Hkv, nq, row_groups, R;
-    uint32_t W;
+    uint32_t grid, cta_warps;   // of the decode kernel
     __half* o;
     float* lse;       // [B][Hq][maps][nq] or null
     float2* row_ml;   // [B][Hkv][G]: (M, 1 / L) for the weights kernel, or null
@@ -470,34 +545,35 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t U = a.prefix[a.B];
     const uint32_t T = (a.prefix[b + 1] - a.prefix[b]) / per_seq;
-    uint32_t w0 = 1, w1 = 0;   // empty unless the sequence has tiles
-    long long s_index = 0;
+    // The stream's records: `cut` of CTAs c0 .. c0 + cut - 1, and the tail when the
+    // stream ends inside a warp's range.
+    uint32_t c0 = 0, cut = 0, tail = 0;
+    const long long stream = static_cast<long long>(b) * per_seq + hk * a.row_groups + rg;
     if (T > 0) {
-        const int sis = hk * a.row_groups + rg;
-        const uint32_t u0 = a.prefix[b] + sis * T;
-        w0 = warp_of(u0, a.W, U);
-        w1 = warp_of(u0 + T - 1, a.W, U);
-        s_index = static_cast<long long>(b) * per_seq + sis;
+        const Split sp = split_of(U, a.grid, a.cta_warps);
+        const uint32_t W = sp.ctas * sp.warps;
+        const uint32_t u0 = a.prefix[b] + (hk * a.row_groups + rg) * T;
+        const uint32_t wf = warp_of(u0, W, U), wl = warp_of(u0 + T - 1, W, U);
+        tail = warp_start(wl + 1, W, U) != u0 + T ? 1 : 0;
+        c0 = wf / sp.warps;
+        if (wl + 1 - tail > wf) cut = (wl - tail) / sp.warps - c0 + 1;
     }
-    // With at least as many tiles as warps every warp range is non-empty, and
-    // the per-record emptiness test (two 64-bit divisions) is skipped.
-    const bool all_busy = U >= a.W;
+    const uint32_t n_rec = cut + tail;
     const int lanes = warps / kMaps, wl = kDiff ? warp >> 1 : warp;
     float mx = -INFINITY, lw = 0.0f, acc[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) acc[e] = 0.0f;
-    for (uint32_t wb = w0 + wl; wb <= w1; wb += lanes * kBatch) {
+    for (uint32_t xb = wl; xb < n_rec; xb += lanes * kBatch) {
         float2 ml[kBatch];
         float v[kBatch][V];
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            const uint32_t w = wb + lanes * j;
+            const uint32_t x = xb + lanes * j;
             ml[j] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
             for (int e = 0; e < V; ++e) v[j][e] = 0.0f;
-            if (w <= w1 &&
-                (all_busy || warp_start(w, a.W, U) < warp_start(w + 1, a.W, U))) {
-                const long long rec = (w + s_index) * a.R + n;
+            if (x < n_rec) {
+                const long long rec = ((x < cut ? c0 + x : a.tail0) + stream) * a.R + n;
                 ml[j] = a.part_ml[rec];
                 const float* p = a.part_o + rec * D + lane * V;
                 if constexpr (V == 2) {
@@ -516,18 +592,17 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
                 }
             }
         }
+        float M = mx;
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) M = fmaxf(M, ml[j].x);
+        const float sc = mx == -INFINITY ? 1.0f : exp2f(mx - M);   // what the warp holds so far
+        lw *= sc;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] *= sc;
+        mx = M;
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
-            if (ml[j].x > mx) {   // a larger max: rescale what this warp holds
-                const float sc = mx == -INFINITY ? 0.0f : exp2f(mx - ml[j].x);
-#pragma unroll
-                for (int e = 0; e < V; ++e) acc[e] *= sc;
-                lw *= sc;
-                mx = ml[j].x;
-            }
-            // a record whose row saw nothing has max -inf and weight 0; a NaN sum stays NaN
-            const float wt = ml[j].x == -INFINITY ? (ml[j].y == 0.0f ? 0.0f : 1.0f)
-                                                  : exp2f(ml[j].x - mx);
+            const float wt = record_weight(ml[j], M);
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] += wt * v[j][e];
             lw += wt * ml[j].y;
@@ -549,7 +624,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
         for (int k = mp; k < warps; k += kMaps) M = fmaxf(M, s_ml[k].x);
         for (int k = mp; k < warps; k += kMaps) {
             const float2 ml = s_ml[k];
-            const float wt = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - M);
+            const float wt = record_weight(ml, M);
             Ls += wt * ml.y;
 #pragma unroll
             for (int e = 0; e < V; ++e) so[e] += wt * s_o[k][lane * V + e];
@@ -587,8 +662,9 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
 }
 
 // weights[slot] += sum over the group's rows of 2^(x - M) / L for every cached
-// token.  A half-warp takes a tile (one token a lane) and every row group's scores
-// of it; the sum runs in row order in one thread and reaches memory by one atomic
+// token.  A warp takes an equal contiguous share of the (sequence, KV head, tile)
+// triples, two tiles (one token a lane) at a time, with every row group's scores of
+// them; the sum runs in row order in one thread and reaches memory by one atomic
 // add per (token, KV head).
 struct WeightArgs {
     const float* scores;
@@ -601,39 +677,52 @@ struct WeightArgs {
 };
 
 __global__ void __launch_bounds__(256) decode_f16_weights_kernel(const WeightArgs a) {
+    const int lane = threadIdx.x & 31;
     // A programmatic dependent of the merge, which itself waited for the decode.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int per_seq = a.Hkv * a.row_groups;
     const uint32_t tiles = a.prefix[a.B] / a.row_groups;   // (sequence, KV head, tile) triples
-    const uint32_t step = gridDim.x * 16;
-    const int tok = threadIdx.x & 15;
-    for (uint32_t x = blockIdx.x * 16 + (threadIdx.x >> 4); x < tiles; x += step) {
-        int lo = 0, hi = a.B - 1;   // largest b whose first triple is <= x
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (a.prefix[mid] / a.row_groups <= x) lo = mid; else hi = mid - 1;
+    const uint32_t W = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
+    uint32_t x = warp_start(w, W, tiles);
+    const uint32_t x_end = warp_start(w + 1, W, tiles);
+    if (x >= x_end) return;
+    int b = 0;
+    for (int hi = a.B - 1; b < hi;) {   // largest b whose first triple is <= x
+        const int mid = (b + hi + 1) >> 1;
+        if (a.prefix[mid] / a.row_groups <= x) b = mid; else hi = mid - 1;
+    }
+    while (x < x_end) {
+        const uint32_t first = a.prefix[b], next = a.prefix[b + 1];
+        const uint32_t T = (next - first) / per_seq;
+        if (T == 0) {
+            ++b;
+            continue;
         }
-        const uint32_t first = a.prefix[lo];
-        const uint32_t T = (a.prefix[lo + 1] - first) / per_seq;
         const uint32_t off = x - first / a.row_groups;
         const int hk = static_cast<int>(off / T), t = static_cast<int>(off - hk * T);
-        const int token = t * kTile + tok;
-        if (token >= a.kv_lens[lo]) continue;
-        const float2* ml = a.row_ml + (static_cast<long long>(lo) * a.Hkv + hk) * a.G;
-        float sum = 0.0f;
-        for (int rg = 0; rg < a.row_groups; ++rg) {
-            const long long u = first + static_cast<long long>(hk * a.row_groups + rg) * T + t;
-            const float* sp = a.scores + u * a.pitch * kTile + tok;
-            const int real = min(a.R, a.G - rg * a.R);
-            for (int r = 0; r < real; ++r) {
-                const float s = sp[r * kTile];
-                const float2 m = ml[rg * a.R + r];
-                sum += s == -INFINITY ? 0.0f : fast_exp2(s - m.x) * m.y;
+        const uint32_t n = min(min(2u, T - t), x_end - x);   // tiles of this step
+        const int token = t * kTile + lane;
+        if (lane < static_cast<int>(n) * kTile && token < a.kv_lens[b]) {
+            const int page = a.table[static_cast<long long>(b) * a.max_pages + token / a.ps];
+            const float2* ml = a.row_ml + (static_cast<long long>(b) * a.Hkv + hk) * a.G;
+            float sum = 0.0f;
+            for (int rg = 0; rg < a.row_groups; ++rg) {
+                const long long u = first + static_cast<long long>(hk * a.row_groups + rg) * T + t;
+                const float* sp = a.scores + (u + (lane >> 4)) * a.pitch * kTile + (lane & 15);
+                const int real = min(a.R, a.G - rg * a.R);
+#pragma unroll 4
+                for (int r = 0; r < real; ++r) {
+                    const float s = sp[r * kTile];
+                    const float2 m = ml[rg * a.R + r];
+                    sum += s == -INFINITY ? 0.0f : fast_exp2(s - m.x) * m.y;
+                }
             }
+            if (page >= 0 && page < a.num_phys)   // else flagged by the decode kernel
+                atomicAdd(a.weights + (static_cast<long long>(page) * a.Hkv + hk) * a.ps + token % a.ps,
+                          sum);
         }
-        const int page = a.table[static_cast<long long>(lo) * a.max_pages + token / a.ps];
-        if (page < 0 || page >= a.num_phys) continue;   // flagged by the decode kernel
-        atomicAdd(a.weights + (static_cast<long long>(page) * a.Hkv + hk) * a.ps + token % a.ps, sum);
+        x += n;
+        if (hk == a.Hkv - 1 && t + static_cast<int>(n) == static_cast<int>(T)) ++b;
     }
 }
 
@@ -643,18 +732,19 @@ int warps_of(int D) { return D == 256 ? 4 : 8; }
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
-// Workspace: partial records for W warps plus one per stream boundary, the
-// (B + 1)-entry tile prefix and, for the weights, every row's (max, 1 / sum) and
-// the scores of every tile that max_kv_len allows.
+// Workspace: partial records, one per CTA and two per stream, the (B + 1)-entry
+// tile prefix and, for the weights, every row's (max, 1 / sum) and the scores of
+// every tile that max_kv_len allows.
 struct Layout {
-    size_t o, ml, prefix, row_ml, scores, total;
+    size_t tail0, o, ml, prefix, row_ml, scores, total;
 };
 
-Layout decode_layout(long long warps, int B, int Hkv, int G, int max_kv, int D, bool weights) {
+Layout decode_layout(long long ctas, int B, int Hkv, int G, int max_kv, int D, bool weights) {
     const int R = rows_per_group(G), rgs = (G + R - 1) / R;
     const size_t streams = static_cast<size_t>(B) * Hkv * rgs;
-    const size_t recs = static_cast<size_t>(warps) + streams;
+    const size_t recs = static_cast<size_t>(ctas) + 2 * streams;
     Layout l{};
+    l.tail0 = static_cast<size_t>(ctas) + streams;
     size_t at = 0;
     l.o = at;
     at += recs * R * D * 4;
@@ -680,8 +770,7 @@ size_t decode_workspace_size(int B, int Hq, int Hkv, int nq, int max_kv, int D, 
     if (B <= 0 || Hq <= 0 || Hkv <= 0 || nq <= 0 || max_kv <= 0 || D <= 0 || Hq % Hkv != 0) return 0;
     const long long G = static_cast<long long>(Hq / Hkv) * nq * maps;
     if (G > 0x7FFFFFFFLL) return 0;
-    return decode_layout(static_cast<long long>(sm_count_or_default()) * warps_of(D), B, Hkv,
-                         static_cast<int>(G), max_kv, D, weights).total;
+    return decode_layout(sm_count_or_default(), B, Hkv, static_cast<int>(G), max_kv, D, weights).total;
 }
 
 template <int D, int NB>
@@ -810,9 +899,8 @@ int run_decode(const DecodeCall& c) {
     if (rc != GBATTN_OK) return rc;
 
     // One CTA per SM; fewer when the workspace holds fewer records.
-    const int cta_warps = warps_of(c.D);
     auto layout = [&](long long ctas) {
-        return decode_layout(ctas * cta_warps, c.B, c.Hkv, G, c.max_kv, c.D, c.weights != nullptr);
+        return decode_layout(ctas, c.B, c.Hkv, G, c.max_kv, c.D, c.weights != nullptr);
     };
     long long ctas = dev.num_sms;
     while (ctas > 1 && layout(ctas).total > c.workspace_bytes) --ctas;
@@ -836,6 +924,7 @@ int run_decode(const DecodeCall& c) {
     a.kv_lens = c.kv_lens;
     a.part_o = reinterpret_cast<float*>(wsp + lay.o);
     a.part_ml = reinterpret_cast<float2*>(wsp + lay.ml);
+    a.tail0 = static_cast<long long>(lay.tail0);
     a.prefix_out = reinterpret_cast<uint32_t*>(wsp + lay.prefix);
     a.scores = c.weights ? reinterpret_cast<float*>(wsp + lay.scores) : nullptr;
     a.status = dev.status;
@@ -871,13 +960,16 @@ int run_decode(const DecodeCall& c) {
     m.nq = c.nq;
     m.row_groups = rgs;
     m.R = R;
-    m.W = static_cast<uint32_t>(ctas * cta_warps);
+    m.tail0 = a.tail0;
+    m.grid = static_cast<uint32_t>(ctas);
+    m.cta_warps = static_cast<uint32_t>(warps_of(c.D));
     m.o = static_cast<__half*>(c.o);
     m.lse = c.lse;
     m.row_ml = c.weights ? reinterpret_cast<float2*>(wsp + lay.row_ml) : nullptr;
     if (c.diff) m.diff = *c.diff;
-    const long long recs = m.W / streams + 2;   // records of an average row
-    const int mw = recs > 64 ? 16 : recs > 16 ? 8 : 4;
+    // Warps per row by the records of an average row (a map of a row): one up to a batch of 8.
+    const long long recs = ctas / streams + 1;
+    const int mw = (recs > 32 ? 8 : recs > 8 ? 4 : 1) * maps;
     const dim3 mgrid(static_cast<unsigned>(rows));
     rc = c.diff       ? launch_dependent(decode_f16_merge_kernel<128, true>, mgrid, 32 * mw, s, m)
          : c.D == 64  ? launch_dependent(decode_f16_merge_kernel<64, false>, mgrid, 32 * mw, s, m)
@@ -902,7 +994,7 @@ int run_decode(const DecodeCall& c) {
     x.ps = c.ps;
     x.max_pages = c.max_pages;
     const long long tiles = static_cast<long long>(c.B) * c.Hkv * ((c.max_kv + kTile - 1) / kTile);
-    const long long want = (tiles + 15) / 16;
+    const long long want = (tiles + 15) / 16;   // a warp takes two tiles or more
     const unsigned grid = static_cast<unsigned>(want < 8LL * dev.num_sms ? want : 8LL * dev.num_sms);
     return launch_dependent(decode_f16_weights_kernel, dim3(grid), 256, s, x);
 }
