@@ -73,6 +73,7 @@ struct DecodeF16Args {
     long long tail0;
     uint32_t* prefix_out; // [B + 1]: tiles of all streams of the sequences before b
     float* scores;        // [tile][pitch][16] log2-unit scores, or null
+    int4* tiles;          // with scores: what the weights kernel needs to know of each tile
     uint32_t* status;
     uint64_t wait_limit;
     int fault;   // test hook: 1 = no stage is loaded, 2 = loads stop after two ring rounds
@@ -194,11 +195,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         const TileLoc L = locate(u, prefix, a.B, per_seq);
         const int tok = L.t * kTile;
         int page = a.table[static_cast<long long>(L.b) * a.max_pages + tok / a.ps];
-        if (page < 0 || page >= a.num_phys) {
+        const bool bad = page < 0 || page >= a.num_phys;
+        if (bad) {
             atomicOr(a.status, kDevBadPage);
             page = 0;
         }
         const int hk = L.sis / a.row_groups;
+        if (a.scores) {
+            // (first slot, sequence and KV head, tiles of the stream, live tokens); none
+            // live on a bad page and for the row groups that group 0's tile stands for
+            const bool skip = bad || L.sis % a.row_groups != 0;
+            a.tiles[u] = make_int4(page * a.ps + tok % a.ps, L.b * a.Hkv + hk,
+                                   static_cast<int>((prefix[L.b + 1] - prefix[L.b]) / per_seq),
+                                   skip ? 0 : min(kTile, a.kv_lens[L.b] - tok));
+        }
         return (static_cast<long long>(hk) << 32) | static_cast<uint32_t>(page * a.ps + tok % a.ps);
     };
     auto issue = [&](uint32_t k, long long src) {   // stage k of this warp's range
@@ -662,67 +672,61 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
 }
 
 // weights[slot] += sum over the group's rows of 2^(x - M) / L for every cached
-// token.  A warp takes an equal contiguous share of the (sequence, KV head, tile)
-// triples, two tiles (one token a lane) at a time, with every row group's scores of
-// them; the sum runs in row order in one thread and reaches memory by one atomic
-// add per (token, KV head).
+// token.  A half-warp takes a tile (one token a lane) with every row group's scores of
+// it, kTiles tiles at once so that their loads overlap; what it has to know of a tile
+// the decode kernel left beside the scores.  The sum runs in row order in one thread and
+// reaches memory by one atomic add per (token, KV head).
 struct WeightArgs {
     const float* scores;
+    const int4* tiles;
     const float2* row_ml;
     const uint32_t* prefix;
-    const int32_t* table;
-    const int32_t* kv_lens;
     float* weights;   // [num_phys][Hkv][ps]
-    int B, Hkv, G, row_groups, R, pitch, num_phys, ps, max_pages;
+    int B, Hkv, G, row_groups, R, pitch, ps;
 };
 
 __global__ void __launch_bounds__(256) decode_f16_weights_kernel(const WeightArgs a) {
-    const int lane = threadIdx.x & 31;
+    constexpr int kTiles = 4;
     // A programmatic dependent of the merge, which itself waited for the decode.
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int per_seq = a.Hkv * a.row_groups;
-    const uint32_t tiles = a.prefix[a.B] / a.row_groups;   // (sequence, KV head, tile) triples
-    const uint32_t W = gridDim.x * 8, w = blockIdx.x * 8 + (threadIdx.x >> 5);
-    uint32_t x = warp_start(w, W, tiles);
-    const uint32_t x_end = warp_start(w + 1, W, tiles);
-    if (x >= x_end) return;
-    int b = 0;
-    for (int hi = a.B - 1; b < hi;) {   // largest b whose first triple is <= x
-        const int mid = (b + hi + 1) >> 1;
-        if (a.prefix[mid] / a.row_groups <= x) b = mid; else hi = mid - 1;
-    }
-    while (x < x_end) {
-        const uint32_t first = a.prefix[b], next = a.prefix[b + 1];
-        const uint32_t T = (next - first) / per_seq;
-        if (T == 0) {
-            ++b;
-            continue;
+    const uint32_t U = a.prefix[a.B];
+    const uint32_t step = gridDim.x * 16;
+    const int tok = threadIdx.x & 15;
+    for (uint32_t u0 = blockIdx.x * 16 + (threadIdx.x >> 4); u0 < U; u0 += kTiles * step) {
+        int4 info[kTiles];
+        float sum[kTiles];
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+            const uint32_t u = u0 + j * step;
+            info[j] = u < U ? a.tiles[u] : make_int4(0, 0, 0, 0);
+            sum[j] = 0.0f;
         }
-        const uint32_t off = x - first / a.row_groups;
-        const int hk = static_cast<int>(off / T), t = static_cast<int>(off - hk * T);
-        const uint32_t n = min(min(2u, T - t), x_end - x);   // tiles of this step
-        const int token = t * kTile + lane;
-        if (lane < static_cast<int>(n) * kTile && token < a.kv_lens[b]) {
-            const int page = a.table[static_cast<long long>(b) * a.max_pages + token / a.ps];
-            const float2* ml = a.row_ml + (static_cast<long long>(b) * a.Hkv + hk) * a.G;
-            float sum = 0.0f;
-            for (int rg = 0; rg < a.row_groups; ++rg) {
-                const long long u = first + static_cast<long long>(hk * a.row_groups + rg) * T + t;
-                const float* sp = a.scores + (u + (lane >> 4)) * a.pitch * kTile + (lane & 15);
-                const int real = min(a.R, a.G - rg * a.R);
-#pragma unroll 4
-                for (int r = 0; r < real; ++r) {
-                    const float s = sp[r * kTile];
-                    const float2 m = ml[rg * a.R + r];
-                    sum += s == -INFINITY ? 0.0f : fast_exp2(s - m.x) * m.y;
+        for (int rg = 0; rg < a.row_groups; ++rg) {
+            const int real = min(a.R, a.G - rg * a.R);
+#pragma unroll 2
+            for (int r = 0; r < real; ++r) {
+                float s[kTiles];
+                float2 m[kTiles];
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j) {
+                    s[j] = -INFINITY;
+                    if (tok >= info[j].w) continue;
+                    const long long u = u0 + j * step + static_cast<long long>(rg) * info[j].z;
+                    s[j] = a.scores[(u * a.pitch + r) * kTile + tok];
+                    m[j] = a.row_ml[static_cast<long long>(info[j].y) * a.G + rg * a.R + r];
                 }
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j)
+                    if (s[j] != -INFINITY) sum[j] += fast_exp2(s[j] - m[j].x) * m[j].y;
             }
-            if (page >= 0 && page < a.num_phys)   // else flagged by the decode kernel
-                atomicAdd(a.weights + (static_cast<long long>(page) * a.Hkv + hk) * a.ps + token % a.ps,
-                          sum);
         }
-        x += n;
-        if (hk == a.Hkv - 1 && t + static_cast<int>(n) == static_cast<int>(T)) ++b;
+#pragma unroll
+        for (int j = 0; j < kTiles; ++j) {
+            if (tok >= info[j].w) continue;
+            const long long page = info[j].x / a.ps;
+            const int hk = info[j].y % a.Hkv;
+            atomicAdd(a.weights + (page * a.Hkv + hk) * a.ps + info[j].x % a.ps + tok, sum[j]);
+        }
     }
 }
 
@@ -733,10 +737,10 @@ int warps_of(int D) { return D == 256 ? 4 : 8; }
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
 // Workspace: partial records, one per CTA and two per stream, the (B + 1)-entry
-// tile prefix and, for the weights, every row's (max, 1 / sum) and the scores of
-// every tile that max_kv_len allows.
+// tile prefix and, for the weights, every row's (max, 1 / sum) and the description
+// and scores of every tile that max_kv_len allows.
 struct Layout {
-    size_t tail0, o, ml, prefix, row_ml, scores, total;
+    size_t tail0, o, ml, prefix, row_ml, tiles, scores, total;
 };
 
 Layout decode_layout(long long ctas, int B, int Hkv, int G, int max_kv, int D, bool weights) {
@@ -754,8 +758,11 @@ Layout decode_layout(long long ctas, int B, int Hkv, int G, int max_kv, int D, b
     at += round16((static_cast<size_t>(B) + 1) * 4);
     l.row_ml = at;
     if (weights) at += round16(static_cast<size_t>(B) * Hkv * G * 8);
+    const size_t tiles = streams * ((static_cast<size_t>(max_kv) + kTile - 1) / kTile);
+    l.tiles = at;
+    if (weights) at += tiles * 16;
     l.scores = at;
-    if (weights) at += streams * ((max_kv + kTile - 1) / kTile) * (rgs > 1 ? R : G) * kTile * 4;
+    if (weights) at += tiles * (rgs > 1 ? R : G) * kTile * 4;
     l.total = at + 16;
     return l;
 }
@@ -927,6 +934,7 @@ int run_decode(const DecodeCall& c) {
     a.tail0 = static_cast<long long>(lay.tail0);
     a.prefix_out = reinterpret_cast<uint32_t*>(wsp + lay.prefix);
     a.scores = c.weights ? reinterpret_cast<float*>(wsp + lay.scores) : nullptr;
+    a.tiles = reinterpret_cast<int4*>(wsp + lay.tiles);
     a.status = dev.status;
     a.wait_limit = wait_limit_ns();
     a.fault = fault_mode();
@@ -979,10 +987,9 @@ int run_decode(const DecodeCall& c) {
 
     WeightArgs x{};
     x.scores = a.scores;
+    x.tiles = a.tiles;
     x.row_ml = m.row_ml;
     x.prefix = a.prefix_out;
-    x.table = c.page_table;
-    x.kv_lens = c.kv_lens;
     x.weights = c.weights;
     x.B = c.B;
     x.Hkv = c.Hkv;
@@ -990,11 +997,9 @@ int run_decode(const DecodeCall& c) {
     x.row_groups = rgs;
     x.R = R;
     x.pitch = a.pitch;
-    x.num_phys = c.num_phys;
     x.ps = c.ps;
-    x.max_pages = c.max_pages;
-    const long long tiles = static_cast<long long>(c.B) * c.Hkv * ((c.max_kv + kTile - 1) / kTile);
-    const long long want = (tiles + 15) / 16;   // a warp takes two tiles or more
+    const long long tiles = streams * ((c.max_kv + kTile - 1) / kTile);
+    const long long want = (tiles + 15) / 16;
     const unsigned grid = static_cast<unsigned>(want < 8LL * dev.num_sms ? want : 8LL * dev.num_sms);
     return launch_dependent(decode_f16_weights_kernel, dim3(grid), 256, s, x);
 }

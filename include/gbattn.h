@@ -321,7 +321,7 @@ int kv_paged_append_f16(const void* k_new, const void* v_new, void* k_pages, voi
  *   its tokens' weights stay as they are).
  *   The work is split over the warps of a persistent grid as in attn_paged_decode_fwd, and the
  *   workspace rules are the same: attn_paged_decode_f16_workspace_size() gives the full-speed size
- *   (weights != 0 adds one FP32 score per query row and cached token, for max_kv_len tokens of
+ *   (weights != 0 adds about one FP32 score per query row and cached token, for max_kv_len tokens of
  *   every sequence), a smaller one runs fewer warps, and below one CTA's worth the call returns
  *   GBATTN_ERR_WORKSPACE.
  */

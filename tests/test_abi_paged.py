@@ -118,8 +118,8 @@ def test_decode_workspace_sizes(lib):
     plain = lib.attn_paged_decode_f16_workspace_size
     assert plain(0, 4, 2, 1, 64, 128, 0) == 0 and plain(2, 5, 2, 1, 64, 128, 0) == 0
     base = plain(2, 4, 2, 1, 4096, 128, 0)
-    # with weights: a (max, 1 / sum) pair per row and a score per row and token
-    assert plain(2, 4, 2, 1, 4096, 128, 1) == base + 2 * 4 * 8 + 2 * 4 * 4096 * 4
+    # with weights: a (max, 1 / sum) pair per row, 16 bytes per tile, a score per row and token
+    assert plain(2, 4, 2, 1, 4096, 128, 1) == base + 2 * 4 * 8 + 2 * 2 * 256 * 16 + 2 * 4 * 4096 * 4
     assert lib.attn_diff_paged_decode_f16_workspace_size(2, 4, 2, 1, 4096, 128) == base
     assert plain(4096, 64, 8, 1, 1 << 20, 128, 1) > 1 << 40      # no 32-bit wrap
 
