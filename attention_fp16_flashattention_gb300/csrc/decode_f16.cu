@@ -133,6 +133,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int per_seq = a.Hkv * a.row_groups;
 
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tk);
+        tma_prefetch_desc(&tv);
+    }
     // ---- tile prefix over sequences (block-wide scan of per-sequence tile counts)
     {
         const int per = (a.B + C::kThreads) / C::kThreads;   // entries 0..B over the threads
@@ -181,12 +185,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t u_beg = warp_start(w, W, U), u_end = idle ? u_beg : warp_start(w + 1, W, U);
 
     const WaitCtl wc{a.wait_limit, a.status, abort_flag};
+    const uint64_t policy = l2_evict_first();   // the cache is read once; records and scores stay
     uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
     uint64_t* full = bars + warp * C::kStages;
-    if (lane == 0) {
-        tma_prefetch_desc(&tk);
-        tma_prefetch_desc(&tv);
-    }
 
     // First cache row ([page * ps + slot] space) of tile u and its KV head, packed
     // as (head, row) in 64 bits.
@@ -219,8 +220,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             mbar_arrive_expect_tx(&full[slot], C::kStageBytes);
 #pragma unroll
             for (int h = 0; h < C::kBoxes; ++h) {
-                tma_load_3d(dst + h * C::kBox, &tk, &full[slot], 64 * h, hk, row);
-                tma_load_3d(dst + (C::kBoxes + h) * C::kBox, &tv, &full[slot], 64 * h, hk, row);
+                tma_load_3d_hint(dst + h * C::kBox, &tk, &full[slot], 64 * h, hk, row, policy);
+                tma_load_3d_hint(dst + (C::kBoxes + h) * C::kBox, &tv, &full[slot], 64 * h, hk, row,
+                                 policy);
             }
         }
         __syncwarp();
@@ -553,6 +555,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
     // Launched as a programmatic dependent of the decode grid: wait for its
     // prefix table and records before reading them.
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t U = a.prefix[a.B];
     const uint32_t T = (a.prefix[b + 1] - a.prefix[b]) / per_seq;
     // The stream's records: `cut` of CTAs c0 .. c0 + cut - 1, and the tail when the
@@ -682,10 +685,10 @@ struct WeightArgs {
     const float2* row_ml;
     const uint32_t* prefix;
     float* weights;   // [num_phys][Hkv][ps]
-    int B, Hkv, G, row_groups, R, pitch, ps;
+    int B, Hkv, G, row_groups, R, pitch, page_bits;
 };
 
-__global__ void __launch_bounds__(256) decode_f16_weights_kernel(const WeightArgs a) {
+__global__ void __launch_bounds__(256, 3) decode_f16_weights_kernel(const WeightArgs a) {
     constexpr int kTiles = 4;
     // A programmatic dependent of the merge, which itself waited for the decode.
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -723,9 +726,9 @@ __global__ void __launch_bounds__(256) decode_f16_weights_kernel(const WeightArg
 #pragma unroll
         for (int j = 0; j < kTiles; ++j) {
             if (tok >= info[j].w) continue;
-            const long long page = info[j].x / a.ps;
-            const int hk = info[j].y % a.Hkv;
-            atomicAdd(a.weights + (page * a.Hkv + hk) * a.ps + info[j].x % a.ps + tok, sum[j]);
+            const long long page = info[j].x >> a.page_bits;
+            const int off = info[j].x & ((1 << a.page_bits) - 1), hk = info[j].y % a.Hkv;
+            atomicAdd(a.weights + ((page * a.Hkv + hk) << a.page_bits) + off + tok, sum[j]);
         }
     }
 }
@@ -997,10 +1000,11 @@ int run_decode(const DecodeCall& c) {
     x.row_groups = rgs;
     x.R = R;
     x.pitch = a.pitch;
-    x.ps = c.ps;
+    x.page_bits = 0;
+    while ((1 << x.page_bits) < c.ps) ++x.page_bits;
     const long long tiles = streams * ((c.max_kv + kTile - 1) / kTile);
     const long long want = (tiles + 15) / 16;
-    const unsigned grid = static_cast<unsigned>(want < 8LL * dev.num_sms ? want : 8LL * dev.num_sms);
+    const unsigned grid = static_cast<unsigned>(want < 3LL * dev.num_sms ? want : 3LL * dev.num_sms);
     return launch_dependent(decode_f16_weights_kernel, dim3(grid), 256, s, x);
 }
 
