@@ -84,21 +84,27 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 // One cluster of 1..8 CTAs takes one (sequence, KV head).  Of its L > budget slots
 // the first `sink` and the last `recent` stay, and of the middle the M = budget -
 // sink - recent heaviest.  The M-th largest weight is found by radix selection on
-// order-preserving 32-bit keys, eight bits a pass: each CTA counts its part of the
-// slots (keys held in shared memory) into 256 bins, the cluster's CTAs read each
-// other's bins.  Keys above it are kept, and of those equal to it the first slots
+// order-preserving 32-bit keys in three passes (11, 11 and 10 bits): each CTA counts
+// its part of the slots (keys held in shared memory) into 2048 bins and adds the
+// counts to every CTA of the cluster.  Eleven bits hold the sign, the exponent and two
+// bits of the mantissa, so even the first pass spreads over some dozens of bins.  Keys above it are kept, and of those equal to it the first slots
 // up to M.  Prefix counts over warps and CTAs give every kept slot its place, in
 // slot order, and the rows move there.
 //
 // In place a row's new slot j is never above its old one, so rows may move in
-// rounds of consecutive j: a round's reads end (cluster barrier) before its
-// writes begin, and a write of this round lands below every later round's reads.
+// steps of consecutive j: a step's reads end (cluster barrier) before its writes
+// begin, and a write of this step lands below every later step's reads, which may
+// therefore run ahead.
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
-constexpr int kEvictRows = 4;            // rows in flight per thread
+constexpr int kEvictStages = 6;          // row steps in flight per thread
 constexpr int kEvictMaxCluster = 8;
-constexpr int kEvictMaxKeys = 24576;     // keys held per CTA (96 KB: two CTAs per SM)
+// Shared memory: the ring (K and V chunks, a weight per row) or the keys, 97 KB: two CTAs per SM.
+constexpr int kEvictRing = kEvictStages * kEvictThreads * (2 * 16 + 1);   // >= 4 chunks a row
+constexpr int kDigits = 3, kBins = 2048;   // 11, 11 and 10 bits of the key
+constexpr int kEvictMaxKeys = kEvictRing / 4 - (kDigits + 1) * kBins;
+static_assert(kBins == 4 * kEvictThreads, "four bins a thread");
 
 struct EvictArgs {
     uint4 *k_pages, *v_pages;
@@ -106,7 +112,7 @@ struct EvictArgs {
     const int32_t *table, *dst_table, *kv_lens;
     int32_t *new_lens, *kept;   // [B], [B][Hkv][budget]
     uint32_t* status;
-    int Hkv, chunk_bits, num_phys, ps, max_pages, dst_pages, max_kv, budget, sink, recent;
+    int Hkv, chunk_bits, page_bits, num_phys, ps, max_pages, dst_pages, max_kv, budget, sink, recent;
     int in_place, keys;         // keys: capacity of the CTA's key array
 };
 
@@ -118,9 +124,10 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictArgs a) {
-    extern __shared__ uint32_t s_keys[];
-    __shared__ uint32_t s_hist[2][256];
-    __shared__ uint32_t s_total[256];
+    extern __shared__ __align__(16) uint32_t s_dyn[];   // selection: counts and keys; then the ring
+    uint32_t* s_total = s_dyn;                          // [kDigits][kBins] of the whole cluster
+    uint32_t* s_hist = s_total + kDigits * kBins;       // [kBins] of this CTA
+    uint32_t* s_keys = s_hist + kBins;
     __shared__ uint32_t s_pick[2];                      // digit, keys still wanted at it
     __shared__ uint2 s_warp[kEvictWarps], s_cta;        // (above, equal) counts
     cg::cluster_group cluster = cg::this_cluster();
@@ -155,7 +162,8 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
     if (bad) return;   // the same answer in every CTA of the cluster
 
     auto weight_at = [&](int t) -> float* {
-        return a.weights + (static_cast<long long>(table[t / a.ps]) * a.Hkv + h) * a.ps + t % a.ps;
+        return a.weights + ((static_cast<long long>(table[t >> a.page_bits]) * a.Hkv + h) << a.page_bits) +
+               (t & (a.ps - 1));
     };
     if (L <= a.budget) {
         for (int j = first; j < n; j += step) kept[j] = j;
@@ -172,47 +180,69 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
             auto key_at = [&](int i) -> uint32_t {   // i relative to lo
                 return i < a.keys ? s_keys[i] : weight_key(*weight_at(a.sink + lo + i));
             };
-            for (int i = tid; i < min(hi - lo, a.keys); i += kEvictThreads)
-                s_keys[i] = weight_key(*weight_at(a.sink + lo + i));
+            for (int x = tid; x < kDigits * kBins; x += kEvictThreads) s_total[x] = 0;
+            // eight weights a thread at a time, so that the loads (each behind a page-table
+            // entry) wait together
+            for (int i0 = tid; i0 < min(hi - lo, a.keys); i0 += 8 * kEvictThreads) {
+                float wt[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = i0 + e * kEvictThreads;
+                    wt[e] = i < min(hi - lo, a.keys) ? *weight_at(a.sink + lo + i) : 0.0f;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = i0 + e * kEvictThreads;
+                    if (i < min(hi - lo, a.keys)) s_keys[i] = weight_key(wt[e]);
+                }
+            }
+            cluster.sync();   // every CTA's s_total is zero before anyone adds to it
             uint32_t chosen = 0, left = static_cast<uint32_t>(want);
 #pragma unroll 1
-            for (int pass = 0; pass < 4; ++pass) {
-                const int shift = 24 - 8 * pass;
-                uint32_t* hist = s_hist[pass & 1];
-                if (tid < 256) hist[tid] = 0;
+            for (int pass = 0; pass < kDigits; ++pass) {
+                const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+                const uint32_t mask = pass == 2 ? 1023u : 2047u;
+                const int above_shift = pass == 1 ? 21 : 10;   // of the digits chosen so far
+                for (int x = tid; x < kBins; x += kEvictThreads) s_hist[x] = 0;
                 __syncthreads();
                 for (int i = tid; i < hi - lo; i += kEvictThreads) {
                     const uint32_t key = key_at(i);
-                    if (pass == 0 || (key >> (shift + 8)) == chosen)
-                        atomicAdd(&hist[(key >> shift) & 255u], 1u);
+                    if (pass == 0 || (key >> above_shift) == chosen)
+                        atomicAdd(&s_hist[(key >> shift) & mask], 1u);
+                }
+                __syncthreads();
+                // few bins are in use: their counts go to every CTA of the cluster
+                uint32_t* total = s_total + pass * kBins;
+                for (int x = tid; x < kBins; x += kEvictThreads) {
+                    const uint32_t count = s_hist[x];
+                    if (count)
+                        for (int r = 0; r < C; ++r)
+                            atomicAdd(cluster.map_shared_rank(total, r) + x, count);
                 }
                 cluster.sync();
-                if (tid < 256) {
-                    uint32_t sum = 0;
-                    for (int r = 0; r < C; ++r) sum += cluster.map_shared_rank(hist, r)[tid];
-                    s_total[tid] = sum;
-                }
-                __syncthreads();
-                if (warp == 0) {   // the bin that holds the left-th largest: eight bins a lane
-                    uint32_t own = 0;
-                    for (int e = 0; e < 8; ++e) own += s_total[255 - (8 * lane + e)];
-                    uint32_t incl = own;
+                // the bin that holds the left-th largest key: four bins a thread, from the top
+                uint32_t own = 0;
 #pragma unroll
-                    for (int sh = 1; sh < 32; sh <<= 1) {
-                        const uint32_t y = __shfl_up_sync(0xffffffffu, incl, sh);
-                        if (lane >= sh) incl += y;
-                    }
-                    uint32_t above = incl - own;
-                    if (above < left && left <= incl) {
-                        int e = 0;
-                        while (above + s_total[255 - (8 * lane + e)] < left)
-                            above += s_total[255 - (8 * lane + e++)];
-                        s_pick[0] = 255 - (8 * lane + e);
-                        s_pick[1] = left - above;
-                    }
+                for (int e = 0; e < 4; ++e) own += total[kBins - 1 - (4 * tid + e)];
+                uint32_t incl = own;
+#pragma unroll
+                for (int sh = 1; sh < 32; sh <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, incl, sh);
+                    if (lane >= sh) incl += y;
+                }
+                if (lane == 31) s_warp[warp].x = incl;
+                __syncthreads();
+                for (int k = 0; k < warp; ++k) incl += s_warp[k].x;
+                uint32_t above = incl - own;
+                if (above < left && left <= incl) {
+                    int e = 0;
+                    while (above + total[kBins - 1 - (4 * tid + e)] < left)
+                        above += total[kBins - 1 - (4 * tid + e++)];
+                    s_pick[0] = kBins - 1 - (4 * tid + e);
+                    s_pick[1] = left - above;
                 }
                 __syncthreads();
-                chosen = (chosen << 8) | s_pick[0];
+                chosen = (chosen << (pass == 2 ? 10 : 11)) | s_pick[0];
                 left = s_pick[1];
             }
             // ---- places: a warp takes consecutive slots; (above, equal) counts before it
@@ -257,43 +287,73 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
     }
     cluster.sync();   // kept[] is complete; nobody reads another CTA's shared memory any more
 
-    // ---- the rows: a thread moves one 16-byte chunk of K and of V of kEvictRows rows a round
-    const int chunks = 1 << a.chunk_bits;
-    const int rows_step = kEvictThreads >> a.chunk_bits;   // rows the CTA's threads cover at once
-    const int per_round = rows_step * kEvictRows;
-    const int c = tid & (chunks - 1), r0 = tid >> a.chunk_bits;
+    // ---- the rows.  A step moves rows_step rows per CTA, a thread one 16-byte chunk of K and
+    // of V of its row (and the row's weight); the copies to shared memory run kEvictStages
+    // steps ahead of the stores.  A thread reads back only what it copied itself, so the ring
+    // needs no barrier; the keys' shared memory is free by now.
+    const int rows_step = kEvictThreads >> a.chunk_bits;
+    const int c = tid & ((1 << a.chunk_bits) - 1), r0 = rank * rows_step + (tid >> a.chunk_bits);
+    const int stride = C * rows_step;
+    const int steps = (n + stride - 1) / stride;   // the same in every CTA of the cluster
     const long long row_chunks = static_cast<long long>(a.Hkv) << a.chunk_bits;
-    for (int base = 0; base < n; base += C * per_round) {
-        uint4 kr[kEvictRows], vr[kEvictRows];
-        float wr[kEvictRows];
-        int to[kEvictRows];
-#pragma unroll
-        for (int u = 0; u < kEvictRows; ++u) {
-            const int j = base + rank * per_round + u * rows_step + r0;
-            to[u] = -1;
-            if (j >= n) continue;
-            const int t = __ldcg(kept + j);
-            if (a.in_place && t == j) continue;
-            to[u] = j;
-            const long long page = table[t / a.ps];
-            const int slot = t % a.ps;
-            const long long at = (page * a.ps + slot) * row_chunks + (h << a.chunk_bits) + c;
-            kr[u] = a.k_pages[at];
-            vr[u] = a.v_pages[at];
-            if (c == 0) wr[u] = a.weights[(page * a.Hkv + h) * a.ps + slot];
+    uint4* ring = reinterpret_cast<uint4*>(s_dyn);
+    float* ring_w = reinterpret_cast<float*>(ring + kEvictStages * 2 * kEvictThreads);
+    // The index chain of a row, old slot then page, is fetched two steps before its copy: each
+    // link has a step's time to arrive.
+    auto old_slot = [&](int step) -> int {   // -1: no row, or one that stays where it is
+        const int j = step * stride + r0;
+        if (j >= n) return -1;
+        const int t = __ldcg(kept + j);
+        return a.in_place && t == j ? -1 : t;
+    };
+    auto page_of = [&](int t) -> int { return t < 0 ? 0 : table[t >> a.page_bits]; };
+    const int slot_mask = a.ps - 1;
+    uint32_t moved = 0;   // bit step % 32: this thread's row of the step has to be stored
+    auto fetch = [&](int step, int t, int page) {
+        const uint32_t bit = 1u << (step & 31);
+        moved = t < 0 ? moved & ~bit : moved | bit;
+        if (t >= 0) {
+            const int st = step % kEvictStages;
+            const long long row = (static_cast<long long>(page) << a.page_bits) + (t & slot_mask);
+            const long long at = row * row_chunks + (h << a.chunk_bits) + c;
+            cp_async16(ring + (2 * st) * kEvictThreads + tid, a.k_pages + at);
+            cp_async16(ring + (2 * st + 1) * kEvictThreads + tid, a.v_pages + at);
+            if (c == 0)
+                cp_async4(ring_w + st * rows_step + (tid >> a.chunk_bits),
+                          a.weights + ((static_cast<long long>(page) * a.Hkv + h) << a.page_bits) +
+                              (t & slot_mask));
         }
-        if (a.in_place) cluster.sync();
-#pragma unroll
-        for (int u = 0; u < kEvictRows; ++u) {
-            if (to[u] < 0) continue;
-            const long long page = dst_table[to[u] / a.ps];
-            const int slot = to[u] % a.ps;
-            const long long at = (page * a.ps + slot) * row_chunks + (h << a.chunk_bits) + c;
-            a.k_pages[at] = kr[u];
-            a.v_pages[at] = vr[u];
-            if (c == 0) a.weights[(page * a.Hkv + h) * a.ps + slot] = wr[u];
+        cp_async_commit();
+    };
+    int t0 = old_slot(0), t1 = old_slot(1);
+    int page0 = page_of(t0);
+    auto advance = [&](int step) {   // copy `step`, move the chain on
+        const int t2 = old_slot(step + 2), page1 = page_of(t1);
+        fetch(step, t0, page0);
+        t0 = t1;
+        t1 = t2;
+        page0 = page1;
+    };
+    for (int step = 0; step < kEvictStages - 1; ++step) advance(step);   // past the last: nothing
+    for (int step = 0; step < steps; ++step) {
+        const int j = step * stride + r0;
+        const bool mine = (moved >> (step & 31)) & 1u;
+        const int dst_page = mine ? dst_table[j >> a.page_bits] : 0;
+        advance(step + kEvictStages - 1);
+        cp_async_wait<kEvictStages - 1>();   // this step's copies have landed
+        if (a.in_place) cluster.sync();      // and those of every other row of the step
+        if (mine) {
+            const int st = step % kEvictStages;
+            const long long row = (static_cast<long long>(dst_page) << a.page_bits) + (j & slot_mask);
+            const long long at = row * row_chunks + (h << a.chunk_bits) + c;
+            a.k_pages[at] = ring[(2 * st) * kEvictThreads + tid];
+            a.v_pages[at] = ring[(2 * st + 1) * kEvictThreads + tid];
+            if (c == 0)
+                a.weights[((static_cast<long long>(dst_page) * a.Hkv + h) << a.page_bits) +
+                          (j & slot_mask)] = ring_w[st * rows_step + (tid >> a.chunk_bits)];
         }
     }
+    cp_async_wait<0>();
 }
 
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
@@ -458,16 +518,16 @@ extern "C" int kv_paged_evict(void* k_pages, void* v_pages, float* weights,
     a.budget = budget;
     a.sink = sink;
     a.recent = recent;
+    while ((1 << a.page_bits) < page_size) ++a.page_bits;
     a.in_place = in_place ? 1 : 0;
-    const int need = (max_kv_len + C - 1) / C;
-    a.keys = need < kEvictMaxKeys ? need : kEvictMaxKeys;
+    a.keys = kEvictMaxKeys;
     static std::once_flag once[64];
     static int attr_rc[64];
     if (dev.device < 0 || dev.device >= 64) return GBATTN_ERR_CUDA;
     std::call_once(once[dev.device], [&] {
         attr_rc[dev.device] = cudaFuncSetAttribute(kv_evict_kernel,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kEvictMaxKeys * 4) == cudaSuccess
+                                                   kEvictRing) == cudaSuccess
                                   ? GBATTN_OK
                                   : GBATTN_ERR_CUDA;
     });
@@ -475,7 +535,7 @@ extern "C" int kv_paged_evict(void* k_pages, void* v_pages, float* weights,
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(streams * C));
     cfg.blockDim = dim3(kEvictThreads);
-    cfg.dynamicSmemBytes = static_cast<size_t>(a.keys) * 4;
+    cfg.dynamicSmemBytes = kEvictRing;
     cfg.stream = static_cast<cudaStream_t>(stream);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -183,11 +183,22 @@ __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
                  "l"(reinterpret_cast<uint64_t>(src))
                  : "memory");
 }
+// 4-byte global -> shared copy.
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src))
+                 : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
 __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+// All but the N most recent committed groups have completed.
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 // All but the most recent committed group have completed.
 __device__ __forceinline__ void cp_async_wait_one() {
