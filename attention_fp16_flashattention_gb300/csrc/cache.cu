@@ -113,7 +113,7 @@ struct EvictArgs {
     int32_t *new_lens, *kept;   // [B], [B][Hkv][budget]
     uint32_t* status;
     int Hkv, chunk_bits, page_bits, num_phys, ps, max_pages, dst_pages, max_kv, budget, sink, recent;
-    int in_place, keys;         // keys: capacity of the CTA's key array
+    int keys;                   // capacity of the CTA's key array
 };
 
 // Larger key = larger weight; NaN is below everything, -0 equals 0.
@@ -123,14 +123,16 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictArgs a) {
-    extern __shared__ __align__(16) uint32_t s_dyn[];   // selection: counts and keys; then the ring
+// Writes new_lens and kept[] of the cluster's (sequence, KV head).  False: nothing is to be
+// moved (the same answer in every CTA of the cluster).
+template <bool kInPlace>
+__device__ __forceinline__ bool evict_select(const EvictArgs& a, uint32_t* s_dyn,
+                                             cg::cluster_group& cluster) {
     uint32_t* s_total = s_dyn;                          // [kDigits][kBins] of the whole cluster
     uint32_t* s_hist = s_total + kDigits * kBins;       // [kBins] of this CTA
     uint32_t* s_keys = s_hist + kBins;
-    __shared__ uint32_t s_pick[2];                      // digit, keys still wanted at it
+    __shared__ uint32_t s_pick[2];                      // a bad page; then digit, keys still wanted at it
     __shared__ uint2 s_warp[kEvictWarps], s_cta;        // (above, equal) counts
-    cg::cluster_group cluster = cg::this_cluster();
     const int C = static_cast<int>(cluster.num_blocks());
     const int rank = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -142,88 +144,119 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
     const int L = a.kv_lens[b];
     const int first = rank * kEvictThreads + tid, step = C * kEvictThreads;
 
-    // ---- a sequence whose length or pages are out of range stays as it is
-    bool bad = L < 0 || L > a.max_kv;
-    const int n = bad ? 0 : min(L, a.budget);
-    if (bad) {
-        if (first == 0) atomicOr(a.status, kDevBadLength);
-    } else {
-        bool bad_page = false;
-        for (int p = tid; p < (L + a.ps - 1) / a.ps; p += kEvictThreads)
-            bad_page |= table[p] < 0 || table[p] >= a.num_phys;
-        if (!a.in_place)
-            for (int p = tid; p < (n + a.ps - 1) / a.ps; p += kEvictThreads)
-                bad_page |= dst_table[p] < 0 || dst_table[p] >= a.num_phys;
-        bad = __syncthreads_or(bad_page) != 0;
-        if (bad && first == 0) atomicOr(a.status, kDevBadPage);
-    }
-    if (h == 0 && first == 0) a.new_lens[b] = bad ? L : n;
-    for (int j = (bad ? 0 : n) + first; j < a.budget; j += step) kept[j] = -1;
-    if (bad) return;   // the same answer in every CTA of the cluster
-
+    const bool bad_len = L < 0 || L > a.max_kv;
+    if (bad_len && first == 0) atomicOr(a.status, kDevBadLength);
+    const int n = bad_len ? 0 : min(L, a.budget);
+    const int want = !bad_len && L > a.budget ? n - a.sink - a.recent : 0;   // M
+    // this CTA's part [lo, hi) of the middle slots
+    const int mid = want > 0 ? L - a.sink - a.recent : 0;
+    const int per = (mid + C - 1) / C;
+    const int lo = min(rank * per, mid), hi = min(lo + per, mid);
+    auto bad_slots = [&](const int32_t* tab, int t_lo, int t_hi) -> bool {   // [t_lo, t_hi)
+        bool bad = false;
+        for (int p = (t_lo >> a.page_bits) + tid; p < (t_hi + a.ps - 1) >> a.page_bits; p += kEvictThreads)
+            bad |= tab[p] < 0 || tab[p] >= a.num_phys;
+        return bad;
+    };
     auto weight_at = [&](int t) -> float* {
         return a.weights + ((static_cast<long long>(table[t >> a.page_bits]) * a.Hkv + h) << a.page_bits) +
                (t & (a.ps - 1));
     };
+    auto key_at = [&](int i) -> uint32_t {   // i relative to lo
+        return i < a.keys ? s_keys[i] : weight_key(*weight_at(a.sink + lo + i));
+    };
+
+    // ---- the keys of this CTA's part, and whether any page is out of range
+    bool bad = false;
+    if (!bad_len) {
+        const int held = min(hi - lo, a.keys);
+        // eight weights a thread at a time, so that the loads (each behind a page-table
+        // entry) wait together
+        for (int i0 = tid; i0 < held; i0 += 8 * kEvictThreads) {
+            int page[8];
+            float wt[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = i0 + e * kEvictThreads;
+                page[e] = i < held ? table[(a.sink + lo + i) >> a.page_bits] : 0;
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = i0 + e * kEvictThreads;
+                const bool out = page[e] < 0 || page[e] >= a.num_phys;
+                bad |= out;
+                wt[e] = 0.0f;
+                if (i < held && !out)
+                    wt[e] = a.weights[((static_cast<long long>(page[e]) * a.Hkv + h) << a.page_bits) +
+                                      ((a.sink + lo + i) & (a.ps - 1))];
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int i = i0 + e * kEvictThreads;
+                if (i < held) s_keys[i] = weight_key(wt[e]);
+            }
+        }
+        // the pages of every other slot
+        if (mid == 0) {
+            bad |= bad_slots(table, 0, L);
+        } else {
+            bad |= bad_slots(table, 0, a.sink) | bad_slots(table, L - a.recent, L) |
+                   bad_slots(table, a.sink + lo + held, a.sink + hi);
+        }
+        if (!kInPlace) bad |= bad_slots(dst_table, 0, n);
+    }
+    for (int x = tid; x < kDigits * kBins; x += kEvictThreads) s_total[x] = 0;
+    bad = __syncthreads_or(bad) != 0;
+    if (C > 1 && want > 0) {   // the CTAs checked different pages; and every s_total is zero
+        if (tid == 0) s_pick[0] = bad ? 1u : 0u;
+        cluster.sync();
+        for (int r = 0; r < C; ++r) bad |= cluster.map_shared_rank(s_pick, r)[0] != 0;
+    }
+    if (bad && first == 0) atomicOr(a.status, kDevBadPage);
+    bad |= bad_len;
+
+    // ---- a sequence whose length or pages are out of range stays as it is
+    if (h == 0 && first == 0) a.new_lens[b] = bad ? L : n;
+    for (int j = (bad ? 0 : n) + first; j < a.budget; j += step) kept[j] = -1;
+    if (bad) return false;
     if (L <= a.budget) {
         for (int j = first; j < n; j += step) kept[j] = j;
-        if (a.in_place) return;
+        if (kInPlace) return false;
     } else {
         for (int j = first; j < a.sink; j += step) kept[j] = j;
         for (int j = first; j < a.recent; j += step) kept[n - a.recent + j] = L - a.recent + j;
-        const int want = n - a.sink - a.recent;   // M
         if (want > 0) {
-            // this CTA's part [lo, hi) of the middle slots
-            const int mid = L - a.sink - a.recent;
-            const int per = (mid + C - 1) / C;
-            const int lo = min(rank * per, mid), hi = min(lo + per, mid);
-            auto key_at = [&](int i) -> uint32_t {   // i relative to lo
-                return i < a.keys ? s_keys[i] : weight_key(*weight_at(a.sink + lo + i));
-            };
-            for (int x = tid; x < kDigits * kBins; x += kEvictThreads) s_total[x] = 0;
-            // eight weights a thread at a time, so that the loads (each behind a page-table
-            // entry) wait together
-            for (int i0 = tid; i0 < min(hi - lo, a.keys); i0 += 8 * kEvictThreads) {
-                float wt[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int i = i0 + e * kEvictThreads;
-                    wt[e] = i < min(hi - lo, a.keys) ? *weight_at(a.sink + lo + i) : 0.0f;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int i = i0 + e * kEvictThreads;
-                    if (i < min(hi - lo, a.keys)) s_keys[i] = weight_key(wt[e]);
-                }
-            }
-            cluster.sync();   // every CTA's s_total is zero before anyone adds to it
             uint32_t chosen = 0, left = static_cast<uint32_t>(want);
 #pragma unroll 1
             for (int pass = 0; pass < kDigits; ++pass) {
                 const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
                 const uint32_t mask = pass == 2 ? 1023u : 2047u;
                 const int above_shift = pass == 1 ? 21 : 10;   // of the digits chosen so far
-                for (int x = tid; x < kBins; x += kEvictThreads) s_hist[x] = 0;
-                __syncthreads();
+                uint32_t* total = s_total + pass * kBins;
+                uint32_t* hist = C > 1 ? s_hist : total;
+                if (C > 1) {
+                    for (int x = tid; x < kBins; x += kEvictThreads) hist[x] = 0;
+                    __syncthreads();
+                }
                 for (int i = tid; i < hi - lo; i += kEvictThreads) {
                     const uint32_t key = key_at(i);
                     if (pass == 0 || (key >> above_shift) == chosen)
-                        atomicAdd(&s_hist[(key >> shift) & mask], 1u);
+                        atomicAdd(&hist[(key >> shift) & mask], 1u);
                 }
                 __syncthreads();
-                // few bins are in use: their counts go to every CTA of the cluster
-                uint32_t* total = s_total + pass * kBins;
-                for (int x = tid; x < kBins; x += kEvictThreads) {
-                    const uint32_t count = s_hist[x];
-                    if (count)
-                        for (int r = 0; r < C; ++r)
-                            atomicAdd(cluster.map_shared_rank(total, r) + x, count);
+                if (C > 1) {   // few bins are in use: their counts go to every CTA of the cluster
+                    for (int x = tid; x < kBins; x += kEvictThreads) {
+                        const uint32_t count = hist[x];
+                        if (count)
+                            for (int r = 0; r < C; ++r)
+                                atomicAdd(cluster.map_shared_rank(total, r) + x, count);
+                    }
+                    cluster.sync();
                 }
-                cluster.sync();
                 // the bin that holds the left-th largest key: four bins a thread, from the top
-                uint32_t own = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) own += total[kBins - 1 - (4 * tid + e)];
+                const int top = kBins - 4 - 4 * tid;
+                const uint4 bins = *reinterpret_cast<const uint4*>(total + top);
+                const uint32_t own = bins.x + bins.y + bins.z + bins.w;
                 uint32_t incl = own;
 #pragma unroll
                 for (int sh = 1; sh < 32; sh <<= 1) {
@@ -235,11 +268,15 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
                 for (int k = 0; k < warp; ++k) incl += s_warp[k].x;
                 uint32_t above = incl - own;
                 if (above < left && left <= incl) {
-                    int e = 0;
-                    while (above + total[kBins - 1 - (4 * tid + e)] < left)
-                        above += total[kBins - 1 - (4 * tid + e++)];
-                    s_pick[0] = kBins - 1 - (4 * tid + e);
-                    s_pick[1] = left - above;
+                    const uint32_t count[4] = {bins.w, bins.z, bins.y, bins.x};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        if (above < left && left <= above + count[e]) {
+                            s_pick[0] = top + 3 - e;
+                            s_pick[1] = left - above;
+                        }
+                        above += count[e];
+                    }
                 }
                 __syncthreads();
                 chosen = (chosen << (pass == 2 ? 10 : 11)) | s_pick[0];
@@ -265,7 +302,7 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
             }
             if (tid == kEvictThreads - 1)
                 s_cta = make_uint2(above + s_warp[warp].x, equal + s_warp[warp].y);
-            cluster.sync();
+            if (C > 1) cluster.sync();
             for (int r = 0; r < rank; ++r) {
                 const uint2 t = *cluster.map_shared_rank(&s_cta, r);
                 above += t.x;
@@ -285,73 +322,179 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_kernel(const EvictA
             }
         }
     }
-    cluster.sync();   // kept[] is complete; nobody reads another CTA's shared memory any more
+    return true;
+}
 
-    // ---- the rows.  A step moves rows_step rows per CTA, a thread one 16-byte chunk of K and
-    // of V of its row (and the row's weight); the copies to shared memory run kEvictStages
-    // steps ahead of the stores.  A thread reads back only what it copied itself, so the ring
-    // needs no barrier; the keys' shared memory is free by now.
-    const int rows_step = kEvictThreads >> a.chunk_bits;
-    const int c = tid & ((1 << a.chunk_bits) - 1), r0 = rank * rows_step + (tid >> a.chunk_bits);
-    const int stride = C * rows_step;
+// The shared-memory ring of row copies in flight: stage, K or V, thread; then a weight per row.
+struct EvictRing {
+    uint4* data;
+    float* w;
+    int tid, rows, row, c;   // rows of a stage; this thread's row and chunk of it
+    long long row_chunks;
+    __device__ __forceinline__ EvictRing(uint32_t* smem, const EvictArgs& a, int t)
+        : data(reinterpret_cast<uint4*>(smem)),
+          w(reinterpret_cast<float*>(data + kEvictStages * 2 * kEvictThreads)),
+          tid(t),
+          rows(kEvictThreads >> a.chunk_bits),
+          row(t >> a.chunk_bits),
+          c(t & ((1 << a.chunk_bits) - 1)),
+          row_chunks(static_cast<long long>(a.Hkv) << a.chunk_bits) {}
+    // Starts the copy of slot t (on physical page `page`) of head h into the stage of `step`.
+    __device__ __forceinline__ void fetch(const EvictArgs& a, int step, int page, int t, int h) {
+        const int st = step % kEvictStages, off = t & (a.ps - 1);
+        const long long at =
+            ((static_cast<long long>(page) << a.page_bits) + off) * row_chunks + (h << a.chunk_bits) + c;
+        cp_async16(data + (2 * st) * kEvictThreads + tid, a.k_pages + at);
+        cp_async16(data + (2 * st + 1) * kEvictThreads + tid, a.v_pages + at);
+        if (c == 0)
+            cp_async4(w + st * rows + row,
+                      a.weights + ((static_cast<long long>(page) * a.Hkv + h) << a.page_bits) + off);
+    }
+    // Writes the stage of `step` to slot j (on physical page `page`).
+    __device__ __forceinline__ void store(const EvictArgs& a, int step, int page, int j, int h) {
+        const int st = step % kEvictStages, off = j & (a.ps - 1);
+        const long long at =
+            ((static_cast<long long>(page) << a.page_bits) + off) * row_chunks + (h << a.chunk_bits) + c;
+        a.k_pages[at] = data[(2 * st) * kEvictThreads + tid];
+        a.v_pages[at] = data[(2 * st + 1) * kEvictThreads + tid];
+        if (c == 0)
+            a.weights[((static_cast<long long>(page) * a.Hkv + h) << a.page_bits) + off] =
+                w[st * rows + row];
+    }
+};
+
+// In place: selection, then the cluster moves its rows.  A step moves rows_step rows per CTA, a
+// thread one 16-byte chunk of K and of V of its row (and the row's weight); the copies to shared
+// memory run ahead of the stores.  A thread reads back only what it copied itself, so the ring
+// needs no barrier of its own; the selection's shared memory is free by then.
+__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_in_place_kernel(const EvictArgs a) {
+    extern __shared__ __align__(16) uint32_t s_dyn[];   // selection: counts and keys; then the ring
+    cg::cluster_group cluster = cg::this_cluster();
+    const bool move = evict_select<true>(a, s_dyn, cluster);
+    cluster.sync();   // kept[] is complete; nobody uses another CTA's shared memory any more
+    if (!move) return;
+    const int C = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int tid = threadIdx.x;
+    const long long stream = blockIdx.x / C;
+    const int b = static_cast<int>(stream / a.Hkv), h = static_cast<int>(stream - static_cast<long long>(b) * a.Hkv);
+    const int32_t* table = a.table + static_cast<long long>(b) * a.max_pages;
+    const int32_t* kept = a.kept + stream * a.budget;
+    const int n = a.budget;   // the selection returned true: the cache was longer
+
+    EvictRing ring(s_dyn, a, tid);
+    const int stride = C * ring.rows, r0 = rank * ring.rows + ring.row;
     const int steps = (n + stride - 1) / stride;   // the same in every CTA of the cluster
-    const long long row_chunks = static_cast<long long>(a.Hkv) << a.chunk_bits;
-    uint4* ring = reinterpret_cast<uint4*>(s_dyn);
-    float* ring_w = reinterpret_cast<float*>(ring + kEvictStages * 2 * kEvictThreads);
     // The index chain of a row, old slot then page, is fetched two steps before its copy: each
     // link has a step's time to arrive.
     auto old_slot = [&](int step) -> int {   // -1: no row, or one that stays where it is
         const int j = step * stride + r0;
         if (j >= n) return -1;
         const int t = __ldcg(kept + j);
-        return a.in_place && t == j ? -1 : t;
+        return t == j ? -1 : t;
     };
     auto page_of = [&](int t) -> int { return t < 0 ? 0 : table[t >> a.page_bits]; };
-    const int slot_mask = a.ps - 1;
     uint32_t moved = 0;   // bit step % 32: this thread's row of the step has to be stored
-    auto fetch = [&](int step, int t, int page) {
-        const uint32_t bit = 1u << (step & 31);
-        moved = t < 0 ? moved & ~bit : moved | bit;
-        if (t >= 0) {
-            const int st = step % kEvictStages;
-            const long long row = (static_cast<long long>(page) << a.page_bits) + (t & slot_mask);
-            const long long at = row * row_chunks + (h << a.chunk_bits) + c;
-            cp_async16(ring + (2 * st) * kEvictThreads + tid, a.k_pages + at);
-            cp_async16(ring + (2 * st + 1) * kEvictThreads + tid, a.v_pages + at);
-            if (c == 0)
-                cp_async4(ring_w + st * rows_step + (tid >> a.chunk_bits),
-                          a.weights + ((static_cast<long long>(page) * a.Hkv + h) << a.page_bits) +
-                              (t & slot_mask));
-        }
-        cp_async_commit();
-    };
     int t0 = old_slot(0), t1 = old_slot(1);
     int page0 = page_of(t0);
     auto advance = [&](int step) {   // copy `step`, move the chain on
         const int t2 = old_slot(step + 2), page1 = page_of(t1);
-        fetch(step, t0, page0);
+        const uint32_t bit = 1u << (step & 31);
+        moved = t0 < 0 ? moved & ~bit : moved | bit;
+        if (t0 >= 0) ring.fetch(a, step, page0, t0, h);
+        cp_async_commit();
         t0 = t1;
         t1 = t2;
         page0 = page1;
     };
-    for (int step = 0; step < kEvictStages - 1; ++step) advance(step);   // past the last: nothing
-    for (int step = 0; step < steps; ++step) {
-        const int j = step * stride + r0;
-        const bool mine = (moved >> (step & 31)) & 1u;
-        const int dst_page = mine ? dst_table[j >> a.page_bits] : 0;
-        advance(step + kEvictStages - 1);
-        cp_async_wait<kEvictStages - 1>();   // this step's copies have landed
-        if (a.in_place) cluster.sync();      // and those of every other row of the step
-        if (mine) {
-            const int st = step % kEvictStages;
-            const long long row = (static_cast<long long>(dst_page) << a.page_bits) + (j & slot_mask);
-            const long long at = row * row_chunks + (h << a.chunk_bits) + c;
-            a.k_pages[at] = ring[(2 * st) * kEvictThreads + tid];
-            a.v_pages[at] = ring[(2 * st + 1) * kEvictThreads + tid];
-            if (c == 0)
-                a.weights[((static_cast<long long>(dst_page) * a.Hkv + h) << a.page_bits) +
-                          (j & slot_mask)] = ring_w[st * rows_step + (tid >> a.chunk_bits)];
+    // A cluster barrier stands between the reads of three steps and their writes.
+    constexpr int kGroup = 3, kAhead = kEvictStages - kGroup;
+    for (int step = 0; step < kAhead; ++step) advance(step);   // past the last: nothing
+    for (int base = 0; base < steps; base += kGroup) {
+        bool mine[kGroup];
+        int dst_page[kGroup];
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+            mine[u] = (moved >> ((base + u) & 31)) & 1u;   // false past the last step
+            dst_page[u] = mine[u] ? table[((base + u) * stride + r0) >> a.page_bits] : 0;
         }
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) advance(base + kAhead + u);
+        cp_async_wait<kAhead>();   // these steps' copies have landed
+        cluster.sync();            // and those of every other row of them
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u)
+            if (mine[u]) ring.store(a, base + u, dst_page[u], (base + u) * stride + r0, h);
+    }
+    cp_async_wait<0>();
+}
+
+// Into other pages: the selection alone, and a copy kernel whose CTAs share all heads' rows evenly.
+__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_select_kernel(const EvictArgs a) {
+    extern __shared__ __align__(16) uint32_t s_dyn[];
+    cg::cluster_group cluster = cg::this_cluster();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    evict_select<false>(a, s_dyn, cluster);
+    cluster.sync();   // nobody leaves while another CTA adds to or reads its shared memory
+}
+
+__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_copy_kernel(const EvictArgs a, int most,
+                                                                         long long units,
+                                                                         int stream_units) {
+    extern __shared__ __align__(16) uint32_t s_dyn[];
+    const int tid = threadIdx.x;
+    EvictRing ring(s_dyn, a, tid);
+    // Unit u is step u % stream_units of head u / stream_units; this CTA takes every grid-th.
+    struct Row {
+        int b, h, j, t;   // t: old slot, -1 for no row
+    };
+    auto old_row = [&](int k) -> Row {
+        Row x{0, 0, 0, -1};
+        const long long u = blockIdx.x + static_cast<long long>(k) * gridDim.x;
+        if (u >= units) return x;
+        const int stream = static_cast<int>(u / stream_units);
+        x.b = stream / a.Hkv;
+        x.h = stream - x.b * a.Hkv;
+        x.j = static_cast<int>(u - static_cast<long long>(stream) * stream_units) * ring.rows + ring.row;
+        if (x.j < most) x.t = a.kept[static_cast<long long>(stream) * a.budget + x.j];
+        return x;
+    };
+    // source and destination page of a row
+    auto pages_of = [&](const Row& x) -> int2 {
+        if (x.t < 0) return make_int2(0, 0);
+        return make_int2(a.table[static_cast<long long>(x.b) * a.max_pages + (x.t >> a.page_bits)],
+                         a.dst_table[static_cast<long long>(x.b) * a.dst_pages + (x.j >> a.page_bits)]);
+    };
+    const long long mine = (units - blockIdx.x + gridDim.x - 1) / gridDim.x;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // The index chain (kept slot, then pages) runs two steps ahead of the copies, the copies
+    // kEvictStages - 1 steps ahead of the stores.
+    Row x0 = old_row(0), x1 = old_row(1);
+    int2 p0 = pages_of(x0);
+    // destination page (-1: no row), slot and head of the rows in flight
+    __shared__ int s_page[kEvictStages][kEvictThreads / 4];
+    __shared__ int2 s_to[kEvictStages][kEvictThreads / 4];
+    auto advance = [&](int k) {
+        const Row x2 = old_row(k + 2);
+        const int2 p1 = pages_of(x1);
+        if (ring.c == 0) {   // read back by the row's threads, all of one warp
+            s_page[k % kEvictStages][ring.row] = x0.t < 0 ? -1 : p0.y;
+            s_to[k % kEvictStages][ring.row] = make_int2(x0.j, x0.h);
+        }
+        if (x0.t >= 0) ring.fetch(a, k, p0.x, x0.t, x0.h);
+        cp_async_commit();
+        x0 = x1;
+        x1 = x2;
+        p0 = p1;
+    };
+    for (int k = 0; k < kEvictStages - 1; ++k) advance(k);
+    for (int k = 0; k < mine; ++k) {
+        __syncwarp();
+        const int page = s_page[k % kEvictStages][ring.row];
+        const int2 to = s_to[k % kEvictStages][ring.row];
+        __syncwarp();
+        advance(k + kEvictStages - 1);
+        cp_async_wait<kEvictStages - 1>();
+        if (page >= 0) ring.store(a, k, page, to.x, to.y);
     }
     cp_async_wait<0>();
 }
@@ -464,7 +607,7 @@ extern "C" int kv_paged_evict(void* k_pages, void* v_pages, float* weights,
         return GBATTN_ERR_NULL;
     if (B <= 0 || Hkv <= 0 || num_phys_pages <= 0 || page_size <= 0 || max_pages <= 0 ||
         dst_pages <= 0 || max_kv_len <= 0 || budget <= 0 || sink < 0 || recent < 0 ||
-        static_cast<long long>(sink) + recent > budget ||
+        static_cast<long long>(sink) + recent > budget || max_kv_len > (1 << 30) ||
         static_cast<long long>(max_kv_len) > static_cast<long long>(max_pages) * page_size)
         return GBATTN_ERR_SHAPE;
     const bool in_place = dst_table == page_table;
@@ -495,9 +638,10 @@ extern "C" int kv_paged_evict(void* k_pages, void* v_pages, float* weights,
     const int rc = current_device(&dev);
     if (rc != GBATTN_OK) return rc;
 
-    // The largest cluster with which every CTA of the grid is resident at once (two per SM).
+    // Selection: a CTA for about 4096 slots, as long as all CTAs are resident at once (two per SM).
+    // In place the cluster also moves its rows, so it is as large as that allows.
     int C = kEvictMaxCluster;
-    while (C > 1 && streams * C > 2LL * dev.num_sms) C /= 2;
+    while (C > 1 && (streams * C > 2LL * dev.num_sms || (!in_place && max_kv_len <= 2048LL * C))) C /= 2;
     EvictArgs a{};
     a.k_pages = static_cast<uint4*>(k_pages);
     a.v_pages = static_cast<uint4*>(v_pages);
@@ -519,17 +663,17 @@ extern "C" int kv_paged_evict(void* k_pages, void* v_pages, float* weights,
     a.sink = sink;
     a.recent = recent;
     while ((1 << a.page_bits) < page_size) ++a.page_bits;
-    a.in_place = in_place ? 1 : 0;
     a.keys = kEvictMaxKeys;
     static std::once_flag once[64];
     static int attr_rc[64];
     if (dev.device < 0 || dev.device >= 64) return GBATTN_ERR_CUDA;
     std::call_once(once[dev.device], [&] {
-        attr_rc[dev.device] = cudaFuncSetAttribute(kv_evict_kernel,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kEvictRing) == cudaSuccess
-                                  ? GBATTN_OK
-                                  : GBATTN_ERR_CUDA;
+        bool ok = cudaFuncSetAttribute(kv_evict_copy_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       kEvictRing) == cudaSuccess;
+        for (auto* k : {kv_evict_in_place_kernel, kv_evict_select_kernel})
+            ok = ok && cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            kEvictRing) == cudaSuccess;
+        attr_rc[dev.device] = ok ? GBATTN_OK : GBATTN_ERR_CUDA;
     });
     if (attr_rc[dev.device] != GBATTN_OK) return attr_rc[dev.device];
     cudaLaunchConfig_t cfg{};
@@ -544,8 +688,25 @@ extern "C" int kv_paged_evict(void* k_pages, void* v_pages, float* weights,
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_evict_kernel, a);
+    cudaError_t e = cudaLaunchKernelEx(&cfg, in_place ? kv_evict_in_place_kernel : kv_evict_select_kernel, a);
     count_launches(1);
+    if (e == cudaSuccess && !in_place) {
+        // Its CTAs may be placed as the selection's leave; they wait for all of it.
+        const int stream_units = (most + (kEvictThreads >> bits) - 1) / (kEvictThreads >> bits);
+        const long long units = streams * stream_units;
+        cudaLaunchConfig_t copy{};
+        copy.gridDim = dim3(static_cast<unsigned>(units < 2LL * dev.num_sms ? units : 2LL * dev.num_sms));
+        copy.blockDim = dim3(kEvictThreads);
+        copy.dynamicSmemBytes = kEvictRing;
+        copy.stream = cfg.stream;
+        cudaLaunchAttribute dep[1];
+        dep[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        dep[0].val.programmaticStreamSerializationAllowed = 1;
+        copy.attrs = dep;
+        copy.numAttrs = 1;
+        e = cudaLaunchKernelEx(&copy, kv_evict_copy_kernel, a, most, units, stream_units);
+        count_launches(1);
+    }
     if (e != cudaSuccess) {
         cudaGetLastError();
         return GBATTN_ERR_CUDA;

@@ -851,7 +851,7 @@ int run_decode(const DecodeCall& c) {
     if (c.B <= 0 || c.Hq <= 0 || c.Hkv <= 0 || c.nq <= 0 || c.num_phys <= 0 || c.ps <= 0 ||
         c.max_pages <= 0 || c.max_kv <= 0)
         return GBATTN_ERR_SHAPE;
-    if (c.Hq % c.Hkv != 0 ||
+    if (c.Hq % c.Hkv != 0 || c.max_kv > (1 << 30) ||
         static_cast<long long>(c.max_kv) > static_cast<long long>(c.max_pages) * c.ps)
         return GBATTN_ERR_SHAPE;
     if (c.diff && c.diff->heads != 1 && c.diff->heads != c.Hq) return GBATTN_ERR_SHAPE;

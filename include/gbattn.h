@@ -315,7 +315,7 @@ int kv_paged_append_f16(const void* k_new, const void* v_new, void* k_pages, voi
  *   weights of a page that several sequences of one call share receive every sequence's addition,
  *   in an order that may change the last bit.
  *   D is 64, 128 or 256; page_size a power of two >= 16; Hq % Hkv == 0; B <= 4096;
- *   max_kv_len <= max_pages * page_size; num_phys_pages * page_size < 2^31.  A length outside
+ *   max_kv_len <= max_pages * page_size, 2^30; num_phys_pages * page_size < 2^31.  A length outside
  *   [0, max_kv_len] sets GBATTN_DEV_BAD_LENGTH and yields O = 0, lse = -inf for that sequence.  An
  *   out-of-range page-table entry sets GBATTN_DEV_BAD_PAGE (that page reads physical page 0, and
  *   its tokens' weights stay as they are).
@@ -354,7 +354,7 @@ int attn_paged_decode_f16_fwd(const void* q, const void* k_pages, const void* v_
  *   of dst_table may be read or written for another purpose by the same call (so shared pages can be
  *   evicted from, into fresh ones).
  *   D is 64, 128 or 256; page_size a power of two >= 16; num_phys_pages * page_size < 2^31;
- *   sink + recent <= budget; max_kv_len <= max_pages * page_size;
+ *   sink + recent <= budget; max_kv_len <= max_pages * page_size, 2^30;
  *   min(budget, max_kv_len) <= dst_pages * page_size.  A sequence whose length is outside
  *   [0, max_kv_len] (GBATTN_DEV_BAD_LENGTH) or with a page that it needs outside
  *   [0, num_phys_pages) (GBATTN_DEV_BAD_PAGE) stays as it is: new_lens[b] = kv_lens[b], kept -1.

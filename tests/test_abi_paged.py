@@ -87,6 +87,7 @@ def test_decode_refusals(lib, diff):
     for n in ("B", "Hq", "Hkv", "nq", "P", "ps", "mp", "max"):
         assert call(**{n: 0}) == SHAPE and call(**{n: -3}) == SHAPE
     assert call(Hq=5) == SHAPE and call(max=65) == SHAPE
+    assert call(mp=1 << 28, max=(1 << 30) + 1) == SHAPE
     for d in (0, 32, 96, 512) + ((64, 256) if diff else ()):
         assert call(D=d) == UNSUPPORTED
     for ps in (8, 24):
