@@ -16,10 +16,10 @@
 //   warp 0      TMA producer: Q once, then K_0, V_0, K_1, V_1, ... through a ring of 32 KB slots.
 //   warp 1      allocates tensor memory and issues S_m = Q_m K_m^T (SMEM x SMEM, 4 MMAs).
 //   warp 10     issues O_m += P_m V (P from TMEM).
-//   warps 2..9  softmax: two threads per query row (TMEM lane = row), one per 64-key half of the tile.
-// Tensor memory (512 columns): S of map 0, S of map 1 (P_m overwrites the first 64 columns of its S
-// as FP16 pairs), O of map 0, O of map 1.  While the softmax works on one map, the tensor core runs
-// PV and the next QK of the other.
+//   warps 2..5, 6..9  softmax of map 0, of map 1: one thread per query row (TMEM lane = row).
+// Tensor memory (512 columns): one S, P of each map (FP16 pairs), O of each map.  S is handed back as
+// soon as the softmax has it in registers, so the other map's QK runs under this one's exponentials,
+// and PV of a tile under the next tile's.
 //
 // Split keys: with fewer query tiles than SMs the key tiles of each are cut into C chunks of their
 // own CTAs, which write unnormalised O_m, max and sum to `workspace`; a merge kernel joins them.
@@ -45,11 +45,12 @@ constexpr int kBN = 128;             // keys per tile (two halves of 64)
 constexpr int kNS = 4;               // K/V ring slots (even: K tiles, odd: V tiles)
 constexpr int kThreads = 352;
 constexpr int kPvWarp = 10;
-constexpr int kSoftmaxThreads = 256;
+constexpr int kSoftmaxThreads = 128;   // per map
 constexpr int kChunk = 128 * 128;    // 128 rows x 64 FP16 columns
 constexpr int kQBytes = kBM * kD * 2;
 constexpr int kSlotBytes = kBN * kD * 2;
-constexpr uint32_t kTO = 256;        // first TMEM column of O of map 0 (map 1: + 128)
+// Tensor memory columns: S, then P of map 0 and of map 1 (FP16 pairs), then O of map 0 and of map 1.
+constexpr uint32_t kTP = 128, kTO = 256;
 constexpr uint32_t kIdescQK = idesc_f16(kBM, kBN, false, false);
 constexpr uint32_t kIdescPV = idesc_f16(kBM, kD, false, true);
 constexpr uint64_t kDrainNs = 200000000ull;   // 0.2 s for draining after an abort
@@ -75,21 +76,22 @@ struct Ctrl {
     uint64_t q_full;
     uint64_t full[kNS];
     uint64_t empty[kNS];
-    uint64_t s_full[2];       // S of a map computed
+    uint64_t s_full[2];       // S of a map's tile computed
+    uint64_t s_free;          // S read into registers (once per step)
     uint64_t p_full[2];       // P of a map written
-    uint64_t pv_done[2];      // PV of a map done: its S buffer is free, its O up to date
+    uint64_t pv_done[2];      // PV of a map done: its P buffer is free, its O up to date
     uint64_t drain;
     uint64_t drain_pv;        // the PV issuer's own drain after an abort
-    uint64_t xchg[4];         // per row quarter: the two half-row threads exchange values
+    uint64_t xchg[4];         // per row quarter: the two threads of a row exchange values
     uint32_t tmem_base;
     int abort;
 };
 
-// Values exchanged between the two threads that share a query row.
+// Values exchanged in the epilogue between the two threads of a query row.
 struct Exchange {
-    float mx[2][2][128];   // [map][column half][row] partial row max
-    float l[2][2][128];    // [map][column half][row] partial row sum (epilogue)
-    float sq[2][128];      // [column half][row] partial sum of squares (epilogue)
+    float mx[2][128];   // [map][row] running max
+    float l[2][128];    // [map][row] row sum
+    float sq[2][128];   // [column half][row] partial sum of squares
 };
 
 constexpr int kCtrlBytes = 256 + static_cast<int>(sizeof(Exchange));
@@ -165,6 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctrl->p_full[i], kSoftmaxThreads);
             mbar_init(&ctrl->pv_done[i], 1);
         }
+        mbar_init(&ctrl->s_free, kSoftmaxThreads);
         for (int i = 0; i < 4; ++i) mbar_init(&ctrl->xchg[i], 64);
         mbar_init(&ctrl->drain, 1);
         mbar_init(&ctrl->drain_pv, 1);
@@ -230,10 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 1) {
-        // ================= QK issuer.  QK of tile t and map m overwrites the S buffer
-        // that PV of tile t - 1 read P from, so it waits for that PV.  K_t sits at
-        // ring position 2 t; the previous item of its slot, K_{t - 2}, was waited for
-        // by this warp.
+        // ================= QK issuer.  A step's QK overwrites the S that the step before
+        // it left, as soon as the softmax has that in registers.  K_t sits at ring
+        // position 2 t; the previous item of its slot, K_{t - 2}, was waited for by
+        // this warp.
         if (n_tiles > 0) {
             bool ok = wait_warp(&ctrl->q_full, 0, w);
             const uint32_t qa = smem_addr(sQ);
@@ -241,7 +244,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int slot = (2 * t) % kNS;
                 const uint32_t ka = smem_addr(sKV + slot * kSlotBytes);
                 for (int m = 0; m < 2; ++m) {
-                    if (t > 0) ok = wait_warp(&ctrl->pv_done[m], (t - 1) & 1, w);
+                    const int s = 2 * t + m;
+                    if (s > 0) ok = wait_warp(&ctrl->s_free, (s - 1) & 1, w);
                     if (m == 0) ok = ok && wait_warp(&ctrl->full[slot], (2 * t / kNS) & 1, w);
                     if (!ok) break;
                     tc_fence_after();
@@ -249,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k16 = 0; k16 < 4; ++k16) {
                             const uint32_t off = m * kChunk + k16 * 32;
-                            mma_ss(tmem + m * 128, sdesc_sw128(qa + off, 16, 1024),
+                            mma_ss(tmem, sdesc_sw128(qa + off, 16, 1024),
                                    sdesc_sw128(ka + off, 16, 1024), kIdescQK, k16 > 0 ? 1u : 0u);
                         }
                         mma_commit(&ctrl->s_full[m]);
@@ -292,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (elect_one()) {
 #pragma unroll
                         for (int k16 = 0; k16 < kBN / 16; ++k16)
-                            mma_ts(tmem + kTO + m * 128, tmem + m * 128 + k16 * 8,
+                            mma_ts(tmem + kTO + m * 128, tmem + kTP + m * 64 + k16 * 8,
                                    sdesc_sw128(va + k16 * 2048, kChunk, 1024), kIdescPV,
                                    (t > 0 || k16 > 0) ? 1u : 0u);
                         if (m == 1) mma_commit(&ctrl->empty[slot]);
@@ -308,62 +312,52 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else {
-        // ================= softmax / correction / epilogue (warps 2..9)
-        // Two threads share each query row: warps 2..5 own key columns 0..63 of
-        // every tile, warps 6..9 columns 64..127 (TMEM lane quarter = warp % 4).
-        // They exchange their partial row max each step (and the row sums at the
-        // end) through shared memory, ordered by the per-quarter xchg mbarrier.
+        // ================= softmax / correction / epilogue (warps 2..5 map 0, 6..9 map 1)
+        // A thread owns one query row of one map (TMEM lane quarter = warp % 4), so nothing is
+        // exchanged until the epilogue and the two maps' warps run out of step: while one map's
+        // are in their exponentials, the other's load scores or wait for the tensor core.
         const int quarter = warp & 3;
-        const int half = (warp - 2) >> 2;
+        const int m = (warp - 2) >> 2;
         const int row = quarter * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t pbuf = tl + kTP + m * 64, obuf = tl + kTO + m * 128;
         const int row_g = q_row0 + row;
         uint64_t* xbar = &ctrl->xchg[quarter];
         const int lim = visible(n, row_g, a.causal);   // keys >= lim are invisible
         const float sl2 = a.scale_log2;
         const uint64_t sl2x2 = f2_pack(sl2, sl2);
-        // running max and sum of the step's map, and of the other map
-        float m_run = -INFINITY, l = 0.0f, m_other = -INFINITY, l_other = 0.0f;
-        uint32_t xphase = 0;
+        float m_run = -INFINITY, l = 0.0f;
         bool ok = true;
-        for (int s = 0; s < 2 * n_tiles; ++s) {
-            const int t = s >> 1, m = s & 1;
-            const uint32_t sbuf = tl + m * 128;
+        for (int t = 0; t < n_tiles; ++t) {
             ok = wait_warp(&ctrl->s_full[m], t & 1, w);
             if (!ok) break;
             tc_fence_after();
-            uint32_t x[64];
-            tmem_ld32(sbuf + half * 64, x);
-            tmem_ld32(sbuf + half * 64 + 32, x + 32);
-            tmem_ld_wait();
-
-            const int kh = (tile0 + t) * kBN + half * 64;
-            if (kh + 64 > lim) {   // keys the row does not see
+            uint32_t x[kBN];
 #pragma unroll
-                for (int c = 0; c < 64; ++c)
-                    if (kh + c >= lim) x[c] = __float_as_uint(-INFINITY);
+            for (int c = 0; c < kBN; c += 32) tmem_ld32(tl + c, x + c);
+            tmem_ld_wait();
+            tc_fence_before();
+            mbar_arrive(&ctrl->s_free);
+
+            const int k0 = (tile0 + t) * kBN;
+            if (k0 + kBN > lim) {   // keys the row does not see
+#pragma unroll
+                for (int c = 0; c < kBN; ++c)
+                    if (k0 + c >= lim) x[c] = __float_as_uint(-INFINITY);
             }
-            // row max of the 64 values with four independent chains (short latency)
+            // row max with four independent chains (short latency)
             float m4[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) m4[k] = __uint_as_float(x[k]);
 #pragma unroll
-            for (int c = 4; c < 60; c += 8) {
+            for (int c = 4; c < 124; c += 8) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     m4[k] = max3f(m4[k], __uint_as_float(x[c + k]), __uint_as_float(x[c + 4 + k]));
             }
-            m4[0] = max3f(m4[0], __uint_as_float(x[60]), __uint_as_float(x[61]));
-            m4[1] = max3f(m4[1], __uint_as_float(x[62]), __uint_as_float(x[63]));
-            const float pm = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
-            ex->mx[m][half][row] = pm;
-            tc_fence_before();   // our S loads are ordered before the partner's P stores
-            mbar_arrive(xbar);
-            ok = wait_warp(xbar, xphase, w);
-            xphase ^= 1u;
-            if (!ok) break;
-            tc_fence_after();
-            const float mx = fmaxf(pm, ex->mx[m][half ^ 1][row]);
+            m4[0] = max3f(m4[0], __uint_as_float(x[124]), __uint_as_float(x[125]));
+            m4[1] = max3f(m4[1], __uint_as_float(x[126]), __uint_as_float(x[127]));
+            const float mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
             const float m_new = fmaxf(m_run, mx * sl2);
             const bool need = m_new > m_run + 8.0f;
             float alpha = 1.0f;
@@ -374,19 +368,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool warp_need = __any_sync(0xffffffffu, need);
             const float m_use = m_run == -INFINITY ? 0.0f : m_run;
             const uint64_t negm = f2_pack(-m_use, -m_use);
+            if (t > 0) {   // the P buffer is free and O complete up to the last tile
+                ok = wait_warp(&ctrl->pv_done[m], (t - 1) & 1, w);
+                if (!ok) break;
+                tc_fence_after();
+            }
             uint64_t rs[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) rs[k] = f2_pack(0.0f, 0.0f);
-            uint32_t p2[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-                float x0, x1;
-                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
-                                 sl2x2, negm),
-                          x0, x1);
-                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                rs[i & 3] = f2_add(rs[i & 3], f2_pack(p0, p1));   // four independent sums
-                p2[i] = pack_half2(p0, p1);
+            for (int c = 0; c < kBN; c += 32) {
+                uint32_t p2[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float x0, x1;
+                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c + 2 * i]),
+                                             __uint_as_float(x[c + 2 * i + 1])),
+                                     sl2x2, negm),
+                              x0, x1);
+                    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                    rs[i & 3] = f2_add(rs[i & 3], f2_pack(p0, p1));   // four independent sums
+                    p2[i] = pack_half2(p0, p1);
+                }
+                tmem_st16(pbuf + c / 2, p2);
             }
             float r0, r1, r2, r3, r4, r5, r6, r7;
             f2_unpack(rs[0], r0, r1);
@@ -394,20 +398,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             f2_unpack(rs[2], r4, r5);
             f2_unpack(rs[3], r6, r7);
             l = l * alpha + (((r0 + r1) + (r2 + r3)) + ((r4 + r5) + (r6 + r7)));
-            // P over the first 64 columns of its S buffer; both threads of the
-            // row have loaded their S halves (they passed the exchange above).
-            tmem_st32(sbuf + half * 32, p2);
             tmem_st_wait();
-            if (warp_need && t > 0) {   // rescale this thread's half of O after the last PV
-                ok = wait_warp(&ctrl->pv_done[m], (t - 1) & 1, w);
-                if (!ok) break;
-                tc_fence_after();
+            if (warp_need && t > 0) {   // rescale the row of O
                 const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll 1
-                for (int cc = 0; cc < 2; ++cc) {
-                    const uint32_t col = tl + kTO + m * 128 + half * 64 + cc * 32;
+                for (int cc = 0; cc < 4; ++cc) {
                     uint32_t o[32];
-                    tmem_ld32(col, o);
+                    tmem_ld32(obuf + cc * 32, o);
                     tmem_ld_wait();
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -417,35 +414,32 @@ __global__ void __launch_bounds__(kThreads, 1)
                         o[2 * e] = __float_as_uint(y0);
                         o[2 * e + 1] = __float_as_uint(y1);
                     }
-                    tmem_st32(col, o);
+                    tmem_st32(obuf + cc * 32, o);
                 }
                 tmem_st_wait();
             }
             tc_fence_before();
             mbar_arrive(&ctrl->p_full[m]);
-            float swap = m_run;
-            m_run = m_other;
-            m_other = swap;
-            swap = l;
-            l = l_other;
-            l_other = swap;
         }
         if (ok && n_tiles > 0) {
             ok = wait_warp(&ctrl->pv_done[0], (n_tiles - 1) & 1, w) &&
                  wait_warp(&ctrl->pv_done[1], (n_tiles - 1) & 1, w);
             tc_fence_after();
         }
-        float l2[2] = {l, l_other};   // an even number of steps: map 0 is current again
-        const float mr[2] = {m_run, m_other};
-        if (ok) {   // combine the partial row sums
-            ex->l[0][half][row] = l2[0];
-            ex->l[1][half][row] = l2[1];
+        // From here a thread works on half of the columns of both maps.
+        const int half = m;
+        uint32_t xphase = 0;
+        float l2[2] = {0.0f, 0.0f}, mr[2] = {-INFINITY, -INFINITY};
+        if (ok) {
+            ex->mx[m][row] = m_run;
+            ex->l[m][row] = l;
             mbar_arrive(xbar);
             ok = wait_warp(xbar, xphase, w);
             xphase ^= 1u;
-            if (ok) {
-                l2[0] += ex->l[0][half ^ 1][row];
-                l2[1] += ex->l[1][half ^ 1][row];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                l2[k] = ex->l[k][row];
+                mr[k] = ex->mx[k][row];
             }
         }
         const bool row_ok = row_g < a.Sq;
@@ -474,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float lambda = diff_lambda(a.diff, head, kD / 2, lane);
             const float f0 = l2[0] == 0.0f ? 0.0f : 1.0f / l2[0];
             const float f1 = l2[1] == 0.0f ? 0.0f : -lambda / l2[1];
-            float y[64];
+            float y[64];   // this thread's columns
             float sq = 0.0f;
 #pragma unroll
             for (int cc = 0; cc < 2; ++cc) {
