@@ -36,16 +36,23 @@ __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t* bar, uint32_t by
                  "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
+// Arrive on and test a barrier given by its shared-memory address.
+__device__ __forceinline__ void mbar_arrive(uint32_t addr) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait(uint32_t addr, uint32_t parity) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
         "selp.u32 %0, 1, 0, p;\n\t}"
         : "=r"(ok)
-        : "r"(smem_addr(bar)), "r"(parity)
+        : "r"(addr), "r"(parity)
         : "memory");
     return ok != 0;
+}
+__device__ __forceinline__ bool mbar_try_wait(uint64_t* bar, uint32_t parity) {
+    return mbar_try_wait(smem_addr(bar), parity);
 }
 
 // Shared state for bounded waits: a time limit, the device status word and a
@@ -81,8 +88,10 @@ __device__ __forceinline__ bool wait_one(uint64_t* bar, uint32_t parity, const W
 }
 
 // Whole-warp wait with a warp-uniform result (every lane polls the barrier; the
-// warp proceeds once all lanes have seen the phase complete).
-__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, const WaitCtl& w) {
+// warp proceeds once all lanes have seen the phase complete).  The barrier is given
+// by a pointer or by its shared-memory address.
+template <typename Bar>
+__device__ __forceinline__ bool wait_warp(Bar bar, uint32_t parity, const WaitCtl& w) {
     const uint32_t lane = threadIdx.x & 31u;
     uint64_t t0 = 0;
     for (uint32_t it = 0;; ++it) {
@@ -283,6 +292,12 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t* r) {
         "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
         "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
         GBATTN_W8(0), GBATTN_W8(8), GBATTN_W8(16), GBATTN_W8(24)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+        GBATTN_W8(0)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {

@@ -403,9 +403,10 @@ int attn_diff_paged_decode_f16_fwd(const void* q, const void* k_pages, const voi
  *   Query head h reads KV head h / (Hq / Hkv).  D == 128; B*Hq <= 65535; Sq <= 2^22, Skv <= 2^30.
  *   A length outside [0, Sq] or [0, Skv] sets GBATTN_DEV_BAD_LENGTH and leaves that batch entry
  *   without queries (O = 0, lse = -inf).
- *   With few query rows the keys are split into chunks whose FP32 partial results go to `workspace`
- *   (32-byte aligned) and are merged; a workspace smaller than attn_diff_prefill_workspace_size()
- *   makes the call use fewer chunks, NULL with 0 bytes one.
+ *   With few query tiles against many keys the key ranges are split evenly over the SMs, the parts'
+ *   FP32 results go to `workspace` (32-byte aligned) and are merged.
+ *   attn_diff_prefill_workspace_size() is 0 where that does not pay; with a smaller workspace, or
+ *   NULL and 0 bytes, every query tile is one CTA's work.
  */
 size_t attn_diff_prefill_workspace_size(int B, int Hq, int Sq, int Skv, int D);
 int attn_diff_prefill_fwd(const void* q, const void* k, const void* v, const float* lambda_vecs,

@@ -100,7 +100,7 @@ def test_diff_prompt_padded_batch(gb, causal):
 
 
 def test_diff_prompt_split_keys(gb):
-    """Few rows against many keys: with the full workspace, with less, and with none."""
+    """Few rows against many keys: with the full workspace, and with too little to split."""
     case = prompt(1, 2, 1, 70, 5000, 65, std=2.0)
     n = gb.attn_diff_prefill_workspace_size(1, 2, 70, 5000, D)
     assert n > 0
@@ -149,7 +149,7 @@ def test_diff_prompt_bad_length_and_lost_load(gb):
     try:
         for mode in (1, 2):
             gb.test_inject_fault(mode)
-            # one chunk (no workspace to split into): mode 2 stops after 8 of its 32 K/V tiles
+            # no workspace to split into: mode 2 stops after 8 of the one CTA's 32 K/V tiles
             gb.attn_diff_prefill_fwd(*(t(x) for x in prompt(1, 1, 1, 128, 2048, 71)), t(vecs), 0.5,
                                      workspace=torch.empty(16, dtype=torch.uint8, device=DEV))
             assert gb.device_status() & gb.DEV_WAIT_TIMEOUT
