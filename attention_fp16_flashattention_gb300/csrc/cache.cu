@@ -437,25 +437,43 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_select_kernel(const
     cluster.sync();   // nobody leaves while another CTA adds to or reads its shared memory
 }
 
-__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_copy_kernel(const EvictArgs a, int most,
-                                                                         long long units,
-                                                                         int stream_units) {
+// Unit u is step u % steps of head u / steps (heads counted over the sequences); a CTA takes every
+// grid-th.  It moves on by adding the grid's own (sequence, head, step), with carries: a division per
+// step and thread cost more than the copy.
+struct CopyPlan {
+    int most, steps;              // rows of a head at most, steps of a head
+    long long units;
+    int d_b, d_h, d_step;         // the grid size as sequences, heads and steps
+};
+
+__global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_copy_kernel(const EvictArgs a,
+                                                                         const CopyPlan plan) {
     extern __shared__ __align__(16) uint32_t s_dyn[];
     const int tid = threadIdx.x;
     EvictRing ring(s_dyn, a, tid);
-    // Unit u is step u % stream_units of head u / stream_units; this CTA takes every grid-th.
     struct Row {
         int b, h, j, t;   // t: old slot, -1 for no row
     };
-    auto old_row = [&](int k) -> Row {
-        Row x{0, 0, 0, -1};
-        const long long u = blockIdx.x + static_cast<long long>(k) * gridDim.x;
-        if (u >= units) return x;
-        const int stream = static_cast<int>(u / stream_units);
-        x.b = stream / a.Hkv;
-        x.h = stream - x.b * a.Hkv;
-        x.j = static_cast<int>(u - static_cast<long long>(stream) * stream_units) * ring.rows + ring.row;
-        if (x.j < most) x.t = a.kept[static_cast<long long>(stream) * a.budget + x.j];
+    const long long mine = (plan.units - blockIdx.x + gridDim.x - 1) / gridDim.x;
+    const int stream0 = static_cast<int>(blockIdx.x / plan.steps);
+    int step = static_cast<int>(blockIdx.x) - stream0 * plan.steps;
+    int b = stream0 / a.Hkv, h = stream0 - b * a.Hkv, drawn = 0;
+    auto next_row = [&]() -> Row {   // this thread's row of the CTA's next unit
+        Row x{b, h, step * ring.rows + ring.row, -1};
+        if (drawn < mine && x.j < plan.most)
+            x.t = a.kept[(static_cast<long long>(b) * a.Hkv + h) * a.budget + x.j];
+        ++drawn;
+        step += plan.d_step;
+        h += plan.d_h;
+        if (step >= plan.steps) {
+            step -= plan.steps;
+            ++h;
+        }
+        b += plan.d_b;
+        if (h >= a.Hkv) {
+            h -= a.Hkv;
+            ++b;
+        }
         return x;
     };
     // source and destination page of a row
@@ -464,17 +482,16 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_copy_kernel(const E
         return make_int2(a.table[static_cast<long long>(x.b) * a.max_pages + (x.t >> a.page_bits)],
                          a.dst_table[static_cast<long long>(x.b) * a.dst_pages + (x.j >> a.page_bits)]);
     };
-    const long long mine = (units - blockIdx.x + gridDim.x - 1) / gridDim.x;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // The index chain (kept slot, then pages) runs two steps ahead of the copies, the copies
     // kEvictStages - 1 steps ahead of the stores.
-    Row x0 = old_row(0), x1 = old_row(1);
+    Row x0 = next_row(), x1 = next_row();
     int2 p0 = pages_of(x0);
     // destination page (-1: no row), slot and head of the rows in flight
     __shared__ int s_page[kEvictStages][kEvictThreads / 4];
     __shared__ int2 s_to[kEvictStages][kEvictThreads / 4];
     auto advance = [&](int k) {
-        const Row x2 = old_row(k + 2);
+        const Row x2 = next_row();
         const int2 p1 = pages_of(x1);
         if (ring.c == 0) {   // read back by the row's threads, all of one warp
             s_page[k % kEvictStages][ring.row] = x0.t < 0 ? -1 : p0.y;
@@ -692,10 +709,16 @@ extern "C" int kv_paged_evict(void* k_pages, void* v_pages, float* weights,
     count_launches(1);
     if (e == cudaSuccess && !in_place) {
         // Its CTAs may be placed as the selection's leave; they wait for all of it.
-        const int stream_units = (most + (kEvictThreads >> bits) - 1) / (kEvictThreads >> bits);
-        const long long units = streams * stream_units;
+        CopyPlan plan{};
+        plan.most = most;
+        plan.steps = (most + (kEvictThreads >> bits) - 1) / (kEvictThreads >> bits);
+        plan.units = streams * plan.steps;
+        const int grid = static_cast<int>(plan.units < 2LL * dev.num_sms ? plan.units : 2LL * dev.num_sms);
+        plan.d_step = grid % plan.steps;
+        plan.d_h = grid / plan.steps % Hkv;
+        plan.d_b = grid / plan.steps / Hkv;
         cudaLaunchConfig_t copy{};
-        copy.gridDim = dim3(static_cast<unsigned>(units < 2LL * dev.num_sms ? units : 2LL * dev.num_sms));
+        copy.gridDim = dim3(static_cast<unsigned>(grid));
         copy.blockDim = dim3(kEvictThreads);
         copy.dynamicSmemBytes = kEvictRing;
         copy.stream = cfg.stream;
@@ -704,7 +727,7 @@ extern "C" int kv_paged_evict(void* k_pages, void* v_pages, float* weights,
         dep[0].val.programmaticStreamSerializationAllowed = 1;
         copy.attrs = dep;
         copy.numAttrs = 1;
-        e = cudaLaunchKernelEx(&copy, kv_evict_copy_kernel, a, most, units, stream_units);
+        e = cudaLaunchKernelEx(&copy, kv_evict_copy_kernel, a, plan);
         count_launches(1);
     }
     if (e != cudaSuccess) {
