@@ -138,6 +138,37 @@ def test_diff_prompt_strided_views(gb):
     assert torch.equal(o, want)
 
 
+def test_diff_prompt_many_query_tiles(gb):
+    """More query tiles than SMs: several rounds of whole tiles, ragged lengths, empty entries and
+    rows without keys among them."""
+    q, k, v = prompt(5, 8, 4, 900, 950, 74)
+    check_prompt(gb, q, k, v, q_lens=[900, 513, 0, 1, 700], kv_lens=[950, 400, 30, 0, 700])
+    check_prompt(gb, q[:, :, :640], k, v, causal=False)
+
+
+@pytest.mark.parametrize("split", [True, False])
+def test_diff_prompt_in_a_graph_and_on_a_side_stream(gb, split):
+    q, k, v = prompt(2, 2, 1, 100, 6000 if split else 200, 75)
+    vecs, weight = inputs.diff_inputs(2, D, 76)
+    assert (gb.attn_diff_prefill_workspace_size(2, 2, 100, k.shape[2], D) > 0) == split
+    args = [t(x) for x in (q, k, v, vecs)]
+    weight, lens = t(weight), t(np.array([k.shape[2], 150], dtype=np.int32))
+    call = lambda **kw: gb.attn_diff_prefill_fwd(*args, 0.4, norm_weight=weight, kv_lens=lens, **kw)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    want = call()
+    torch.cuda.synchronize()
+    got = call(stream=side)
+    side.synchronize()
+    assert torch.equal(got, want)
+    with torch.cuda.graph(graph):
+        o = call()
+    lens.copy_(t(np.array([77, k.shape[2]], dtype=np.int32)))
+    graph.replay()
+    torch.cuda.synchronize()
+    got = o.clone()
+    assert torch.equal(got, call()) and not torch.equal(got, want) and gb.device_status() == 0
+
+
 def test_diff_prompt_bad_length_and_lost_load(gb):
     q, k, v = prompt(2, 1, 1, 100, 100, 70)
     vecs, _ = inputs.diff_inputs(1, D, 61)

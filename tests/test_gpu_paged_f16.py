@@ -153,6 +153,22 @@ def test_decode_many_and_long_sequences(gb):
     check_decode(gb, *inputs.paged_f16_inputs(3, 4, 1, 1, (70001, 3, 50), 128, 15, page_size=128))
 
 
+@pytest.mark.parametrize("Hq,Hkv,nq", [(3, 3, 1), (9, 1, 1), (16, 2, 2), (20, 1, 2), (6, 2, 4)])
+@pytest.mark.parametrize("D", [64, 256])
+def test_decode_weights_over_row_groups(gb, Hq, Hkv, nq, D):
+    """Weights summed over one row, one and several row groups; rows that see nothing add none."""
+    case = inputs.paged_f16_inputs(4, Hq, Hkv, nq, (530, nq - 1, 33, 0), D, 22, page_size=16,
+                                   spare_pages=1, poison=True)
+    check_decode(gb, *case)
+
+
+def test_decode_most_sequences(gb):
+    """4096 sequences, the most a call takes, some of them empty, with the narrow and the wide CTA."""
+    lens = tuple(int(x) for x in np.random.default_rng(23).integers(0, 5, 4096))
+    for D in (64, 256):
+        check_decode(gb, *inputs.paged_f16_inputs(4096, 1, 1, 1, lens, D, 23, page_size=16))
+
+
 def test_decode_smaller_workspace_and_refusals(gb):
     case = inputs.paged_f16_inputs(2, 8, 2, 1, (3000, 700), 128, 16)
     full = gb.attn_paged_decode_f16_workspace_size(2, 8, 2, 1, 3008, 128, True)
@@ -322,6 +338,56 @@ def test_evict_bad_sequences_stay(gb):
     assert torch.all(kept[:3] == -1) and np.array_equal(kept[3:].cpu().numpy(), rkept)
     assert np.array_equal(gk.cpu().numpy(), rk) and np.array_equal(gv.cpu().numpy(), rv)
     assert np.array_equal(gw.cpu().numpy(), rw)
+
+
+def captured(call):
+    """`call` captured into a graph and replayed once."""
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call()
+    graph.replay()
+    torch.cuda.synchronize()
+    return out
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+def test_append_and_evict_in_graphs_and_on_a_side_stream(gb, in_place):
+    """The same bits captured and replayed, and on a stream of its own, as called directly."""
+    B, Hkv, D, ps, budget = 3, 2, 128, 16, 100
+    _, kp, vp, table, lens, w = inputs.paged_f16_inputs(B, Hkv, Hkv, 1, (300, 90, 150), D, 34,
+                                                        page_size=ps, spare_pages=B * 7)
+    free = np.setdiff1d(np.arange(kp.shape[0]), table[table >= 0]).astype(np.int32)
+    dst = None if in_place else t(free.reshape(B, 7))
+    kn = np.random.default_rng(34).standard_normal((B, Hkv, 5, D)).astype(np.float16)
+    tk, tt, tl = t(kn), t(table), t(lens)
+    side, results = torch.cuda.Stream(), []
+    for how in ("direct", "graph", "side"):
+        gk, gv, gw = t(kp), t(vp), t(w)
+
+        def step(stream=None):
+            gb.kv_paged_append_f16(tk, tk, gk, gv, tt, tl, weights=gw, stream=stream)
+            return gb.kv_paged_evict(gk, gv, gw, tt, tl, budget, sink=3, recent=20, dst_table=dst,
+                                     stream=stream)
+        torch.cuda.synchronize()
+        out = captured(step) if how == "graph" else step(side if how == "side" else None)
+        torch.cuda.synchronize()
+        results.append([x.clone() for x in (gk, gv, gw) + tuple(out)])
+    assert gb.device_status() == 0
+    for other in results[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(results[0], other))
+
+
+def test_evict_the_same_cache_twice(gb):
+    """A second eviction right behind the first on the stream, on the lengths that the first wrote."""
+    _, kp, vp, table, lens, w = inputs.paged_f16_inputs(2, 2, 2, 1, (400, 310), 64, 35, page_size=16)
+    gk, gv, gw, tt = t(kp), t(vp), t(w), t(table)
+    l1, _ = gb.kv_paged_evict(gk, gv, gw, tt, t(lens), 200, sink=2, recent=30)
+    l2, kept = gb.kv_paged_evict(gk, gv, gw, tt, l1, 77, sink=2, recent=30)
+    k1, v1, w1, n1, _ = OP.evict(kp, vp, w, table, table, lens, 200, 2, 30)
+    k2, v2, w2, n2, rkept = OP.evict(k1, v1, w1, table, table, n1, 77, 2, 30)
+    assert np.array_equal(l2.cpu().numpy(), n2) and np.array_equal(kept.cpu().numpy(), rkept)
+    assert np.array_equal(gk.cpu().numpy(), k2) and np.array_equal(gv.cpu().numpy(), v2)
+    assert np.array_equal(gw.cpu().numpy(), w2) and gb.device_status() == 0
 
 
 # ---------------------------------------------------------------- together
