@@ -711,13 +711,15 @@ __global__ void __launch_bounds__(256, 3) decode_f16_weights_kernel(const Weight
                 float s[kTiles];
                 float2 m[kTiles];
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j) {
+                for (int j = 0; j < kTiles; ++j) {   // group 0's scores need not wait for info
+                    const uint32_t u = u0 + j * step;
                     s[j] = -INFINITY;
-                    if (tok >= info[j].w) continue;
-                    const long long u = u0 + j * step + static_cast<long long>(rg) * info[j].z;
-                    s[j] = a.scores[(u * a.pitch + r) * kTile + tok];
-                    m[j] = a.row_ml[static_cast<long long>(info[j].y) * a.G + rg * a.R + r];
+                    if (rg == 0 ? u < U : tok < info[j].w)
+                        s[j] = a.scores[((u + static_cast<long long>(rg) * info[j].z) * a.pitch + r) * kTile + tok];
                 }
+#pragma unroll
+                for (int j = 0; j < kTiles; ++j)
+                    m[j] = a.row_ml[static_cast<long long>(info[j].y) * a.G + rg * a.R + r];
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j)
                     if (s[j] != -INFINITY) sum[j] += fast_exp2(s[j] - m[j].x) * m[j].y;
