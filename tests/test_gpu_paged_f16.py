@@ -162,6 +162,28 @@ def test_decode_weights_over_row_groups(gb, Hq, Hkv, nq, D):
     check_decode(gb, *case)
 
 
+@pytest.mark.parametrize("Hq,D", [(32, 128), (20, 64), (64, 256), (100, 64)])
+def test_decode_row_groups_side_by_side(gb, Hq, D):
+    """A length bound above 256 MB of cache, where 2, 4 or 8 row groups share a CTA's tiles."""
+    q, kp, vp, table, lens, w = inputs.paged_f16_inputs(3, Hq, 1, 1, (2100, 40, 700), D, 24,
+                                                        page_size=64, poison=True)
+    wide = np.zeros((3, 1 << 16), dtype=np.int32)       # 4M tokens of bound, the rest not in use
+    wide[:, :table.shape[1]] = table
+    case = (q, kp, vp, wide, lens)
+    check_decode(gb, *case)
+    lse = torch.empty((3, Hq, 1), device=DEV)
+    n = gb.attn_paged_decode_f16_workspace_size(3, Hq, 1, 1, 400000, D, True)
+    tw = t(w)
+    o = gb.attn_paged_decode_f16_fwd(*(t(x) for x in case), max_kv_len=400000, lse=lse, weights=tw,
+                                     workspace=torch.empty(n, dtype=torch.uint8, device=DEV))
+    narrow = t(w)
+    want = gb.attn_paged_decode_f16_fwd(*(t(x) for x in (q, kp, vp, table, lens)), weights=narrow)
+    assert gb.device_status() == 0
+    assert (o.float() - want.float()).abs().max().item() <= 2.0 ** -10    # other joins, same bounds
+    assert torch.allclose(tw, narrow, rtol=1e-5, atol=1e-6)
+    check_decode(gb, *case, w=w, max_kv=400000)
+
+
 def test_decode_most_sequences(gb):
     """4096 sequences, the most a call takes, some of them empty, with the narrow and the wide CTA."""
     lens = tuple(int(x) for x in np.random.default_rng(23).integers(0, 5, 4096))
