@@ -280,6 +280,36 @@ def test_decode_abandoned_load_is_reported(gb):
     check_decode(gb, *case)
 
 
+def test_abandoned_loads_with_weights_touch_no_other_weight(gb):
+    """A decode that gives up describes none of its tiles as live, whatever its workspace held: no
+    weight outside the sequences' slots moves, and the next call is right again."""
+    lens = (40000, 17)   # far more tiles than a warp fetches pages for in advance
+    q, kp, vp, table, lens, w = inputs.paged_f16_inputs(2, 4, 1, 1, lens, 64, 26, spare_pages=40)
+    held = np.zeros(w.shape, dtype=bool)
+    for b, n in enumerate(lens):
+        at = np.arange(n)
+        held[table[b, at // 32], :, at % 32] = True
+    # one CTA's worth of workspace (a record: 8 rows of 64 values, a max and a sum), so that every
+    # warp's range is long
+    full = gb.attn_paged_decode_f16_workspace_size(2, 4, 1, 1, table.shape[1] * 32, 64, True)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    ws = torch.empty(full - (sms - 1) * 8 * (64 * 4 + 8), dtype=torch.uint8, device=DEV)
+    gb.set_wait_limit_ns(20_000_000)
+    try:
+        for mode in (1, 2):
+            gb.test_inject_fault(mode)
+            gw = t(w)
+            ws.fill_(255)
+            gb.attn_paged_decode_f16_fwd(t(q), t(kp), t(vp), t(table), t(lens), weights=gw,
+                                         workspace=ws)
+            assert gb.device_status() & gb.DEV_WAIT_TIMEOUT
+            assert np.array_equal(gw.cpu().numpy()[~held], w[~held])
+    finally:
+        gb.test_inject_fault(0)
+        gb.set_wait_limit_ns(1_000_000_000)
+    check_decode(gb, q, kp, vp, table, lens, w, workspace=ws)
+
+
 # ---------------------------------------------------------------- eviction
 
 def run_evict(gb, lens, budget, sink=0, recent=0, Hkv=2, D=64, ps=16, in_place=True, seed=31,
