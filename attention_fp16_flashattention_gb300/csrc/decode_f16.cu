@@ -519,6 +519,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 for (uint32_t p = p0; p < p1; ++p) {
                     const uint32_t wi = (p << a.side_bits) + i;
                     const float2 ml = s_ml[wi][r];
+                    if (ml.y == 0.0f) continue;   // saw nothing: O may hold 0 times a cached infinity
                     const float wt = record_weight(ml, M);
                     const float4 v =
                         *reinterpret_cast<const float4*>(all + wi * kRingFloats + r * kPitch + d);
@@ -641,6 +642,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
         mx = M;
 #pragma unroll
         for (int j = 0; j < kBatch; ++j) {
+            if (ml[j].y == 0.0f) continue;   // saw nothing (or past the last record)
             const float wt = record_weight(ml[j], M);
 #pragma unroll
             for (int e = 0; e < V; ++e) acc[e] += wt * v[j][e];

@@ -83,8 +83,10 @@ enum gbattn_device_flag {
                                      that page's tokens were written as zeros */
     GBATTN_DEV_BAD_INDEX = 4u,    /* a VSA cube list was not strictly ascending or held an
                                      index outside [0, S/block); the entry was skipped */
-    GBATTN_DEV_BAD_LENGTH = 8u    /* a decode sequence length was outside [nq, max_kv_len];
-                                     that sequence's rows were written as O = 0, lse = -inf */
+    GBATTN_DEV_BAD_LENGTH = 8u    /* a sequence length was outside the range that the call states
+                                     (the E4M3 decode: [nq, max_kv_len]); attention wrote that
+                                     sequence's rows as O = 0, lse = -inf, an append or an
+                                     eviction left it as it was */
 };
 
 /* Flags of the causal prefill calls. */
@@ -311,7 +313,10 @@ int kv_paged_append_f16(const void* k_new, const void* v_new, void* k_pages, voi
  *   position; one that sees none (kv_lens[b] < nq) gets O = 0, lse = -inf.  Query head h reads KV
  *   head h / (Hq / Hkv).  Scores, softmax and accumulation are FP32 (probabilities enter the PV
  *   product as FP16 hi + lo halves), O is rounded to FP16 once.
- *   Slots of a page at or past kv_lens[b] may hold anything.  Sequences may share pages; the
+ *   Slots of a page at or past kv_lens[b] may hold anything.  A cached value within kv_lens[b] that is
+ *   infinite or NaN makes that column of the queries that see it infinite or NaN (an infinite one too:
+ *   P is a sum of two halves, of which one may be zero or negative); it may also reach queries of the
+ *   call before its token (nq > 1), unless they see no token at all.  Sequences may share pages; the
  *   weights of a page that several sequences of one call share receive every sequence's addition,
  *   in an order that may change the last bit.
  *   D is 64, 128 or 256; page_size a power of two >= 16; Hq % Hkv == 0; B <= 4096;
@@ -323,7 +328,8 @@ int kv_paged_append_f16(const void* k_new, const void* v_new, void* k_pages, voi
  *   workspace rules are the same: attn_paged_decode_f16_workspace_size() gives the full-speed size
  *   (weights != 0 adds about one FP32 score per query row and cached token, for max_kv_len tokens of
  *   every sequence), a smaller one runs fewer warps, and below one CTA's worth the call returns
- *   GBATTN_ERR_WORKSPACE.
+ *   GBATTN_ERR_WORKSPACE.  The workspace needs no initial value; calls that may run at the same
+ *   time (two streams, concurrent graph launches) need separate ones.
  */
 size_t attn_paged_decode_f16_workspace_size(int B, int Hq, int Hkv, int nq, int max_kv_len, int D,
                                             int weights);
@@ -398,6 +404,8 @@ int attn_diff_paged_decode_f16_fwd(const void* q, const void* k_pages, const voi
  *          exist (what lies behind them may be anything); query i < q_lens[b] sits at position
  *          kv_lens[b] - q_lens[b] + i and sees the keys up to it (causal = 1) or all of them
  *          (causal = 0).  Rows that see nothing, and rows i >= q_lens[b], get O = 0, lse = -inf.
+ *          An infinite or NaN value of an existing key may also reach queries before it, unless they
+ *          see no key at all.
  *   lse  : optional dense [B][Hq][2][Sq] FP32, of the two maps
  *   scale: finite, > 0 (typically 1/sqrt(D/2))
  *   Query head h reads KV head h / (Hq / Hkv).  D == 128; B*Hq <= 65535; Sq <= 2^22, Skv <= 2^30.
@@ -406,7 +414,8 @@ int attn_diff_paged_decode_f16_fwd(const void* q, const void* k_pages, const voi
  *   With few query tiles against many keys the key ranges are split evenly over the SMs, the parts'
  *   FP32 results go to `workspace` (32-byte aligned) and are merged.
  *   attn_diff_prefill_workspace_size() is 0 where that does not pay; with a smaller workspace, or
- *   NULL and 0 bytes, every query tile is one CTA's work.
+ *   NULL and 0 bytes, no query tile's keys are split.  The workspace needs no initial value; calls
+ *   that may run at the same time need separate ones.
  */
 size_t attn_diff_prefill_workspace_size(int B, int Hq, int Sq, int Skv, int D);
 int attn_diff_prefill_fwd(const void* q, const void* k, const void* v, const float* lambda_vecs,

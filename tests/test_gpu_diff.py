@@ -99,6 +99,27 @@ def test_diff_prompt_padded_batch(gb, causal):
     check_prompt(gb, q, k, v, q_lens=q_lens, kv_lens=kv_lens, causal=causal)
 
 
+@pytest.mark.parametrize("Sq,Skv,q_len,kv_len", [(200, 100, 200, 100), (128, 3000, 60, 2900)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_diff_prompt_rows_that_see_nothing_beside_an_infinite_value(gb, Sq, Skv, q_len, kv_len, norm):
+    """Rows before the first key, and padding rows of a split call, share key tiles with rows that
+    see an infinite value."""
+    q, k, v = prompt(1, 2, 1, Sq, Skv, 71)
+    v[:, :, 5] = np.inf
+    vecs, weight = inputs.diff_inputs(2, D, 71, norm=norm)
+    lse = torch.zeros((1, 2, 2, Sq), device=DEV)
+    lens = [t(np.array([n], dtype=np.int32)) for n in (q_len, kv_len)]
+    o = gb.attn_diff_prefill_fwd(t(q), t(k), t(v), t(vecs), 0.5, norm_weight=t(weight), lse=lse,
+                                 q_lens=lens[0], kv_lens=lens[1])
+    assert gb.device_status() == 0
+    i = np.arange(Sq)
+    visible = np.where(i < q_len, np.maximum(kv_len - q_len + i + 1, 0), 0)
+    none, all_of_it = t(visible == 0), t(visible > 5)
+    assert none.any() and torch.all(o[:, :, none] == 0)
+    assert torch.all(torch.isneginf(lse[..., none]))
+    assert not torch.isfinite(o[:, :, all_of_it]).any()
+
+
 def test_diff_prompt_split_keys(gb):
     """Few rows against many keys: with the full workspace, and with too little to split."""
     case = prompt(1, 2, 1, 70, 5000, 65, std=2.0)

@@ -280,6 +280,20 @@ def test_decode_abandoned_load_is_reported(gb):
     check_decode(gb, *case)
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_decode_rows_that_see_nothing_beside_an_infinite_value(gb, D):
+    """A query before the cache's first token gives O = 0 although a later query's value is inf."""
+    q, kp, vp, table, lens, _ = inputs.paged_f16_inputs(2, 4, 1, 5, (2, 700), D, 27)
+    vp[table[0, 0], 0] = np.inf
+    lse = torch.zeros((2, 4, 5), device=DEV)
+    o = gb.attn_paged_decode_f16_fwd(t(q), t(kp), t(vp), t(table), t(lens), lse=lse)
+    assert gb.device_status() == 0
+    assert torch.all(o[0, :, :3] == 0) and torch.all(torch.isneginf(lse[0, :, :3]))
+    # a row that sees the inf is not finite; inf or NaN, since P = hi + lo with lo zero or negative
+    # and 0 inf = NaN, inf - inf = NaN
+    assert not torch.isfinite(o[0, :, 3:]).any() and torch.isfinite(o[1]).all()
+
+
 def test_abandoned_loads_with_weights_touch_no_other_weight(gb):
     """A decode that gives up describes none of its tiles as live, whatever its workspace held: no
     weight outside the sequences' slots moves, and the next call is right again."""
