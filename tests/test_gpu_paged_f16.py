@@ -498,3 +498,75 @@ def test_serving_loop_with_a_budget(gb):
             assert np.array_equal(new_lens.cpu().numpy(), lens)
         assert np.array_equal(gk.cpu().numpy().view(np.uint16), kp.view(np.uint16))
     assert evictions >= 2 and gb.device_status() == 0
+
+
+def test_pages_past_32_bit_offsets(gb):
+    """Pages at the end of a pool of 4.6e9 elements: append, decode with weights, eviction in place
+    and into other pages give what they give in a small pool, bit for bit."""
+    B, Hq, Hkv, D, ps, n_pages = 2, 8, 8, 128, 64, 24
+    big = 2 ** 32 // (ps * Hkv * D) + 1 + 2 * n_pages
+    q, kp, vp, table, lens, w = inputs.paged_f16_inputs(B, Hq, Hkv, 1, (700, 333), D, 41, page_size=ps,
+                                                        spare_pages=7)
+    P = kp.shape[0]
+    assert P == n_pages and (big - P) * ps * Hkv * D > 2 ** 32
+    spare = np.setdiff1d(np.arange(P), table)[:6].reshape(2, 3).astype(np.int32)
+    kn, vn = np.random.default_rng(42).standard_normal((2, B, Hkv, 3, D)).astype(np.float16)
+
+    def run(pool, first):
+        gk, gv = (torch.empty((pool, ps, Hkv, D), dtype=torch.float16, device=DEV) for _ in range(2))
+        gw = torch.empty((pool, Hkv, ps), device=DEV)
+        mine = slice(first, first + P)
+        gk[mine], gv[mine], gw[mine] = t(kp), t(vp), t(w)
+        gt = t(np.where(table < 0, table, table + first).astype(np.int32))
+        gl = t(lens)
+        gb.kv_paged_append_f16(t(kn), t(vn), gk, gv, gt, gl, weights=gw)
+        o = gb.attn_paged_decode_f16_fwd(t(q), gk, gv, gt, gl, weights=gw)
+        moved = gb.kv_paged_evict(gk, gv, gw, gt, gl, 150, sink=4, recent=20, dst_table=t(spare + first))
+        there = gb.kv_paged_evict(gk, gv, gw, gt, gl, 200, sink=4, recent=20)
+        assert gb.device_status() == 0
+        return [o, *moved, *there, gk[mine].clone(), gv[mine].clone(), gw[mine].clone()]
+
+    small, large = run(P, 0), run(big, big - P)
+    for a, b in zip(small, large):
+        assert torch.equal(a, b)
+
+
+def test_decodes_at_the_same_time(gb):
+    """Two calls on two streams, each with a workspace of its own."""
+    cases = [inputs.paged_f16_inputs(3, 8, 2, 1, (9000, 5000, 12000), 128, seed) for seed in (43, 44)]
+    on_gpu = [[t(x) for x in case] for case in cases]
+    want = []
+    for q, kp, vp, table, lens, w in on_gpu:
+        gw = w.clone()
+        want.append((gb.attn_paged_decode_f16_fwd(q, kp, vp, table, lens, weights=gw), gw))
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[torch.empty_like(c[0]) for _ in range(8)] for c in on_gpu]
+    sums = [[c[5].clone() for _ in range(8)] for c in on_gpu]
+    ws = [torch.empty(gb.attn_paged_decode_f16_workspace_size(3, 8, 2, 1, c[3].shape[1] * 32, 128, True),
+                      dtype=torch.uint8, device=DEV) for c in on_gpu]
+    torch.cuda.synchronize()
+    for k in range(8):
+        for s, (q, kp, vp, table, lens, _), o, gw, space in zip(streams, on_gpu, outs, sums, ws):
+            gb.attn_paged_decode_f16_fwd(q, kp, vp, table, lens, o=o[k], weights=gw[k],
+                                         workspace=space, stream=s)
+    torch.cuda.synchronize()
+    for (o, gw), os, gws in zip(want, outs, sums):
+        assert all(torch.equal(o, x) for x in os) and all(torch.equal(gw, x) for x in gws)
+
+
+def test_shared_prefix_pages_are_evicted_into_fresh_ones(gb):
+    """Two sequences over the same first pages keep different tokens of them; the shared pages and
+    their weights stay as they are."""
+    q, kp, vp, table, lens, w = inputs.paged_f16_inputs(2, 4, 2, 1, (300, 300), 64, 45, page_size=16,
+                                                        spare_pages=12)
+    spare = np.setdiff1d(np.arange(kp.shape[0]), table)[:12].reshape(2, 6).astype(np.int32)
+    table[1, :10] = table[0, :10]
+    lens[1] = 250
+    gk, gv, gw = t(kp), t(vp), t(w)
+    new_lens, kept = gb.kv_paged_evict(gk, gv, gw, t(table), t(lens), 90, sink=3, recent=30,
+                                       dst_table=t(spare))
+    rk, rv, rw, rlens, rkept = OP.evict(kp, vp, w, table, spare, lens, 90, 3, 30)
+    assert gb.device_status() == 0
+    assert np.array_equal(kept.cpu().numpy(), rkept) and np.array_equal(new_lens.cpu().numpy(), rlens)
+    for got, ref in ((gk, rk), (gv, rv), (gw, rw)):
+        assert np.array_equal(got.cpu().numpy(), ref)
