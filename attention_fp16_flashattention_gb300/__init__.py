@@ -74,6 +74,8 @@ DEV_BAD_PAGE = 2
 DEV_BAD_INDEX = 4
 DEV_BAD_LENGTH = 8
 
+_Strides3 = ctypes.c_int64 * 3
+
 
 class GbattnError(RuntimeError):
     def __init__(self, fn, status):
@@ -155,7 +157,8 @@ def _strides(t):
     """{batch, head, row} element strides of a [B, H, S, D] view, or None when dense."""
     if t.is_contiguous():
         return None
-    return (ctypes.c_int64 * 3)(t.stride(0), t.stride(1), t.stride(2))
+    b, h, s, _ = t.stride()
+    return _Strides3(b, h, s)
 
 
 def _scale(scale, D):
@@ -394,6 +397,44 @@ def _same_device(*tensors):
             raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
 
 
+def _current_device(t, name):
+    """The current device, for a call whose first tensor is t (on a GPU, so CUDA is initialised)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return torch._C._cuda_getDevice()
+
+
+def _need_on(t, name, dtype, ndim, dev):
+    """_need, and on the current device `dev`.  Calls on one token's work are bound by the host, so
+    the usual case is one line."""
+    try:
+        if (t.dtype is dtype and t.dim() == ndim and t.get_device() == dev
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    _need(t, name, dtype, ndim)
+    _same_device(t)
+
+
+def _need_view_on(t, name, dtype, dev):
+    """_need_view, and on the current device `dev`."""
+    try:
+        if t.dtype is dtype and t.dim() == 4 and t.get_device() == dev and t.stride(3) == 1:
+            return
+    except AttributeError:
+        pass
+    _need_view(t, name, dtype)
+    _same_device(t)
+
+
+def _raw_stream(stream, dev):
+    """The handle of `stream`, or of device dev's current stream (_stream, the device known)."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
 def _new_tensor(shape, dtype, device, stream):
     """A tensor this module allocates for a call on `stream` (None: the current stream), taken
     from that stream's memory so that nothing queued on another stream still uses it."""
@@ -404,25 +445,33 @@ def _new_tensor(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _new_like(t, stream):
+    """_new_tensor of a contiguous tensor's shape and type."""
+    import torch
+    return torch.empty_like(t) if stream is None else _new_tensor(t.shape, t.dtype, t.device, stream)
+
+
 def _scratch(nbytes, device, stream):
     """Workspace bytes for one call on `stream`."""
     import torch
     return _new_tensor(max(int(nbytes), 16), torch.uint8, device, stream)
 
 
-def _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, Hkv, D):
-    """Checks an FP16 page pool with its table; returns (pages, page size, max pages)."""
+def _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, Hkv, D, dev):
+    """Checks an FP16 page pool with its table; returns (pages, page size, KV heads, max pages)."""
     import torch
-    _need(k_pages, "k_pages", torch.float16, 4)
-    _need(v_pages, "v_pages", torch.float16, 4)
-    _need(page_table, "page_table", torch.int32, 2)
-    _need(kv_lens, "kv_lens", torch.int32, 1)
-    P, ps, h, d = k_pages.shape
-    if tuple(v_pages.shape) != tuple(k_pages.shape) or d != D or (Hkv is not None and h != Hkv):
+    _need_on(k_pages, "k_pages", torch.float16, 4, dev)
+    _need_on(v_pages, "v_pages", torch.float16, 4, dev)
+    _need_on(page_table, "page_table", torch.int32, 2, dev)
+    _need_on(kv_lens, "kv_lens", torch.int32, 1, dev)
+    shape = k_pages.shape
+    P, ps, h, d = shape
+    if v_pages.shape != shape or d != D or (Hkv is not None and h != Hkv):
         raise ValueError("k_pages and v_pages must be [P, page, Hkv, D] matching the tokens")
-    if page_table.shape[0] != B or kv_lens.shape[0] != B:
+    rows, max_pages = page_table.shape
+    if rows != B or kv_lens.shape[0] != B:
         raise ValueError("page_table and kv_lens need one row per sequence")
-    return P, ps, page_table.shape[1]
+    return P, ps, h, max_pages
 
 
 def kv_paged_append_f16(k_new, v_new, k_pages, v_pages, page_table, kv_lens, new_lens=None,
@@ -433,23 +482,23 @@ def kv_paged_append_f16(k_new, v_new, k_pages, v_pages, page_table, kv_lens, new
     (device) appends only the first rows of each sequence; weights FP32 [P,Hkv,page] gets zeros
     at the new slots."""
     import torch
-    _need_view(k_new, "k_new", torch.float16)
-    _need_view(v_new, "v_new", torch.float16)
+    dev = _current_device(k_new, "k_new")
+    _need_view_on(k_new, "k_new", torch.float16, dev)
+    _need_view_on(v_new, "v_new", torch.float16, dev)
     B, Hkv, n, D = k_new.shape
-    if tuple(v_new.shape) != tuple(k_new.shape) or v_new.stride() != k_new.stride():
+    if v_new.shape != k_new.shape or v_new.stride() != k_new.stride():
         raise ValueError("k_new and v_new must have the same shape and strides")
-    P, ps, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, Hkv, D)
+    P, ps, _, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, Hkv, D, dev)
     if new_lens is not None:
-        _need(new_lens, "new_lens", torch.int32, 1)
+        _need_on(new_lens, "new_lens", torch.int32, 1, dev)
         _need_shape(new_lens, "new_lens", (B,))
     if weights is not None:
-        _need(weights, "weights", torch.float32, 3)
+        _need_on(weights, "weights", torch.float32, 3, dev)
         _need_shape(weights, "weights", (P, Hkv, ps))
-    _same_device(k_new, v_new, k_pages, v_pages, page_table, kv_lens, new_lens, weights)
-    rc = load().kv_paged_append_f16(_ptr(k_new), _ptr(v_new), _ptr(k_pages), _ptr(v_pages),
-                                    _ptr(page_table), _ptr(kv_lens), _ptr(new_lens), _ptr(weights),
-                                    B, Hkv, n, D, _strides(k_new), P, ps, max_pages,
-                                    _stream(stream))
+    rc = load().kv_paged_append_f16(k_new.data_ptr(), v_new.data_ptr(), k_pages.data_ptr(),
+                                    v_pages.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(),
+                                    _ptr(new_lens), _ptr(weights), B, Hkv, n, D, _strides(k_new), P,
+                                    ps, max_pages, _raw_stream(stream, dev))
     _check("kv_paged_append_f16", rc)
     return k_pages, v_pages
 
@@ -466,31 +515,34 @@ def attn_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, max_kv_l
     attention every cached token receives (what kv_paged_evict ranks by).  max_kv_len defaults to
     max_pages * page_size (no device read)."""
     import torch
-    _need(q, "q", torch.float16, 4)
+    dev = _current_device(q, "q")
+    _need_on(q, "q", torch.float16, 4, dev)
     B, Hq, nq, D = q.shape
-    P, ps, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, None, D)
-    Hkv = k_pages.shape[2]
+    P, ps, Hkv, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, None, D, dev)
     max_kv_len = max_pages * ps if max_kv_len is None else int(max_kv_len)
-    o = _new_tensor(q.shape, torch.float16, q.device, stream) if o is None else o
-    _need(o, "o", torch.float16, 4)
-    _need_shape(o, "o", q.shape)
+    if o is None:
+        o = _new_like(q, stream)
+    else:
+        _need_on(o, "o", torch.float16, 4, dev)
+        _need_shape(o, "o", q.shape)
     if lse is not None:
-        _need(lse, "lse", torch.float32)
+        _need_on(lse, "lse", torch.float32, 3, dev)
         _need_shape(lse, "lse", (B, Hq, nq))
     if weights is not None:
-        _need(weights, "weights", torch.float32, 3)
+        _need_on(weights, "weights", torch.float32, 3, dev)
         _need_shape(weights, "weights", (P, Hkv, ps))
     if workspace is None:
         workspace = _scratch(attn_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len, D,
                                                                   weights is not None),
                              q.device, stream)
-    _same_device(q, k_pages, v_pages, page_table, kv_lens, o, lse, weights, workspace)
-    rc = load().attn_paged_decode_f16_fwd(_ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table),
-                                          _ptr(kv_lens), _ptr(o), _ptr(lse), _ptr(weights), B, Hq,
-                                          Hkv, nq, D, P, ps, max_pages, max_kv_len,
-                                          _scale(scale, D), _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(),
-                                          _stream(stream))
+    elif workspace.get_device() != dev:
+        _same_device(workspace)
+    rc = load().attn_paged_decode_f16_fwd(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+                                          page_table.data_ptr(), kv_lens.data_ptr(), o.data_ptr(),
+                                          _ptr(lse), _ptr(weights), B, Hq, Hkv, nq, D, P, ps,
+                                          max_pages, max_kv_len, _scale(scale, D),
+                                          workspace.data_ptr(), workspace.nbytes,
+                                          _raw_stream(stream, dev))
     _check("attn_paged_decode_f16_fwd", rc)
     return o
 
@@ -504,18 +556,19 @@ def kv_paged_evict(k_pages, v_pages, weights, page_table, kv_lens, budget, sink=
     import torch
     if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in (torch.float16, torch.uint8):
         raise ValueError("k_pages must be a float16 or uint8 tensor")
-    _need(k_pages, "k_pages", k_pages.dtype, 4)
-    _need(v_pages, "v_pages", k_pages.dtype, 4)
-    _need(weights, "weights", torch.float32, 3)
-    _need(page_table, "page_table", torch.int32, 2)
-    _need(kv_lens, "kv_lens", torch.int32, 1)
+    cur = _current_device(k_pages, "k_pages")
+    _need_on(k_pages, "k_pages", k_pages.dtype, 4, cur)
+    _need_on(v_pages, "v_pages", k_pages.dtype, 4, cur)
+    _need_on(weights, "weights", torch.float32, 3, cur)
+    _need_on(page_table, "page_table", torch.int32, 2, cur)
+    _need_on(kv_lens, "kv_lens", torch.int32, 1, cur)
     P, ps, Hkv, D = k_pages.shape
     B, max_pages = page_table.shape
     _need_shape(v_pages, "v_pages", k_pages.shape)
     _need_shape(weights, "weights", (P, Hkv, ps))
     _need_shape(kv_lens, "kv_lens", (B,))
     dst = page_table if dst_table is None else dst_table
-    _need(dst, "dst_table", torch.int32, 2)
+    _need_on(dst, "dst_table", torch.int32, 2, cur)
     if dst.shape[0] != B:
         raise ValueError("dst_table needs one row per sequence")
     max_kv_len = max_pages * ps if max_kv_len is None else int(max_kv_len)
@@ -527,28 +580,31 @@ def kv_paged_evict(k_pages, v_pages, weights, page_table, kv_lens, budget, sink=
         new_lens = _new_tensor((B,), torch.int32, dev, stream)
     if kept is None:
         kept = _new_tensor((B, Hkv, budget), torch.int32, dev, stream)
-    _need(new_lens, "new_lens", torch.int32, 1)
+    _need_on(new_lens, "new_lens", torch.int32, 1, cur)
     _need_shape(new_lens, "new_lens", (B,))
-    _need(kept, "kept", torch.int32, 3)
+    _need_on(kept, "kept", torch.int32, 3, cur)
     _need_shape(kept, "kept", (B, Hkv, budget))
-    _same_device(k_pages, v_pages, weights, page_table, kv_lens, dst, new_lens, kept)
-    rc = load().kv_paged_evict(_ptr(k_pages), _ptr(v_pages), _ptr(weights), _ptr(page_table),
-                               _ptr(dst), _ptr(kv_lens), _ptr(new_lens), _ptr(kept), B, Hkv, D,
+    rc = load().kv_paged_evict(k_pages.data_ptr(), v_pages.data_ptr(), weights.data_ptr(),
+                               page_table.data_ptr(), dst.data_ptr(), kv_lens.data_ptr(),
+                               new_lens.data_ptr(), kept.data_ptr(), B, Hkv, D,
                                k_pages.element_size(), P, ps, max_pages, dst.shape[1], max_kv_len,
-                               budget, int(sink), int(recent), _stream(stream))
+                               budget, int(sink), int(recent), _raw_stream(stream, cur))
     _check("kv_paged_evict", rc)
     return new_lens, kept
 
 
-def _need_diff(lambda_vecs, norm_weight, Hq, D):
+def _need_diff(lambda_vecs, norm_weight, Hq, D, dev):
     """Checks the learned tensors of differential heads; returns lambda_heads (1 or Hq)."""
     import torch
     _need(lambda_vecs, "lambda_vecs", torch.float32)
-    heads = lambda_vecs.shape[1] if lambda_vecs.dim() == 3 else 1
-    if tuple(lambda_vecs.shape) not in ((4, D // 2), (4, 1, D // 2), (4, Hq, D // 2)):
+    if lambda_vecs.get_device() != dev:
+        _same_device(lambda_vecs)
+    shape = tuple(lambda_vecs.shape)
+    heads = shape[1] if len(shape) == 3 else 1
+    if shape != (4, Hq, D // 2) and shape not in ((4, D // 2), (4, 1, D // 2)):
         raise ValueError("lambda_vecs must be [4, D/2], [4, 1, D/2] or [4, Hq, D/2]")
     if norm_weight is not None:
-        _need(norm_weight, "norm_weight", torch.float32, 1)
+        _need_on(norm_weight, "norm_weight", torch.float32, 1, dev)
         _need_shape(norm_weight, "norm_weight", (D,))
     return heads
 
@@ -565,28 +621,30 @@ def attn_diff_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, lam
     (lq1, lk1, lq2, lk2); norm_weight FP32 [128] or None; lse FP32 [B,Hq,2,nq].  scale defaults to
     1/sqrt(64)."""
     import torch
-    _need(q, "q", torch.float16, 4)
+    dev = _current_device(q, "q")
+    _need_on(q, "q", torch.float16, 4, dev)
     B, Hq, nq, D = q.shape
-    P, ps, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, None, D)
-    Hkv = k_pages.shape[2]
-    heads = _need_diff(lambda_vecs, norm_weight, Hq, D)
+    P, ps, Hkv, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, None, D, dev)
+    heads = _need_diff(lambda_vecs, norm_weight, Hq, D, dev)
     max_kv_len = max_pages * ps if max_kv_len is None else int(max_kv_len)
-    o = _new_tensor(q.shape, torch.float16, q.device, stream) if o is None else o
-    _need(o, "o", torch.float16, 4)
-    _need_shape(o, "o", q.shape)
+    if o is None:
+        o = _new_like(q, stream)
+    else:
+        _need_on(o, "o", torch.float16, 4, dev)
+        _need_shape(o, "o", q.shape)
     if lse is not None:
-        _need(lse, "lse", torch.float32)
+        _need_on(lse, "lse", torch.float32, 4, dev)
         _need_shape(lse, "lse", (B, Hq, 2, nq))
     if workspace is None:
         workspace = _scratch(attn_diff_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len,
                                                                        D), q.device, stream)
-    _same_device(q, k_pages, v_pages, page_table, kv_lens, lambda_vecs, norm_weight, o, lse,
-                 workspace)
+    elif workspace.get_device() != dev:
+        _same_device(workspace)
     rc = load().attn_diff_paged_decode_f16_fwd(
-        _ptr(q), _ptr(k_pages), _ptr(v_pages), _ptr(page_table), _ptr(kv_lens), _ptr(lambda_vecs),
-        heads, float(lambda_init), _ptr(norm_weight), float(eps), _ptr(o), _ptr(lse), B, Hq, Hkv,
-        nq, D, P, ps, max_pages, max_kv_len, _scale(scale, D // 2), _ptr(workspace),
-        workspace.numel() * workspace.element_size(), _stream(stream))
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        kv_lens.data_ptr(), lambda_vecs.data_ptr(), heads, float(lambda_init), _ptr(norm_weight),
+        float(eps), o.data_ptr(), _ptr(lse), B, Hq, Hkv, nq, D, P, ps, max_pages, max_kv_len,
+        _scale(scale, D // 2), workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
     _check("attn_diff_paged_decode_f16_fwd", rc)
     return o
 
@@ -604,33 +662,38 @@ def attn_diff_prefill_fwd(q, k, v, lambda_vecs, lambda_init, norm_weight=None, e
     or None; q_lens, kv_lens int32 [B] (device) or None: padded batches; lse FP32 [B,Hq,2,Sq].
     scale defaults to 1/sqrt(64)."""
     import torch
-    for t, n in ((q, "q"), (k, "k"), (v, "v")):
-        _need_view(t, n, torch.float16)
+    dev = _current_device(q, "q")
+    _need_view_on(q, "q", torch.float16, dev)
+    _need_view_on(k, "k", torch.float16, dev)
+    _need_view_on(v, "v", torch.float16, dev)
     B, Hq, Sq, D = q.shape
-    Hkv, Skv = k.shape[1], k.shape[2]
-    if tuple(v.shape) != tuple(k.shape) or k.shape[0] != B or k.shape[3] != D:
+    Bk, Hkv, Skv, Dk = k.shape
+    if v.shape != k.shape or Bk != B or Dk != D:
         raise ValueError("k and v must be [B, Hkv, Skv, D] matching q")
     if k.stride() != v.stride():
         raise ValueError("k and v must have the same strides")
-    heads = _need_diff(lambda_vecs, norm_weight, Hq, D)
+    heads = _need_diff(lambda_vecs, norm_weight, Hq, D, dev)
     for t, n in ((q_lens, "q_lens"), (kv_lens, "kv_lens")):
         if t is not None:
-            _need(t, n, torch.int32, 1)
+            _need_on(t, n, torch.int32, 1, dev)
             _need_shape(t, n, (B,))
-    o = _new_tensor((B, Hq, Sq, D), torch.float16, q.device, stream) if o is None else o
-    _need_view(o, "o", torch.float16)
-    _need_shape(o, "o", (B, Hq, Sq, D))
+    if o is None:
+        o = _new_tensor((B, Hq, Sq, D), torch.float16, q.device, stream)
+    else:
+        _need_view_on(o, "o", torch.float16, dev)
+        _need_shape(o, "o", (B, Hq, Sq, D))
     if lse is not None:
-        _need(lse, "lse", torch.float32)
+        _need_on(lse, "lse", torch.float32, 4, dev)
         _need_shape(lse, "lse", (B, Hq, 2, Sq))
     if workspace is None:
         workspace = _scratch(attn_diff_prefill_workspace_size(B, Hq, Sq, Skv, D), q.device, stream)
-    _same_device(q, k, v, lambda_vecs, norm_weight, q_lens, kv_lens, o, lse, workspace)
+    elif workspace.get_device() != dev:
+        _same_device(workspace)
     rc = load().attn_diff_prefill_fwd(
-        _ptr(q), _ptr(k), _ptr(v), _ptr(lambda_vecs), heads, float(lambda_init), _ptr(norm_weight),
-        float(eps), _ptr(q_lens), _ptr(kv_lens), _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, Skv, D,
-        _strides(q), _strides(k), _strides(o), _scale(scale, D // 2), 1 if causal else 0,
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream))
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), lambda_vecs.data_ptr(), heads, float(lambda_init),
+        _ptr(norm_weight), float(eps), _ptr(q_lens), _ptr(kv_lens), o.data_ptr(), _ptr(lse), B, Hq,
+        Hkv, Sq, Skv, D, _strides(q), _strides(k), _strides(o), _scale(scale, D // 2),
+        1 if causal else 0, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
     _check("attn_diff_prefill_fwd", rc)
     return o
 

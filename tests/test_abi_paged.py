@@ -183,3 +183,17 @@ def test_diff_prefill_refusals(lib):
     assert call(ql=None, kl=None, lse=None, norm=None, eps=0.0) in (OK, CUDA)
     assert call() in (OK, CUDA)
     assert lib.attn_diff_prefill_workspace_size(1, 16, 8192, 8192, 128) == 0     # enough rows
+
+
+def test_wrappers_refuse_cpu_tensors(lib):
+    import torch
+    import attention_fp16_flashattention_gb300 as gb
+    z = torch.zeros(1, 1, 1, 64, dtype=torch.float16)
+    for call in (lambda x: gb.kv_paged_append_f16(x, z, z, z, z, z),
+                 lambda x: gb.attn_paged_decode_f16_fwd(x, z, z, z, z),
+                 lambda x: gb.kv_paged_evict(x, z, z, z, z, 4),
+                 lambda x: gb.attn_diff_paged_decode_f16_fwd(x, z, z, z, z, z, 0.5),
+                 lambda x: gb.attn_diff_prefill_fwd(x, z, z, z, 0.5)):
+        for x in (z, None):
+            with pytest.raises(ValueError):
+                call(x)

@@ -281,3 +281,24 @@ def test_diff_decode_in_a_graph(gb):
     want = gb.attn_diff_paged_decode_f16_fwd(*args, 0.3, norm_weight=weight)
     torch.cuda.synchronize()
     assert torch.equal(o, want)
+
+
+def test_wrappers_refuse_wrong_tensors(gb):
+    q, k, v = (t(x) for x in prompt(2, 2, 1, 9, 17, 72))
+    vecs, weight = (t(x) for x in inputs.diff_inputs(2, D, 72))
+    lens = t(np.array([9, 5], dtype=np.int32))
+    pages = torch.zeros((3, 16, 1, D), dtype=torch.float16, device=DEV)
+    table = torch.zeros((2, 2), dtype=torch.int32, device=DEV)
+    calls = [(gb.attn_diff_prefill_fwd, (q, k, v, vecs, 0.5, weight, 1e-5, True, lens, lens,
+                                         torch.empty_like(q))),
+             (gb.attn_diff_paged_decode_f16_fwd, (q, pages, pages, table, lens, vecs, 0.5, weight,
+                                                  1e-5, None, torch.empty_like(q)))]
+    for call, args in calls:
+        for i, x in enumerate(args):
+            if not isinstance(x, torch.Tensor):
+                continue
+            wider = x.double() if x.is_floating_point() else x.long()
+            for wrong in (x.cpu(), wider, x[..., :-1], x[:1].clone(), x[None]):
+                with pytest.raises(ValueError):
+                    call(*args[:i], wrong, *args[i + 1:])
+    assert gb.device_status() == 0

@@ -570,3 +570,21 @@ def test_shared_prefix_pages_are_evicted_into_fresh_ones(gb):
     assert np.array_equal(kept.cpu().numpy(), rkept) and np.array_equal(new_lens.cpu().numpy(), rlens)
     for got, ref in ((gk, rk), (gv, rv), (gw, rw)):
         assert np.array_equal(got.cpu().numpy(), ref)
+
+
+def test_wrappers_refuse_wrong_tensors(gb):
+    """A wrong type, shape, stride or device of each tensor of a call is a ValueError."""
+    q, kp, vp, table, lens, w = (t(x) for x in inputs.paged_f16_inputs(2, 4, 2, 1, (40, 70), 64, 46))
+    k_new = torch.zeros((2, 2, 1, 64), dtype=torch.float16, device=DEV)
+    calls = [(gb.kv_paged_append_f16, (k_new, k_new, kp, vp, table, lens, lens, w)),
+             (gb.attn_paged_decode_f16_fwd, (q, kp, vp, table, lens, None, torch.empty_like(q), None, w)),
+             (gb.kv_paged_evict, (kp, vp, w, table, lens, 16, 0, 0, table.clone()))]
+    for call, args in calls:
+        for i, x in enumerate(args):
+            if not isinstance(x, torch.Tensor):
+                continue
+            wider = x.double() if x.is_floating_point() else x.long()
+            for wrong in (x.cpu(), wider, x[..., :-1], x[:1].clone(), x[None]):
+                with pytest.raises(ValueError):
+                    call(*args[:i], wrong, *args[i + 1:])
+    assert gb.device_status() == 0
