@@ -33,8 +33,8 @@
 //     depend on any order unless two sequences share a page.
 // Measured (graph replays): 4 sequences of 65,571 to 131,072 tokens, 6 query heads on
 // one KV head of 256 (450 MB) 76 us, 5.9 TB/s, 0.87 of the measured copy; 32 of 257
-// to 8,191, 32 on 8 of 128, with weights (581 MB) 115 us, of which the decode kernel 98
-// (it also writes 17 MB of scores), the merge 5 and the weights 12; one sequence of 511
+// to 8,191, 32 on 8 of 128, with weights (581 MB) 112 us, 15 of them for the weights (a
+// kernel of its own, and 17 MB of scores written beside the cache's stream); one sequence of 511
 // 9 us, latency of the two kernels' dependent loads.  What the decode kernel loses
 // against the copy rate is its start (lengths, then page table, then the first tiles:
 // three trips to memory) and the joins at its end, 6 us together.
@@ -80,12 +80,13 @@ struct DecodeF16Args {
     float2* part_ml;
     long long tail0;
     uint32_t* prefix_out; // [B + 1]: tiles of all streams of the sequences before b
-    float* scores;        // [tile][pitch][16] log2-unit scores, or null
+    float* scores;        // log2-unit scores [tile][pairs][8][2][2]: of rows 2 p and 2 p + 1, tokens
+                          // g and g + 8, as one lane has them; or null
     uint4* tiles;         // with scores: what the weights kernel needs to know of each tile
     uint32_t* status;
     uint64_t wait_limit;
     int fault;   // test hook: 1 = no stage is loaded, 2 = loads stop after two ring rounds
-    int B, Hq, Hkv, nq, G, pitch, num_phys, ps, max_pages, max_kv;
+    int B, Hq, Hkv, nq, G, pairs, num_phys, ps, max_pages, max_kv;
     int side_bits, sets;  // row groups: `side` = 2^side_bits side by side in a CTA, `sets` such sets
     int maps;             // 1, or 2: row r is map r % 2 of query r / 2
     float sl2;            // softmax scale * log2(e)
@@ -197,6 +198,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
     const WaitCtl wc{a.wait_limit, a.status, abort_flag};
     const uint64_t policy = l2_evict_first();   // the cache is read once; records and scores stay
+    // scores are read back soon: kept in L2 (without this ncu saw 9 to 15 of their 17 MB written out
+    // to memory while the cache streams through, and the call took 1.4 us more)
+    const uint64_t keep = l2_evict_last();
     uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
     uint64_t* full = bars + warp * C::kStages;
 
@@ -356,15 +360,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 const int r0 = 8 * n + 2 * c;
                 const int real = a.G - (((L.sis % a.sets) << a.side_bits) + beside) * R;
                 const long long tile = (static_cast<long long>(u_beg + k) << a.side_bits) + beside;
-                float* sp = a.scores + (tile * a.pitch + r0) * kTile + g;
-                if (r0 < real) {
-                    sp[0] = x[0];
-                    sp[8] = x[2];
-                }
-                if (r0 + 1 < real) {
-                    sp[kTile] = x[1];
-                    sp[kTile + 8] = x[3];
-                }
+                if (r0 < real)
+                    store_f32x4_hint(a.scores + (tile * a.pairs + r0 / 2) * (2 * kTile) + 4 * g, x, keep);
             }
             // ---- online softmax for this lane's query columns 2c, 2c+1
             float mx0 = fmaxf(x[0], x[2]), mx1 = fmaxf(x[1], x[3]);
@@ -550,7 +547,7 @@ struct MergeArgs {
     uint32_t grid, parts;   // of the decode kernel
     __half* o;
     float* lse;       // [B][Hq][maps][nq] or null
-    float2* row_ml;   // [B][Hkv][G]: (M, 1 / L) for the weights kernel, or null
+    float2* row_ml;   // [B][Hkv][G, made even]: (M, 1 / L) for the weights kernel, or null
     DiffArgs diff;
 };
 
@@ -679,7 +676,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
                 a.lse[((static_cast<long long>(b) * a.Hq + head) * kMaps + mp) * a.nq + i] =
                     Ls == 0.0f ? -INFINITY : (M + log2f(Ls)) * kLn2;
             if (!kDiff && a.row_ml)
-                a.row_ml[(static_cast<long long>(b) * a.Hkv + hk) * (grp * a.nq) + r] =
+                a.row_ml[(static_cast<long long>(b) * a.Hkv + hk) * ((grp * a.nq + 1) & ~1) + r] =
                     make_float2(M, inv);
         }
     }
@@ -713,16 +710,20 @@ struct WeightArgs {
     const float2* row_ml;
     const uint32_t* prefix;
     float* weights;   // [num_phys][Hkv][ps]
-    int B, Hkv, G, row_groups, R, pitch, page_bits, side_bits, sets;
+    int B, Hkv, G, row_groups, R, pairs, page_bits, side_bits, sets;
 };
 
-__global__ void __launch_bounds__(256, 3) decode_f16_weights_kernel(const WeightArgs a) {
-    constexpr int kTiles = 4;
+// Bound by the latency of its loads (under ncu 20% of the DRAM rate, 30% of the issue slots).  What the
+// weights add to a call of 32 sequences (67,000 tiles of four rows), by tiles in flight and CTAs per SM:
+// 4 and 3 19.0 us, 2 and 3 17.0, 2 and 4 15.8, 2 and 5 15.0, 1 and 6 15.9, 1 and 4 17.7.
+constexpr int kWeightCtas = 5;
+__global__ void __launch_bounds__(256, kWeightCtas) decode_f16_weights_kernel(const WeightArgs a) {
+    constexpr int kTiles = 2;
     // A programmatic dependent of the merge, which itself waited for the decode.
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t N = a.prefix[a.B] / a.sets;   // (sequence, KV head, tile) triples
     const uint32_t step = gridDim.x * 16;
-    const int tok = threadIdx.x & 15;
+    const int tok = threadIdx.x & 15, g_even = (a.G + 1) & ~1;
     for (uint32_t x0 = blockIdx.x * 16 + (threadIdx.x >> 4); x0 < N; x0 += kTiles * step) {
         uint4 info[kTiles];
         float sum[kTiles];
@@ -736,9 +737,9 @@ __global__ void __launch_bounds__(256, 3) decode_f16_weights_kernel(const Weight
             const int set = rg >> a.side_bits, beside = rg - (set << a.side_bits);
             const int real = min(a.R, a.G - rg * a.R);
 #pragma unroll 2
-            for (int r = 0; r < real; ++r) {
-                float s[kTiles];
-                float2 m[kTiles];
+            for (int r = 0; r < real; r += 2) {
+                float2 s[kTiles];
+                float4 m[kTiles];
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j) {
                     // with one row group a triple's tile has its number: no wait for info
@@ -747,14 +748,21 @@ __global__ void __launch_bounds__(256, 3) decode_f16_weights_kernel(const Weight
                                             ? x
                                             : ((info[j].z + static_cast<long long>(set) * (info[j].w >> 5))
                                                << a.side_bits) + beside;
-                    s[j] = x < N ? a.scores[(u * a.pitch + r) * kTile + tok] : -INFINITY;
+                    s[j] = make_float2(-INFINITY, -INFINITY);
+                    if (x < N)
+                        s[j] = *reinterpret_cast<const float2*>(
+                            a.scores + (u * a.pairs + r / 2) * (2 * kTile) + 4 * (tok & 7) + 2 * (tok >> 3));
                 }
 #pragma unroll
                 for (int j = 0; j < kTiles; ++j)
-                    m[j] = a.row_ml[static_cast<long long>(info[j].y) * a.G + rg * a.R + r];
+                    m[j] = *reinterpret_cast<const float4*>(
+                        a.row_ml + static_cast<long long>(info[j].y) * g_even + rg * a.R + r);
 #pragma unroll
-                for (int j = 0; j < kTiles; ++j)
-                    if (s[j] != -INFINITY) sum[j] += fast_exp2(s[j] - m[j].x) * m[j].y;
+                for (int j = 0; j < kTiles; ++j) {
+                    if (s[j].x != -INFINITY) sum[j] += fast_exp2(s[j].x - m[j].x) * m[j].y;
+                    // an odd last row has no partner
+                    if (s[j].y != -INFINITY && r + 1 < real) sum[j] += fast_exp2(s[j].y - m[j].z) * m[j].w;
+                }
             }
         }
 #pragma unroll
@@ -799,6 +807,9 @@ struct Layout {
     size_t tail0, o, ml, prefix, row_ml, tiles, scores, total;
 };
 
+// Pairs of rows whose scores a tile of a row group has.
+int row_pairs(int groups, int R, int G) { return groups > 1 ? R / 2 : (G + 1) / 2; }
+
 Layout decode_layout(long long ctas, int B, int Hkv, int G, int max_kv, int D, bool weights) {
     const RowPlan rows = row_plan(G, D, B, Hkv, max_kv);
     const int R = rows.R;
@@ -814,13 +825,13 @@ Layout decode_layout(long long ctas, int B, int Hkv, int G, int max_kv, int D, b
     l.prefix = at;
     at += round16((static_cast<size_t>(B) + 1) * 4);
     l.row_ml = at;
-    if (weights) at += round16(static_cast<size_t>(B) * Hkv * G * 8);
+    if (weights) at += static_cast<size_t>(B) * Hkv * ((G + 1) & ~1) * 8;
     const size_t triples = static_cast<size_t>(B) * Hkv * ((static_cast<size_t>(max_kv) + kTile - 1) / kTile);
     const size_t tiles = triples * rows.groups;
     l.tiles = at;
     if (weights) at += triples * 16;
     l.scores = at;
-    if (weights) at += tiles * (rows.groups > 1 ? R : G) * kTile * 4;
+    if (weights) at += tiles * row_pairs(rows.groups, R, G) * (2 * kTile * 4);
     l.total = at + 16;
     return l;
 }
@@ -1004,7 +1015,7 @@ int run_decode(const DecodeCall& c) {
     a.G = G;
     a.side_bits = plan.side_bits;
     a.sets = plan.sets;
-    a.pitch = plan.groups > 1 ? R : G;
+    a.pairs = row_pairs(plan.groups, R, G);
     a.num_phys = c.num_phys;
     a.ps = c.ps;
     a.max_pages = c.max_pages;
@@ -1059,12 +1070,12 @@ int run_decode(const DecodeCall& c) {
     x.side_bits = plan.side_bits;
     x.sets = plan.sets;
     x.R = R;
-    x.pitch = a.pitch;
+    x.pairs = a.pairs;
     x.page_bits = 0;
     while ((1 << x.page_bits) < c.ps) ++x.page_bits;
     const long long tiles = static_cast<long long>(c.B) * c.Hkv * ((c.max_kv + kTile - 1) / kTile);
     const long long want = (tiles + 15) / 16;
-    const unsigned grid = static_cast<unsigned>(want < 3LL * dev.num_sms ? want : 3LL * dev.num_sms);
+    const unsigned grid = static_cast<unsigned>(want < 1LL * kWeightCtas * dev.num_sms ? want : 1LL * kWeightCtas * dev.num_sms);
     return launch_dependent(decode_f16_weights_kernel, dim3(grid), 256, s, x);
 }
 

@@ -175,6 +175,17 @@ __device__ __forceinline__ uint64_t l2_evict_first() {
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
     return p;
 }
+// L2 policy of data that is read again soon: its lines are the last to be replaced.
+__device__ __forceinline__ uint64_t l2_evict_last() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+__device__ __forceinline__ void store_f32x4_hint(float* dst, const float (&x)[4], uint64_t policy) {
+    asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1,%2,%3,%4}, %5;" ::"l"(dst), "f"(x[0]),
+                 "f"(x[1]), "f"(x[2]), "f"(x[3]), "l"(policy)
+                 : "memory");
+}
 // tma_load_3d under an L2 policy.
 __device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* m, uint64_t* bar,
                                                  int c0, int c1, int c2, uint64_t policy) {
