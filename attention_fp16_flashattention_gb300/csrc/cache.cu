@@ -138,9 +138,11 @@ __device__ __forceinline__ bool evict_select(const EvictArgs& a, uint32_t* s_dyn
                                              cg::cluster_group& cluster) {
     uint32_t* s_total = s_dyn;                          // [kDigits][kBins] of the whole cluster
     uint32_t* s_hist = s_total + kDigits * kBins;       // [kBins] of this CTA
-    uint32_t* s_keys = s_hist + kBins;
-    __shared__ uint32_t s_pick[2];                      // a bad page; then digit, keys still wanted at it
+    uint32_t* s_keys = s_hist + kBins;                  // [a.keys]; behind the first min(per, keys) the
+                                                        // cluster's keys of the chosen first digit
+    __shared__ uint32_t s_pick[2];                      // digit, keys still wanted at it
     __shared__ uint2 s_warp[kEvictWarps], s_cta;        // (above, equal) counts
+    __shared__ uint32_t s_bad, s_own;                   // s_own: keys this CTA has listed
     const int C = static_cast<int>(cluster.num_blocks());
     const int rank = static_cast<int>(cluster.block_rank());
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -160,12 +162,11 @@ __device__ __forceinline__ bool evict_select(const EvictArgs& a, uint32_t* s_dyn
     const int mid = want > 0 ? L - a.sink - a.recent : 0;
     const int per = (mid + C - 1) / C;
     const int lo = min(rank * per, mid), hi = min(lo + per, mid);
-    auto bad_slots = [&](const int32_t* tab, int t_lo, int t_hi) -> bool {   // [t_lo, t_hi)
-        bool bad = false;
-        for (int p = (t_lo >> a.page_bits) + tid; p < (t_hi + a.ps - 1) >> a.page_bits; p += kEvictThreads)
-            bad |= tab[p] < 0 || tab[p] >= a.num_phys;
-        return bad;
-    };
+    const bool together = C > 1 && want > 0;   // the cluster's CTAs exchange anything at all
+    for (int x = tid; x < (kDigits + 1) * kBins; x += kEvictThreads) s_total[x] = 0;   // s_hist too
+    if (tid == 0) s_bad = s_own = 0;
+    if (together) cluster.barrier_arrive();    // waited for before the first remote access
+    uint32_t* s_list = s_keys + min(per, a.keys);
     auto weight_at = [&](int t) -> float* {
         return a.weights + ((static_cast<long long>(table[t >> a.page_bits]) * a.Hkv + h) << a.page_bits) +
                (t & (a.ps - 1));
@@ -178,6 +179,22 @@ __device__ __forceinline__ bool evict_select(const EvictArgs& a, uint32_t* s_dyn
     bool bad = false;
     if (!bad_len) {
         const int held = min(hi - lo, a.keys);
+        // The pages of every slot whose weight is not loaded here, one after the other: with a middle
+        // those of the sinks, of the recent and of what the key array does not hold, else all; then the
+        // destination's.  The first of them are on their way before the weights.
+        auto pages_to = [&](int t) -> int { return (t + a.ps - 1) >> a.page_bits; };
+        const int p0 = mid == 0 ? pages_to(L) : pages_to(a.sink);
+        const int at1 = (L - a.recent) >> a.page_bits, p1 = mid == 0 ? 0 : pages_to(L) - at1;
+        const int at2 = (a.sink + lo + held) >> a.page_bits;
+        const int p2 = mid == 0 || held == hi - lo ? 0 : pages_to(a.sink + hi) - at2;
+        const int p3 = kInPlace ? 0 : pages_to(n);
+        auto page_at = [&](int x) -> int {
+            if (x < p0) return table[x];
+            if ((x -= p0) < p1) return table[at1 + x];
+            if ((x -= p1) < p2) return table[at2 + x];
+            return (x -= p2) < p3 ? dst_table[x] : 0;
+        };
+        const int early = page_at(tid);
         // eight weights a thread at a time, so that the loads (each behind a page-table
         // entry) wait together
         for (int i0 = tid; i0 < held; i0 += 8 * kEvictThreads) {
@@ -204,21 +221,42 @@ __device__ __forceinline__ bool evict_select(const EvictArgs& a, uint32_t* s_dyn
                 if (i < held) s_keys[i] = weight_key(wt[e]);
             }
         }
-        // the pages of every other slot
-        if (mid == 0) {
-            bad |= bad_slots(table, 0, L);
-        } else {
-            bad |= bad_slots(table, 0, a.sink) | bad_slots(table, L - a.recent, L) |
-                   bad_slots(table, a.sink + lo + held, a.sink + hi);
+        bad |= early < 0 || early >= a.num_phys;
+        for (int x = tid + kEvictThreads; x < p0 + p1 + p2 + p3; x += kEvictThreads) {
+            const int page = page_at(x);
+            bad |= page < 0 || page >= a.num_phys;
         }
-        if (!kInPlace) bad |= bad_slots(dst_table, 0, n);
     }
-    for (int x = tid; x < kDigits * kBins; x += kEvictThreads) s_total[x] = 0;
     bad = __syncthreads_or(bad) != 0;
-    if (C > 1 && want > 0) {   // the CTAs checked different pages; and every s_total is zero
-        if (tid == 0) s_pick[0] = bad ? 1u : 0u;
-        cluster.sync();
-        for (int r = 0; r < C; ++r) bad |= cluster.map_shared_rank(s_pick, r)[0] != 0;
+
+    // ---- the first digit, over the whole cluster.  Its CTAs checked different pages: what one
+    // found goes to all of them on the way.
+    auto count_keys = [&](uint32_t* hist, int pass, uint32_t chosen) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+        const uint32_t mask = pass == 2 ? 1023u : 2047u;
+        const int above_shift = pass == 1 ? 21 : 10;   // of the digits chosen so far
+        for (int i = tid; i < hi - lo; i += kEvictThreads) {
+            const uint32_t key = key_at(i);
+            if (pass == 0 || (key >> above_shift) == chosen) atomicAdd(&hist[(key >> shift) & mask], 1u);
+        }
+    };
+    auto share_counts = [&](uint32_t* total) {   // few bins are in use: theirs go to every CTA
+        for (int x = tid; x < kBins; x += kEvictThreads) {
+            const uint32_t count = s_hist[x];
+            if (count)
+                for (int r = 0; r < C; ++r) atomicAdd(cluster.map_shared_rank(total, r) + x, count);
+        }
+    };
+    if (want > 0 && (together || !bad)) {
+        if (!bad) count_keys(together ? s_hist : s_total, 0, 0);   // (it may look pages up again)
+        __syncthreads();
+        if (together) {
+            cluster.barrier_wait();
+            if (bad && tid < C) *cluster.map_shared_rank(&s_bad, tid) = 1;
+            share_counts(s_total);
+            cluster.sync();
+            bad = s_bad != 0;
+        }
     }
     if (bad && first == 0) atomicOr(a.status, kDevBadPage);
     bad |= bad_len;
@@ -235,31 +273,28 @@ __device__ __forceinline__ bool evict_select(const EvictArgs& a, uint32_t* s_dyn
         for (int j = first; j < a.recent; j += step) kept[n - a.recent + j] = L - a.recent + j;
         if (want > 0) {
             uint32_t chosen = 0, left = static_cast<uint32_t>(want);
+            uint32_t gathered = 0;   // keys of the chosen first digit, in s_list behind the CTA's own
 #pragma unroll 1
             for (int pass = 0; pass < kDigits; ++pass) {
-                const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-                const uint32_t mask = pass == 2 ? 1023u : 2047u;
-                const int above_shift = pass == 1 ? 21 : 10;   // of the digits chosen so far
                 uint32_t* total = s_total + pass * kBins;
-                uint32_t* hist = C > 1 ? s_hist : total;
-                if (C > 1) {
-                    for (int x = tid; x < kBins; x += kEvictThreads) hist[x] = 0;
-                    __syncthreads();
-                }
-                for (int i = tid; i < hi - lo; i += kEvictThreads) {
-                    const uint32_t key = key_at(i);
-                    if (pass == 0 || (key >> above_shift) == chosen)
-                        atomicAdd(&hist[(key >> shift) & mask], 1u);
-                }
-                __syncthreads();
-                if (C > 1) {   // few bins are in use: their counts go to every CTA of the cluster
-                    for (int x = tid; x < kBins; x += kEvictThreads) {
-                        const uint32_t count = hist[x];
-                        if (count)
-                            for (int r = 0; r < C; ++r)
-                                atomicAdd(cluster.map_shared_rank(total, r) + x, count);
+                if (pass > 0 && gathered > 0) {   // every CTA counts the cluster's few by itself
+                    const int shift = pass == 1 ? 10 : 0, above_shift = pass == 1 ? 21 : 10;
+                    const uint32_t mask = pass == 1 ? 2047u : 1023u;
+                    for (uint32_t i = tid; i < gathered; i += kEvictThreads) {
+                        const uint32_t key = s_list[gathered + i];
+                        if ((key >> above_shift) == chosen) atomicAdd(&total[(key >> shift) & mask], 1u);
                     }
+                    __syncthreads();
+                } else if (pass > 0 && C > 1) {
+                    for (int x = tid; x < kBins; x += kEvictThreads) s_hist[x] = 0;
+                    __syncthreads();
+                    count_keys(s_hist, pass, chosen);
+                    __syncthreads();
+                    share_counts(total);
                     cluster.sync();
+                } else if (pass > 0) {
+                    count_keys(total, pass, chosen);
+                    __syncthreads();
                 }
                 // the bin that holds the left-th largest key: four bins a thread, from the top
                 const int top = kBins - 4 - 4 * tid;
@@ -287,8 +322,29 @@ __device__ __forceinline__ bool evict_select(const EvictArgs& a, uint32_t* s_dyn
                     }
                 }
                 __syncthreads();
-                chosen = (chosen << (pass == 2 ? 10 : 11)) | s_pick[0];
+                const uint32_t digit = s_pick[0];
+                chosen = (chosen << (pass == 2 ? 10 : 11)) | digit;
                 left = s_pick[1];
+                // The keys of the chosen first digit are few unless most weights are alike.  Every CTA
+                // lists its own, then reads all lists, and the other digits need no more of the cluster.
+                if (C > 1 && pass == 0 &&
+                    2 * total[digit] <= static_cast<uint32_t>(a.keys - min(per, a.keys))) {
+                    gathered = total[digit];
+                    for (int i = tid; i < hi - lo; i += kEvictThreads) {
+                        const uint32_t key = key_at(i);
+                        if ((key >> 21) == digit) s_list[atomicAdd(&s_own, 1u)] = key;
+                    }
+                    cluster.sync();
+                    const int warps = kEvictWarps / C, r = warp / warps;   // a list's warps, and the list
+                    const uint32_t own = lane < C ? *cluster.map_shared_rank(&s_own, lane) : 0u;
+                    const uint32_t before = __reduce_add_sync(0xffffffffu, lane < r ? own : 0u);
+                    const uint32_t here = __shfl_sync(0xffffffffu, own, r);
+                    const uint32_t* list = cluster.map_shared_rank(s_list, r);
+#pragma unroll 4
+                    for (uint32_t i = (warp - r * warps) * 32 + lane; i < here; i += warps * 32)
+                        s_list[gathered + before + i] = list[i];
+                    __syncthreads();
+                }
             }
             // ---- places: a warp takes consecutive slots; (above, equal) counts before it
             const int wper = ((hi - lo + kEvictWarps - 1) / kEvictWarps + 31) & ~31;
@@ -311,10 +367,11 @@ __device__ __forceinline__ bool evict_select(const EvictArgs& a, uint32_t* s_dyn
             if (tid == kEvictThreads - 1)
                 s_cta = make_uint2(above + s_warp[warp].x, equal + s_warp[warp].y);
             if (C > 1) cluster.sync();
-            for (int r = 0; r < rank; ++r) {
-                const uint2 t = *cluster.map_shared_rank(&s_cta, r);
-                above += t.x;
-                equal += t.y;
+            if (rank > 0) {
+                uint2 t = make_uint2(0u, 0u);
+                if (lane < rank) t = *cluster.map_shared_rank(&s_cta, lane);
+                above += __reduce_add_sync(0xffffffffu, t.x);
+                equal += __reduce_add_sync(0xffffffffu, t.y);
             }
             const uint32_t below = (1u << lane) - 1u;
             for (int i0 = w0; i0 < w1; i0 += 32) {

@@ -385,6 +385,55 @@ def test_evict_more_slots_than_the_key_array(gb):
     run_evict(gb, (215000,), 3000, 4, 1000, Hkv=1, D=64, ps=256, in_place=False)
 
 
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("weights", ["equal", "one digit", "two digits", "ties"])
+def test_evict_in_clusters_with_alike_weights(gb, weights, in_place):
+    """The keys of the chosen first digit fill the lists of a cluster's CTAs, or pass them (from about
+    13,000 on at these lengths)."""
+    lens = (30000, 12000)
+    _, kp, vp, table, lens, w = inputs.paged_f16_inputs(2, 1, 1, 1, lens, 64, 47, page_size=64,
+                                                        spare_pages=128)
+    rng = np.random.default_rng(48)
+    w = {"equal": np.full(w.shape, 0.25), "one digit": 1.0 + 0.2 * rng.random(w.shape),
+         "two digits": np.where(rng.random(w.shape) < 0.5, 1.0 + 0.2 * rng.random(w.shape),
+                                2.0 + 0.4 * rng.random(w.shape)),
+         "ties": rng.integers(0, 4, w.shape)}[weights].astype(np.float32)
+    spare = np.setdiff1d(np.arange(kp.shape[0]), table)[:128].reshape(2, 64).astype(np.int32)
+    gk, gv, gw, tt = t(kp), t(vp), t(w), t(table)
+    for budget in (4000, 3999):
+        dst = table if in_place else spare
+        new_lens, kept = gb.kv_paged_evict(gk, gv, gw, tt, t(lens), budget, sink=7, recent=100,
+                                           dst_table=None if in_place else t(dst))
+        assert gb.device_status() == 0
+        kp, vp, w, rlens, rkept = OP.evict(kp, vp, w, table, dst, lens, budget, 7, 100)
+        assert np.array_equal(kept.cpu().numpy(), rkept)
+        assert np.array_equal(new_lens.cpu().numpy(), rlens)
+        assert np.array_equal(gk.cpu().numpy(), kp) and np.array_equal(gv.cpu().numpy(), vp)
+        assert np.array_equal(gw.cpu().numpy(), w)
+        lens = rlens if in_place else lens
+
+
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("at", [0, 100, 150, 700, 839])   # sinks, held keys, beyond them, recent
+def test_evict_bad_page_of_a_long_sequence(gb, at, in_place):
+    """A page out of range anywhere in a sequence that eight CTAs share leaves it as it is."""
+    _, kp, vp, table, lens, w = inputs.paged_f16_inputs(2, 1, 1, 1, (215000, 500), 64, 49, page_size=256,
+                                                        spare_pages=8)
+    spare = np.setdiff1d(np.arange(kp.shape[0]), table)[:8].reshape(2, 4).astype(np.int32)
+    bad = table.copy()
+    bad[0, at] = kp.shape[0]
+    dst = bad if in_place else spare
+    gk, gv, gw, tt = t(kp), t(vp), t(w), t(bad)
+    new_lens, kept = gb.kv_paged_evict(gk, gv, gw, tt, t(lens), 400, sink=30, recent=200,
+                                       dst_table=None if in_place else t(dst))
+    assert gb.device_status() == gb.DEV_BAD_PAGE
+    rk, rv, rw, _, rkept = OP.evict(kp, vp, w, table[1:], dst[1:], lens[1:], 400, 30, 200)
+    assert new_lens.cpu().tolist() == [215000, 400]
+    assert torch.all(kept[0] == -1) and np.array_equal(kept[1:].cpu().numpy(), rkept)
+    assert np.array_equal(gk.cpu().numpy(), rk) and np.array_equal(gv.cpu().numpy(), rv)
+    assert np.array_equal(gw.cpu().numpy(), rw)
+
+
 def test_evict_one_at_a_time(gb):
     """A step of a loop that evicts as soon as the budget is passed: most rows do not move."""
     run_evict(gb, (1025, 1024, 1026), 1024, 4, 64, Hkv=2, D=128, ps=16)
