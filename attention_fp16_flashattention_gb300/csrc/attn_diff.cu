@@ -30,8 +30,9 @@
 // range of them (as the decode kernels do); the parts of a unit that ranges cut leave unnormalised
 // O_m, max and sum in `workspace`, and a merge kernel joins them.
 //
-// Measured: 16 heads x 8192 causal 272 us (1516 useful TFLOP/s, 0.80 of the measured burst; tensor
-// pipe 65% active under ncu), 500 queries on 32,500 keys 162 us.  How it got there (the first case):
+// Measured: 16 heads x 8192 causal 272 to 284 us on several GPUs (1450 to 1516 useful TFLOP/s, 0.77 to
+// 0.80 of the measured burst; tensor pipe 66% active under ncu; 310 us in long runs under the power
+// cap), 500 queries on 32,500 keys 162 to 179 us.  How it got there (the first case):
 // both maps' softmax on eight warps in step, P over S 350 us (the softmax alone, without any MMA,
 // took 320); a warpgroup per map and S handed back early into registers 294; persistent CTAs 286;
 // PV in two halves 272.  Without softmax the MMA handshakes take 232 us, and the softmax without

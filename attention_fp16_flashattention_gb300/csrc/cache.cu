@@ -85,13 +85,14 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 // Selection.  One cluster of 1..8 CTAs takes one (sequence, KV head).  Of its L > budget
 // slots the first `sink` and the last `recent` stay, and of the middle the M = budget -
 // sink - recent heaviest.  The M-th largest weight is found by radix selection on
-// order-preserving 32-bit keys in three passes (11, 11 and 10 bits): each CTA counts its
-// part of the slots (keys held in shared memory) into 2048 bins and adds the counts to
-// every CTA of the cluster.  Eleven bits hold the sign, the exponent and two bits of the
-// mantissa, so even the first pass spreads over some dozens of bins (with 8-bit digits it
-// met in seven, and a fourth pass was due).  Keys above the M-th are kept, and of those
-// equal to it the first slots up to M.  Prefix counts over warps and CTAs give every kept
-// slot its place, in slot order.
+// order-preserving 32-bit keys, by digits of 11, 11 and 10 bits.  For the first, each CTA
+// counts its part of the slots (keys held in shared memory) into 2048 bins and adds the
+// counts to every CTA of the cluster.  Eleven bits hold the sign, the exponent and two bits
+// of the mantissa, so the bin that holds the M-th has a few percent of the keys as a rule:
+// the CTAs exchange those, and each counts the other digits by itself.  Where most weights
+// are alike they pass the lists, and the counts are exchanged for every digit.  Keys above
+// the M-th are kept, and of those equal to it the first slots up to M.  Prefix counts over
+// warps and CTAs give every kept slot its place, in slot order.
 //
 // Moving.  Into other pages a second kernel copies the rows, shared evenly over the GPU's
 // warps whatever the number of heads.  In place a row's new slot j is never above its old
@@ -100,9 +101,11 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(const AppendA
 // which may therefore run ahead; the cluster that selected moves its own rows.
 //
 // Bound by HBM: the kept rows read and written.  16 sequences of about 1,100 tokens kept to
-// 1,024 (8 KV heads of 128, 136 MB): 8 us of selection, a chain of small latencies, and 20 us
-// of copies (6.7 TB/s), 32 us in all.  4 of 20,011 to 32,768 kept to 8,192 (274 MB): 18 us in
-// clusters of eight and 40 us, 67 us in all; in place 78 us.
+// 1,024 (8 KV heads of 128, 136 MB): 7.5 us of selection, half of it the wait for lengths, pages
+// and weights, one behind the other, and 20 us of copies (6.7 TB/s), 31 us in all.  4 of
+// 20,011 to 32,768 kept to 8,192 (274 MB): 15 us in clusters of eight and 40 us, 63 us in all
+// (67 with the counts of every digit exchanged; 66 and 77 in clusters of four and two); in
+// place 76 us (and the former 38).
 
 constexpr int kEvictThreads = 512;
 constexpr int kEvictWarps = kEvictThreads / 32;
@@ -745,7 +748,7 @@ extern "C" int kv_paged_evict(void* k_pages, void* v_pages, float* weights,
     const int rc = current_device(&dev);
     if (rc != GBATTN_OK) return rc;
 
-    // Selection: a CTA for about 4096 slots, as long as all CTAs are resident at once (two per SM).
+    // Selection: a CTA for 2048 to 4096 slots, as long as all CTAs are resident at once (two per SM).
     // In place the cluster also moves its rows, so it is as large as that allows.
     int C = kEvictMaxCluster;
     while (C > 1 && (streams * C > 2LL * dev.num_sms || (!in_place && max_kv_len <= 2048LL * C))) C /= 2;

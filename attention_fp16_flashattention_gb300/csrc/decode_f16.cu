@@ -32,8 +32,8 @@
 //     Every (token, KV head) is added to once per call, so the result does not
 //     depend on any order unless two sequences share a page.
 // Measured (graph replays): 4 sequences of 65,571 to 131,072 tokens, 6 query heads on
-// one KV head of 256 (450 MB) 76 us, 5.9 TB/s, 0.87 of the measured copy; 32 of 257
-// to 8,191, 32 on 8 of 128, with weights (581 MB) 112 us, 15 of them for the weights (a
+// one KV head of 256 (450 MB) 75 us, 6.0 TB/s, 0.89 of the measured copy; 32 of 257
+// to 8,191, 32 on 8 of 128, with weights (581 MB) 110 us, 15 of them for the weights (a
 // kernel of its own, and 17 MB of scores written beside the cache's stream); one sequence of 511
 // 9 us, latency of the two kernels' dependent loads.  What the decode kernel loses
 // against the copy rate is its start (lengths, then page table, then the first tiles:
@@ -199,7 +199,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const WaitCtl wc{a.wait_limit, a.status, abort_flag};
     const uint64_t policy = l2_evict_first();   // the cache is read once; records and scores stay
     // scores are read back soon: kept in L2 (without this ncu saw 9 to 15 of their 17 MB written out
-    // to memory while the cache streams through, and the call took 1.4 us more)
+    // to memory while the cache streams through, and the call took 1.4 us more; 65 MB of them cost a
+    // later kernel 2.3 us, once, until its own lines have taken their place)
     const uint64_t keep = l2_evict_last();
     uint8_t* ring = smem + warp * C::kStages * C::kStageBytes;
     uint64_t* full = bars + warp * C::kStages;
