@@ -34,8 +34,8 @@
 // 0.80 of the measured burst; tensor pipe 66% active under ncu; 310 us in long runs under the power
 // cap), 500 queries on 32,500 keys 162 to 179 us.  How it got there (the first case):
 // both maps' softmax on eight warps in step, P over S 350 us (the softmax alone, without any MMA,
-// took 320); a warpgroup per map and S handed back early into registers 294; persistent CTAs 286;
-// PV in two halves 272.  Without softmax the MMA handshakes take 232 us, and the softmax without
+// took 320); a warpgroup per map and S handed back early into registers 294; persistent CTAs 284;
+// PV in two halves 275.  Without softmax the MMA handshakes take 232 us, and the softmax without
 // MMAs 252.  Slower: 16 softmax warps on one step (372) or eight per map (305), exponentials against
 // the last reference while the max is still being found (336), P released by halves (301).
 //
