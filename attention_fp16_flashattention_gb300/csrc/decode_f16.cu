@@ -31,14 +31,19 @@
 //     sum, a third kernel adds sum_r 2^(x - max) / sum to every token's weight.
 //     Every (token, KV head) is added to once per call, so the result does not
 //     depend on any order unless two sequences share a page.
+//   * Short caches without weights: a cluster of up to eight CTAs takes each stream, and
+//     joins the partials through its shared memory; one kernel (rule at cluster_of).
 // Measured (graph replays): 4 sequences of 65,571 to 131,072 tokens, 6 query heads on
 // one KV head of 256 (450 MB) 75 us, 6.0 TB/s, 0.89 of the measured copy; 32 of 257
 // to 8,191, 32 on 8 of 128, with weights (581 MB) 110 us, 15 of them for the weights (a
 // kernel of its own, and 17 MB of scores written beside the cache's stream); one sequence of 511
-// 9 us, latency of the two kernels' dependent loads.  What the decode kernel loses
-// against the copy rate is its start (lengths, then page table, then the first tiles:
-// three trips to memory) and the joins at its end, 6 us together.
+// 7.3 us in clusters (9.1 with a merge kernel), latency of the loads behind each other.
+// What the decode kernel loses against the copy rate is its start (lengths, then page
+// table, then the first tiles: three trips to memory) and the joins at its end, 6 us
+// together.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
+
 #include <mutex>
 
 #include "diff.cuh"
@@ -46,12 +51,15 @@
 #include "ptx.cuh"
 #include "tiles.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace gbattn {
 namespace {
 
 constexpr int kTile = 16;        // tokens per tile (one MMA M block)
 constexpr int kMaxSeqs = 4096;   // sequences per launch (prefix table in shared memory)
 constexpr float kRescale = 8.0f;
+constexpr int kMaxCluster = 8;      // CTAs of a stream's cluster
 constexpr float kLn2 = 0.69314718055994531f;
 
 template <int D>
@@ -66,6 +74,14 @@ struct Cfg {
     static constexpr int kRing = kWarps * kStages * kStageBytes;
     static constexpr int kBarBytes = kWarps * kStages * 8;
     static constexpr int kSmem = kRing + kBarBytes + 4 * (kMaxSeqs + 1) + 16 + 1024;
+};
+
+// Where a finished row goes, and what the differential form does to it.
+struct RowOut {
+    __half* o;
+    float* lse;       // [B][Hq][maps][nq] or null
+    int Hq, nq;
+    DiffArgs diff;
 };
 
 struct DecodeF16Args {
@@ -90,6 +106,7 @@ struct DecodeF16Args {
     int side_bits, sets;  // row groups: `side` = 2^side_bits side by side in a CTA, `sets` such sets
     int maps;             // 1, or 2: row r is map r % 2 of query r / 2
     float sl2;            // softmax scale * log2(e)
+    RowOut out;           // a cluster a stream: where its rows go
 };
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -126,7 +143,47 @@ __device__ __forceinline__ float record_weight(float2 ml, float M) {
     return ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : exp2f(ml.x - M);
 }
 
-template <int D, int NB>
+// The end of a row, a warp on D columns (V a lane): map mp's joint (M, sum Ls) and O scaled by
+// 2^(x - M) give O / Ls and lse = (M + log2 Ls) ln 2; a row that sees nothing gets 0 and -inf.
+template <int V>
+__device__ __forceinline__ void add_map(float (&out)[V], const float (&so)[V], float M, float Ls, int mp,
+                                        float lambda, const RowOut& t, int b, int head, int i, int maps,
+                                        int lane) {
+    const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
+    const float f = mp == 0 ? inv : -lambda * inv;
+#pragma unroll
+    for (int e = 0; e < V; ++e) out[e] += so[e] * f;
+    if (lane == 0 && t.lse)
+        t.lse[((static_cast<long long>(b) * t.Hq + head) * maps + mp) * t.nq + i] =
+            Ls == 0.0f ? -INFINITY : (M + log2f(Ls)) * kLn2;
+}
+template <int D>
+__device__ __forceinline__ void store_row(float (&out)[D / 32], bool diff, const RowOut& t, int b,
+                                          int head, int i, int lane) {
+    constexpr int V = D / 32;
+    if (diff && t.diff.norm) {
+        float sq = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) sq += out[e] * out[e];
+        const float rn = rsqrtf(warp_sum(sq) * (1.0f / D) + t.diff.eps) * (1.0f - t.diff.init);
+#pragma unroll
+        for (int e = 0; e < V; ++e) out[e] *= rn * t.diff.norm[lane * V + e];
+    }
+    __half* op = t.o + ((static_cast<long long>(b) * t.Hq + head) * t.nq + i) * D + lane * V;
+    if constexpr (V == 2) {
+        *reinterpret_cast<uint32_t*>(op) = pack_half2(out[0], out[1]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; e += 4)
+            *reinterpret_cast<uint2*>(op + e) =
+                make_uint2(pack_half2(out[e], out[e + 1]), pack_half2(out[e + 2], out[e + 3]));
+    }
+}
+
+// kOne: a cluster takes one stream, its CTAs' warps equal shares of the stream's tiles, and joins the
+// partials in its shared memory: short caches, where the merge kernel would cost more than an uneven
+// split (rule and times at cluster_of).
+template <int D, int NB, bool kOne>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     decode_f16_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
                       DecodeF16Args a) {
@@ -149,8 +206,23 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         tma_prefetch_desc(&tk);
         tma_prefetch_desc(&tv);
     }
-    // ---- tile prefix over sequences (block-wide scan of per-sequence tile counts)
-    {
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C_one = kOne ? static_cast<int>(cluster.num_blocks()) : 1;
+    TileLoc one{};   // kOne: the stream and its tiles
+    if constexpr (kOne) {
+        const int stream = static_cast<int>(blockIdx.x) / C_one;
+        one.b = stream / per_seq;
+        one.sis = stream - one.b * per_seq;
+        const int len = a.kv_lens[one.b];
+        if ((len < 0 || len > a.max_kv) && threadIdx.x == 0) atomicOr(a.status, kDevBadLength);
+        one.s_end = seq_tiles(len, a.max_kv);
+        if (threadIdx.x == 0) {
+            for (int s = 0; s < C::kWarps * C::kStages; ++s) mbar_init(&bars[s], 1);
+            *abort_flag = 0;
+            mbar_init_fence();
+        }
+        __syncthreads();
+    } else {   // ---- tile prefix over sequences (block-wide scan of per-sequence tile counts)
         const int per = (a.B + C::kThreads) / C::kThreads;   // entries 0..B over the threads
         const int b0 = threadIdx.x * per;
         uint32_t sum = 0;
@@ -186,15 +258,21 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             for (int b = threadIdx.x; b <= a.B; b += C::kThreads) a.prefix_out[b] = prefix[b];
     }
     // The merge grid may start launching now; it waits for this grid to finish.
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t U = prefix[a.B];
-    const Split sp = split_of(U, gridDim.x, C::kWarps >> a.side_bits);
-    if (blockIdx.x >= sp.ctas) return;
+    if constexpr (!kOne) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const uint32_t U = kOne ? one.s_end : prefix[a.B];
+    const Split sp = kOne ? Split{static_cast<uint32_t>(C_one), static_cast<uint32_t>(C::kWarps)}
+                          : split_of(U, gridDim.x, C::kWarps >> a.side_bits);
+    if (!kOne && blockIdx.x >= sp.ctas) return;
     // every part below sp.parts has at least one tile; the others wait at the end
+    const uint32_t cta = kOne ? cluster.block_rank() : blockIdx.x;
     const uint32_t W = sp.ctas * sp.parts;
-    const uint32_t w = blockIdx.x * sp.parts + min(static_cast<uint32_t>(part), sp.parts - 1);
+    const uint32_t w = cta * sp.parts + min(static_cast<uint32_t>(part), sp.parts - 1);
     const bool idle = static_cast<uint32_t>(part) >= sp.parts;
     const uint32_t u_beg = warp_start(w, W, U), u_end = idle ? u_beg : warp_start(w + 1, W, U);
+    auto place = [&](uint32_t u) -> TileLoc {
+        if constexpr (kOne) return TileLoc{one.b, one.sis, static_cast<int>(u), one.s_end};
+        return locate(u, prefix, a.B, per_seq);
+    };
 
     const WaitCtl wc{a.wait_limit, a.status, abort_flag};
     const uint64_t policy = l2_evict_first();   // the cache is read once; records and scores stay
@@ -209,7 +287,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // as (head, row) in 64 bits.
     auto tile_src = [&](uint32_t u, bool dead = false) -> long long {
         if (u >= u_end) return 0;
-        const TileLoc L = locate(u, prefix, a.B, per_seq);
+        const TileLoc L = place(u);
         const int tok = L.t * kTile;
         int page = a.table[static_cast<long long>(L.b) * a.max_pages + tok / a.ps];
         const bool bad = page < 0 || page >= a.num_phys;
@@ -218,7 +296,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             page = 0;
         }
         const int hk = L.sis / a.sets;
-        if (a.scores) {
+        if (!kOne && a.scores) {
             // One description for all row groups: group 0's tile leaves (first slot, sequence and
             // KV head, its own number, live tokens + 32 * tiles of the stream); none live on a
             // bad page, or where the warp gave up (dead).  Row group r's tile is side * (number + (r / side) tiles) + r % side.
@@ -263,7 +341,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     float o[NB][C::kSteps][4];
     float m_ref[NB][2], l_sum[NB][2];
     uint32_t qf[NB][C::kSteps][2];
-    TileLoc L = locate(u_beg, prefix, a.B, per_seq);
+    TileLoc L = place(u_beg);
     int kv_len = 0, lim[NB][2], first_masked = 0;
     // Start of a stream segment: state reset and the Q operand of the stream's rows.
     auto begin_stream = [&]() {
@@ -307,6 +385,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     // lane / 16; V rows (lane % 8) + 8 (lane / 16), chunk (lane / 8) % 2.
     const int k_row = lane & 15, k_ch = lane >> 4;
     const int v_row = (lane & 7) + ((lane >> 4) << 3), v_ch = (lane >> 3) & 1;
+
+    // kOne: the warp's first query at the end and its lambda, which need not wait until then
+    const int hk_one = one.sis / a.sets, rg_one = one.sis - hk_one * a.sets;
+    const int queries = min(R, a.G - rg_one * R) / a.maps;   // R and G are multiples of maps
+    const int j_first = static_cast<int>(cta) * C::kWarps + warp;
+    float lambda = 0.0f;
+    if constexpr (kOne) {
+        if (a.maps == 2 && j_first < queries)
+            lambda = diff_lambda(a.out.diff, hk_one * (a.Hq / a.Hkv) + (rg_one * (R / 2) + j_first) / a.nq,
+                                 D / 2, lane);
+    }
 
     bool aborted = false;
     for (uint32_t k = 0; k < n_tiles; ++k) {
@@ -357,7 +446,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 if (t1 > lim[n][0]) x[2] = -INFINITY;
                 if (t1 > lim[n][1]) x[3] = -INFINITY;
             }
-            if (a.scores) {
+            if (!kOne && a.scores) {
                 const int r0 = 8 * n + 2 * c;
                 const int real = a.G - (((L.sis % a.sets) << a.side_bits) + beside) * R;
                 const long long tile = (static_cast<long long>(u_beg + k) << a.side_bits) + beside;
@@ -431,7 +520,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 
         // ---- the stream ends inside the range: write its record, move on
         const uint32_t u = u_beg + k;
-        if (u + 1 == L.s_end && k + 1 < n_tiles) {
+        if (!kOne && u + 1 == L.s_end && k + 1 < n_tiles) {
             // query rows of padding are skipped
             const int rbase = (((L.sis % a.sets) << a.side_bits) + beside) * R;
             const long long rec =
@@ -461,7 +550,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
     if (aborted) {
         // The weights kernel follows every description: none may be left unwritten.
-        if (a.scores)
+        if (!kOne && a.scores)
             for (uint32_t k = lane; k < n_tiles; k += 32) tile_src(u_beg + k, true);
         // Stages already issued must land before the CTA's shared memory goes away.
         if (lane == 0) {
@@ -502,6 +591,80 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     __syncthreads();
     constexpr int kRingFloats = C::kStages * C::kStageBytes / 4;
     const float* all = reinterpret_cast<const float*>(smem);
+    if constexpr (kOne) {
+        // The CTA's record in the place of the prefix table, then every row's over the cluster: a warp a
+        // query, both maps of it.
+        static_assert(R * D * 4 <= 4 * (kMaxSeqs + 1), "record fits the prefix table");
+        __shared__ float2 s_rec[R];
+        float* rec_o = reinterpret_cast<float*>(prefix);
+        for (int x = threadIdx.x; x < R * (D / 4); x += C::kThreads) {
+            const int r = x / (D / 4), d = 4 * (x % (D / 4));
+            float M = -INFINITY, l = 0.0f;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int p = 0; p < C::kWarps; ++p) M = fmaxf(M, s_ml[p][r].x);
+#pragma unroll
+            for (int p = 0; p < C::kWarps; ++p) {
+                const float2 ml = s_ml[p][r];
+                if (ml.y == 0.0f) continue;   // no tile, or saw nothing
+                const float wt = record_weight(ml, M);
+                const float4 v = *reinterpret_cast<const float4*>(all + p * kRingFloats + r * kPitch + d);
+                acc = make_float4(acc.x + wt * v.x, acc.y + wt * v.y, acc.z + wt * v.z, acc.w + wt * v.w);
+                l += wt * ml.y;
+            }
+            *reinterpret_cast<float4*>(rec_o + r * D + d) = acc;
+            if (d == 0) s_rec[r] = make_float2(M, l);
+        }
+        cluster.sync();
+        constexpr int V = D / 32;
+        for (int j = j_first; j < queries; j += C_one * C::kWarps) {
+            const int rq = rg_one * (R / a.maps) + j;
+            const int head = hk_one * (a.Hq / a.Hkv) + rq / a.nq, i = rq % a.nq;
+            if (j != j_first && a.maps == 2) lambda = diff_lambda(a.out.diff, head, D / 2, lane);
+            // lane c holds CTA c's (max, sum) of the query's row in each map
+            float M[2], Ls[2], wt_c[2], so[2][V];
+#pragma unroll
+            for (int mp = 0; mp < 2; ++mp) {
+                float2 ml = make_float2(-INFINITY, 0.0f);
+                if (mp < a.maps && lane < C_one)
+                    ml = cluster.map_shared_rank(s_rec, lane)[j * a.maps + mp];
+                M[mp] = ml.x;
+#pragma unroll
+                for (int sh = 1; sh < kMaxCluster; sh <<= 1)
+                    M[mp] = fmaxf(M[mp], __shfl_xor_sync(0xffffffffu, M[mp], sh));
+                M[mp] = __shfl_sync(0xffffffffu, M[mp], 0);
+                wt_c[mp] = ml.y == 0.0f ? 0.0f : record_weight(ml, M[mp]);
+                Ls[mp] = warp_sum(wt_c[mp] * ml.y);
+#pragma unroll
+                for (int e = 0; e < V; ++e) so[mp][e] = 0.0f;
+            }
+#pragma unroll
+            for (int c8 = 0; c8 < kMaxCluster; ++c8) {
+                if (c8 >= C_one) break;
+                const float* p = cluster.map_shared_rank(rec_o, c8) + j * a.maps * D + lane * V;
+#pragma unroll
+                for (int mp = 0; mp < 2; ++mp) {
+                    if (mp >= a.maps) break;
+                    const float wt = __shfl_sync(0xffffffffu, wt_c[mp], c8);
+#pragma unroll
+                    for (int e = 0; e < V; e += 2) {
+                        const float2 v = *reinterpret_cast<const float2*>(p + mp * D + e);
+                        so[mp][e] += wt * v.x;
+                        so[mp][e + 1] += wt * v.y;
+                    }
+                }
+            }
+            float out[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) out[e] = 0.0f;
+            add_map<V>(out, so[0], M[0], Ls[0], 0, lambda, a.out, one.b, head, i, a.maps, lane);
+            if (a.maps == 2)
+                add_map<V>(out, so[1], M[1], Ls[1], 1, lambda, a.out, one.b, head, i, a.maps, lane);
+            store_row<D>(out, a.maps == 2, a.out, one.b, head, i, lane);
+        }
+        cluster.sync();   // nobody leaves while another CTA reads its record
+        return;
+    }
     for (uint32_t p0 = 0, p1; p0 < sp.parts; p0 = p1) {
         const long long stream = s_stream[p0 << a.side_bits];
         for (p1 = p0 + 1; p1 < sp.parts && s_stream[p1 << a.side_bits] == stream; ++p1) {}
@@ -546,10 +709,8 @@ struct MergeArgs {
     long long tail0;
     int B, Hq, Hkv, nq, R, side_bits, sets;
     uint32_t grid, parts;   // of the decode kernel
-    __half* o;
-    float* lse;       // [B][Hq][maps][nq] or null
     float2* row_ml;   // [B][Hkv][G, made even]: (M, 1 / L) for the weights kernel, or null
-    DiffArgs diff;
+    RowOut out;
 };
 
 constexpr int kMergeMaxWarps = 16;
@@ -575,7 +736,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
     const int rg = r / a.R, n = r - rg * a.R;
     const int set = rg >> a.side_bits, per_seq = a.Hkv * a.sets, sis = hk * a.sets + set;
     float lambda = 0.0f;
-    if (kDiff && warp == 0) lambda = diff_lambda(a.diff, head, D / 2, lane);
+    if (kDiff && warp == 0) lambda = diff_lambda(a.out.diff, head, D / 2, lane);
     // Launched as a programmatic dependent of the decode grid: wait for its
     // prefix table and records before reading them.
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -668,36 +829,12 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
 #pragma unroll
             for (int e = 0; e < V; ++e) so[e] += wt * s_o[k][lane * V + e];
         }
-        const float inv = Ls == 0.0f ? 0.0f : 1.0f / Ls;
-        const float f = mp == 0 ? inv : -lambda * inv;
-#pragma unroll
-        for (int e = 0; e < V; ++e) out[e] += so[e] * f;
-        if (lane == 0) {
-            if (a.lse)
-                a.lse[((static_cast<long long>(b) * a.Hq + head) * kMaps + mp) * a.nq + i] =
-                    Ls == 0.0f ? -INFINITY : (M + log2f(Ls)) * kLn2;
-            if (!kDiff && a.row_ml)
-                a.row_ml[(static_cast<long long>(b) * a.Hkv + hk) * ((grp * a.nq + 1) & ~1) + r] =
-                    make_float2(M, inv);
-        }
+        add_map<V>(out, so, M, Ls, mp, lambda, a.out, b, head, i, kMaps, lane);
+        if (!kDiff && lane == 0 && a.row_ml)
+            a.row_ml[(static_cast<long long>(b) * a.Hkv + hk) * ((grp * a.nq + 1) & ~1) + r] =
+                make_float2(M, Ls == 0.0f ? 0.0f : 1.0f / Ls);
     }
-    if (kDiff && a.diff.norm) {
-        float sq = 0.0f;
-#pragma unroll
-        for (int e = 0; e < V; ++e) sq += out[e] * out[e];
-        const float rn = rsqrtf(warp_sum(sq) * (1.0f / D) + a.diff.eps) * (1.0f - a.diff.init);
-#pragma unroll
-        for (int e = 0; e < V; ++e) out[e] *= rn * a.diff.norm[lane * V + e];
-    }
-    __half* op = a.o + row * D + lane * V;
-    if constexpr (V == 2) {
-        *reinterpret_cast<uint32_t*>(op) = pack_half2(out[0], out[1]);
-    } else {
-#pragma unroll
-        for (int e = 0; e < V; e += 4)
-            *reinterpret_cast<uint2*>(op + e) =
-                make_uint2(pack_half2(out[e], out[e + 1]), pack_half2(out[e + 2], out[e + 3]));
-    }
+    store_row<D>(out, kDiff, a.out, b, head, i, lane);
 }
 
 // weights[slot] += sum over the group's rows of 2^(x - M) / L for every cached
@@ -850,30 +987,67 @@ size_t decode_workspace_size(int B, int Hq, int Hkv, int nq, int max_kv, int D, 
     return decode_layout(sm_count_or_default(), B, Hkv, static_cast<int>(G), max_kv, D, weights).total;
 }
 
-template <int D, int NB>
-int launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, int ctas, const DecodeF16Args& a,
-                  cudaStream_t s) {
+// CTAs of a cluster when every stream gets one (kOne), 0 when the streams' tiles are laid end to end.  A
+// cluster saves the merge kernel, the tile prefix and the records' way through memory, but its SMs read
+// one stream only, whatever the others' lengths: so where all clusters run at once and max_kv_len gives
+// a warp at most 12, 6 or 1 tiles at D = 64, 128, 256.  Measured, laid end to end against clusters, in us:
+//   1 sequence, 8 KV heads of 128    64 tokens 7.8 and 6.7,  2,048 9.9 and 8.3,  8,192 13.2 and 12.0
+//   1 sequence, 4 KV heads of 128                            4,096 10.2 and 9.4, 8,192 10.8 and 11.8
+//   16 sequences of half to all of   512 tokens, 8 KV heads of 128 15.0 and 9.0, 2,048 25.7 and 20.4
+//   8 sequences, 1 KV head of 64     512 tokens 9.7 and 6.6, 8,192 12.4 and 9.8
+//   1 sequence, 1 KV head of 256     64 tokens 8.5 and 8.5, 512 9.1 and 9.4, 2,048 11.2 and 11.6
+int cluster_of(long long streams, int max_kv, int D, int sms) {
+    const int tiles = (max_kv + kTile - 1) / kTile, per_warp = D == 64 ? 12 : D == 128 ? 6 : 1;
+    int c = kMaxCluster;
+    while (c > 1 && streams * c > sms) c /= 2;
+    return streams * c <= sms && tiles <= per_warp * c * warps_of(D) ? c : 0;
+}
+
+template <int D, int NB, bool kOne>
+int launch_decode(const CUtensorMap& tk, const CUtensorMap& tv, int ctas, int cluster,
+                  const DecodeF16Args& a, cudaStream_t s) {
     static std::once_flag once[64];
     static int rc[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return GBATTN_ERR_CUDA;
+    auto* kernel = decode_f16_kernel<D, NB, kOne>;
     std::call_once(once[dev], [&] {
-        rc[dev] = cudaFuncSetAttribute(decode_f16_kernel<D, NB>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
+        rc[dev] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        Cfg<D>::kSmem) == cudaSuccess
                       ? GBATTN_OK
                       : GBATTN_ERR_CUDA;
     });
     if (rc[dev] != GBATTN_OK) return rc[dev];
-    decode_f16_kernel<D, NB><<<ctas, Cfg<D>::kThreads, Cfg<D>::kSmem, s>>>(tk, tv, a);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(ctas));
+    cfg.blockDim = dim3(Cfg<D>::kThreads);
+    cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = kOne ? 1 : 0;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, tk, tv, a);
     count_launches(1);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return GBATTN_ERR_CUDA;
+    }
     return launch_status();
 }
 
+// cluster: CTAs of a stream's cluster, or 0.
 template <int D>
-int launch_decode_rows(int R, const CUtensorMap& tk, const CUtensorMap& tv, int ctas,
+int launch_decode_rows(int R, const CUtensorMap& tk, const CUtensorMap& tv, int ctas, int cluster,
                        const DecodeF16Args& a, cudaStream_t s) {
-    return R == 8 ? launch_decode<D, 1>(tk, tv, ctas, a, s) : launch_decode<D, 2>(tk, tv, ctas, a, s);
+    if (cluster)
+        return R == 8 ? launch_decode<D, 1, true>(tk, tv, ctas, cluster, a, s)
+                      : launch_decode<D, 2, true>(tk, tv, ctas, cluster, a, s);
+    return R == 8 ? launch_decode<D, 1, false>(tk, tv, ctas, 1, a, s)
+                  : launch_decode<D, 2, false>(tk, tv, ctas, 1, a, s);
 }
 
 // A launch whose CTAs may be placed while the grid before it on the stream still
@@ -1023,12 +1197,14 @@ int run_decode(const DecodeCall& c) {
     a.max_kv = c.max_kv;
     a.maps = maps;
     a.sl2 = c.scale * 1.4426950408889634f;
+    a.out = RowOut{static_cast<__half*>(c.o), c.lse, c.Hq, c.nq, c.diff ? *c.diff : DiffArgs{}};
     cudaStream_t s = static_cast<cudaStream_t>(c.stream);
-    const int n = static_cast<int>(ctas);
-    rc = c.D == 64    ? launch_decode_rows<64>(R, tk, tv, n, a, s)
-         : c.D == 128 ? launch_decode_rows<128>(R, tk, tv, n, a, s)
-                      : launch_decode_rows<256>(R, tk, tv, n, a, s);
-    if (rc != GBATTN_OK) return rc;
+    const int cl = c.weights || plan.side > 1 ? 0 : cluster_of(streams, c.max_kv, c.D, dev.num_sms);
+    const int n = static_cast<int>(cl ? streams * cl : ctas);
+    rc = c.D == 64    ? launch_decode_rows<64>(R, tk, tv, n, cl, a, s)
+         : c.D == 128 ? launch_decode_rows<128>(R, tk, tv, n, cl, a, s)
+                      : launch_decode_rows<256>(R, tk, tv, n, cl, a, s);
+    if (rc != GBATTN_OK || cl) return rc;
 
     MergeArgs m{};
     m.part_o = a.part_o;
@@ -1044,10 +1220,8 @@ int run_decode(const DecodeCall& c) {
     m.tail0 = a.tail0;
     m.grid = static_cast<uint32_t>(ctas);
     m.parts = static_cast<uint32_t>(warps_of(c.D) / plan.side);
-    m.o = static_cast<__half*>(c.o);
-    m.lse = c.lse;
+    m.out = a.out;
     m.row_ml = c.weights ? reinterpret_cast<float2*>(wsp + lay.row_ml) : nullptr;
-    if (c.diff) m.diff = *c.diff;
     // Warps per row by the records of an average row (a map of a row): one up to a batch of 8.
     const long long recs = ctas * plan.side / streams + 1;
     const int mw = (recs > 32 ? 8 : recs > 8 ? 4 : 1) * maps;

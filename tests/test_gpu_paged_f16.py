@@ -191,6 +191,35 @@ def test_decode_most_sequences(gb):
         check_decode(gb, *inputs.paged_f16_inputs(4096, 1, 1, 1, lens, D, 23, page_size=16))
 
 
+@pytest.mark.parametrize("Hq,Hkv,nq", [(1, 1, 1), (6, 1, 2), (16, 2, 2), (20, 1, 2)])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("max_kv", [None, 300000])
+def test_decode_short_caches_both_ways(gb, Hq, Hkv, nq, D, max_kv):
+    """Lengths from none to 700, in clusters of eight CTAs a stream down to one, and under a bound so
+    far above them that the streams' tiles are laid end to end."""
+    for lens in ((700,), (1, 0, 17, 300), tuple(range(40)), tuple(range(5, 300, 4))):
+        q, kp, vp, table, lens, _ = inputs.paged_f16_inputs(len(lens), Hq, Hkv, nq, lens, D, 50,
+                                                            page_size=16, poison=True)
+        if max_kv is not None:
+            wide = np.full((len(lens), max_kv // 16), -1, dtype=np.int32)
+            wide[:, :table.shape[1]] = table
+            table = wide
+        check_decode(gb, q, kp, vp, table, lens, max_kv=max_kv)
+
+
+def test_decode_bad_length_in_clusters(gb):
+    q, kp, vp, table, lens, _ = inputs.paged_f16_inputs(3, 4, 2, 1, (90, 100, 50), 64, 51, page_size=16)
+    bad, bad_lens = table.copy(), lens.copy()
+    bad[0, 2] = -7
+    bad_lens[2] = 5000
+    lse = torch.zeros((3, 4, 1), device=DEV)
+    o = gb.attn_paged_decode_f16_fwd(t(q), t(kp), t(vp), t(bad), t(bad_lens), lse=lse)
+    assert gb.device_status() == gb.DEV_BAD_LENGTH | gb.DEV_BAD_PAGE
+    assert torch.all(o[2] == 0) and torch.all(torch.isneginf(lse[2]))
+    ref = OP.decode(q[1:2], kp, vp, table[1:2], lens[1:2], inputs.softmax_scale(64))
+    assert np.abs(o[1].float().cpu().numpy() - ref["o"][0]).max() < 2e-3
+
+
 def test_decode_smaller_workspace_and_refusals(gb):
     case = inputs.paged_f16_inputs(2, 8, 2, 1, (3000, 700), 128, 16)
     full = gb.attn_paged_decode_f16_workspace_size(2, 8, 2, 1, 3008, 128, True)
