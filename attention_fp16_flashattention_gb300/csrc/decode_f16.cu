@@ -31,8 +31,8 @@
 //     sum, a third kernel adds sum_r 2^(x - max) / sum to every token's weight.
 //     Every (token, KV head) is added to once per call, so the result does not
 //     depend on any order unless two sequences share a page.
-//   * Short caches without weights: a cluster of up to eight CTAs takes each stream, and
-//     joins the partials through its shared memory; one kernel (rule at cluster_of).
+//   * Short caches: a cluster of up to eight CTAs takes each stream, joins the partials
+//     through its shared memory and adds the weights; one kernel (rule at cluster_of).
 // Measured (graph replays): 4 sequences of 65,571 to 131,072 tokens, 6 query heads on
 // one KV head of 256 (450 MB) 75 us, 6.0 TB/s, 0.89 of the measured copy; 32 of 257
 // to 8,191, 32 on 8 of 128, with weights (581 MB) 110 us, 15 of them for the weights (a
@@ -107,6 +107,7 @@ struct DecodeF16Args {
     int maps;             // 1, or 2: row r is map r % 2 of query r / 2
     float sl2;            // softmax scale * log2(e)
     RowOut out;           // a cluster a stream: where its rows go
+    float* weights;       // and their weights, with `scores`
 };
 
 __device__ __forceinline__ uint32_t h2_bits(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
@@ -390,6 +391,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const int hk_one = one.sis / a.sets, rg_one = one.sis - hk_one * a.sets;
     const int queries = min(R, a.G - rg_one * R) / a.maps;   // R and G are multiples of maps
     const int j_first = static_cast<int>(cta) * C::kWarps + warp;
+    const long long one_tile0 = (static_cast<long long>(one.b) * per_seq + one.sis) *
+                                ((a.max_kv + kTile - 1) / kTile);   // the stream's tiles in `scores`
     float lambda = 0.0f;
     if constexpr (kOne) {
         if (a.maps == 2 && j_first < queries)
@@ -446,10 +449,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 if (t1 > lim[n][0]) x[2] = -INFINITY;
                 if (t1 > lim[n][1]) x[3] = -INFINITY;
             }
-            if (!kOne && a.scores) {
+            if (a.scores) {
                 const int r0 = 8 * n + 2 * c;
                 const int real = a.G - (((L.sis % a.sets) << a.side_bits) + beside) * R;
-                const long long tile = (static_cast<long long>(u_beg + k) << a.side_bits) + beside;
+                const long long tile = kOne ? one_tile0 + u_beg + k
+                                            : (static_cast<long long>(u_beg + k) << a.side_bits) + beside;
                 if (r0 < real)
                     store_f32x4_hint(a.scores + (tile * a.pairs + r0 / 2) * (2 * kTile) + 4 * g, x, keep);
             }
@@ -616,6 +620,50 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (d == 0) s_rec[r] = make_float2(M, l);
         }
         cluster.sync();
+        if (a.scores) {
+            // The weights, by the lanes that hold the scores: every row's joint max and sum, then
+            // sum_r 2^(x - max) / sum over the lane's rows and the four lanes of a token.
+            __shared__ float2 s_row[R];
+            if (threadIdx.x < R) {
+                float M = -INFINITY, l = 0.0f;
+                for (int c8 = 0; c8 < C_one; ++c8)
+                    M = fmaxf(M, cluster.map_shared_rank(s_rec, c8)[threadIdx.x].x);
+                for (int c8 = 0; c8 < C_one; ++c8) {
+                    const float2 ml = cluster.map_shared_rank(s_rec, c8)[threadIdx.x];
+                    l += ml.y == 0.0f ? 0.0f : record_weight(ml, M) * ml.y;
+                }
+                s_row[threadIdx.x] = make_float2(M, l == 0.0f ? 0.0f : 1.0f / l);
+            }
+            __syncthreads();
+            for (uint32_t k = 0; k < (aborted ? 0u : n_tiles); ++k) {
+                const int tok = static_cast<int>(u_beg + k) * kTile;
+                const int page = a.table[static_cast<long long>(one.b) * a.max_pages + tok / a.ps];
+                float w0 = 0.0f, w1 = 0.0f;   // tokens g and g + 8
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    const int r0 = 8 * n + 2 * c;
+                    if (r0 >= a.G) continue;
+                    const float4 x = *reinterpret_cast<const float4*>(
+                        a.scores + ((one_tile0 + u_beg + k) * a.pairs + r0 / 2) * (2 * kTile) + 4 * g);
+                    const float2 m0 = s_row[r0], m1 = s_row[r0 + 1];
+                    if (x.x != -INFINITY) w0 += fast_exp2(x.x - m0.x) * m0.y;
+                    if (x.z != -INFINITY) w1 += fast_exp2(x.z - m0.x) * m0.y;
+                    if (r0 + 1 < a.G) {   // an odd last row has no partner
+                        if (x.y != -INFINITY) w0 += fast_exp2(x.y - m1.x) * m1.y;
+                        if (x.w != -INFINITY) w1 += fast_exp2(x.w - m1.x) * m1.y;
+                    }
+                }
+#pragma unroll
+                for (int sh = 1; sh < 4; sh <<= 1) {
+                    w0 += __shfl_xor_sync(0xffffffffu, w0, sh);
+                    w1 += __shfl_xor_sync(0xffffffffu, w1, sh);
+                }
+                const int t = tok + g + 8 * c;   // lane c = 0 adds token g's, c = 1 token g + 8's
+                if (c < 2 && t < kv_len && page >= 0 && page < a.num_phys)
+                    atomicAdd(a.weights + (static_cast<long long>(page) * a.Hkv + hk_one) * a.ps + t % a.ps,
+                              c == 0 ? w0 : w1);
+            }
+        }
         constexpr int V = D / 32;
         for (int j = j_first; j < queries; j += C_one * C::kWarps) {
             const int rq = rg_one * (R / a.maps) + j;
@@ -1197,9 +1245,11 @@ int run_decode(const DecodeCall& c) {
     a.max_kv = c.max_kv;
     a.maps = maps;
     a.sl2 = c.scale * 1.4426950408889634f;
+    a.weights = c.weights;
     a.out = RowOut{static_cast<__half*>(c.o), c.lse, c.Hq, c.nq, c.diff ? *c.diff : DiffArgs{}};
     cudaStream_t s = static_cast<cudaStream_t>(c.stream);
-    const int cl = c.weights || plan.side > 1 ? 0 : cluster_of(streams, c.max_kv, c.D, dev.num_sms);
+    // (row groups of their own would add to the weights in any order)
+    const int cl = plan.side > 1 || (c.weights && plan.groups > 1) ? 0 : cluster_of(streams, c.max_kv, c.D, dev.num_sms);
     const int n = static_cast<int>(cl ? streams * cl : ctas);
     rc = c.D == 64    ? launch_decode_rows<64>(R, tk, tv, n, cl, a, s)
          : c.D == 128 ? launch_decode_rows<128>(R, tk, tv, n, cl, a, s)

@@ -198,26 +198,29 @@ def test_decode_short_caches_both_ways(gb, Hq, Hkv, nq, D, max_kv):
     """Lengths from none to 700, in clusters of eight CTAs a stream down to one, and under a bound so
     far above them that the streams' tiles are laid end to end."""
     for lens in ((700,), (1, 0, 17, 300), tuple(range(40)), tuple(range(5, 300, 4))):
-        q, kp, vp, table, lens, _ = inputs.paged_f16_inputs(len(lens), Hq, Hkv, nq, lens, D, 50,
+        q, kp, vp, table, lens, w = inputs.paged_f16_inputs(len(lens), Hq, Hkv, nq, lens, D, 50,
                                                             page_size=16, poison=True)
         if max_kv is not None:
             wide = np.full((len(lens), max_kv // 16), -1, dtype=np.int32)
             wide[:, :table.shape[1]] = table
             table = wide
         check_decode(gb, q, kp, vp, table, lens, max_kv=max_kv)
+        check_decode(gb, q, kp, vp, table, lens, w, max_kv=max_kv)
 
 
 def test_decode_bad_length_in_clusters(gb):
-    q, kp, vp, table, lens, _ = inputs.paged_f16_inputs(3, 4, 2, 1, (90, 100, 50), 64, 51, page_size=16)
+    q, kp, vp, table, lens, w = inputs.paged_f16_inputs(3, 4, 2, 1, (90, 100, 50), 64, 51, page_size=16)
     bad, bad_lens = table.copy(), lens.copy()
     bad[0, 2] = -7
     bad_lens[2] = 5000
-    lse = torch.zeros((3, 4, 1), device=DEV)
-    o = gb.attn_paged_decode_f16_fwd(t(q), t(kp), t(vp), t(bad), t(bad_lens), lse=lse)
+    tw, lse = t(w), torch.zeros((3, 4, 1), device=DEV)
+    o = gb.attn_paged_decode_f16_fwd(t(q), t(kp), t(vp), t(bad), t(bad_lens), lse=lse, weights=tw)
     assert gb.device_status() == gb.DEV_BAD_LENGTH | gb.DEV_BAD_PAGE
     assert torch.all(o[2] == 0) and torch.all(torch.isneginf(lse[2]))
     ref = OP.decode(q[1:2], kp, vp, table[1:2], lens[1:2], inputs.softmax_scale(64))
     assert np.abs(o[1].float().cpu().numpy() - ref["o"][0]).max() < 2e-3
+    gone = np.concatenate([table[0, 2:3], table[2, :4]])   # the bad page's tokens, the bad length's
+    assert np.array_equal(tw.cpu().numpy()[gone], w[gone])
 
 
 def test_decode_smaller_workspace_and_refusals(gb):
