@@ -1044,6 +1044,8 @@ size_t decode_workspace_size(int B, int Hq, int Hkv, int nq, int max_kv, int D, 
 //   16 sequences of half to all of   512 tokens, 8 KV heads of 128 15.0 and 9.0, 2,048 25.7 and 20.4
 //   8 sequences, 1 KV head of 64     512 tokens 9.7 and 6.6, 8,192 12.4 and 9.8
 //   1 sequence, 1 KV head of 256     64 tokens 8.5 and 8.5, 512 9.1 and 9.4, 2,048 11.2 and 11.6
+//   with weights: 1 sequence, 8 KV heads of 128   512 tokens 11.6 and 8.9, 2,048 12.6 and 11.1, 4,096 13.2
+//   and 13.8; 16 of half to all of 512 tokens 17.1 and 12.5
 int cluster_of(long long streams, int max_kv, int D, int sms) {
     const int tiles = (max_kv + kTile - 1) / kTile, per_warp = D == 64 ? 12 : D == 128 ? 6 : 1;
     int c = kMaxCluster;
