@@ -324,8 +324,9 @@ int kv_paged_append_f16(const void* k_new, const void* v_new, void* k_pages, voi
  *   [0, max_kv_len] sets GBATTN_DEV_BAD_LENGTH and yields O = 0, lse = -inf for that sequence.  An
  *   out-of-range page-table entry sets GBATTN_DEV_BAD_PAGE (that page reads physical page 0, and
  *   its tokens' weights stay as they are).
- *   The work is split over the warps of a persistent grid as in attn_paged_decode_fwd, and the
- *   workspace rules are the same: attn_paged_decode_f16_workspace_size() gives the full-speed size
+ *   The work is split over the warps of a persistent grid as in attn_paged_decode_fwd (where
+ *   max_kv_len is small a thread-block cluster takes each stream, in one kernel), and the workspace
+ *   rules are the same: attn_paged_decode_f16_workspace_size() gives the full-speed size
  *   (weights != 0 adds about one FP32 score per query row and cached token, for max_kv_len tokens of
  *   every sequence), a smaller one runs fewer warps, and below one CTA's worth the call returns
  *   GBATTN_ERR_WORKSPACE.  The workspace needs no initial value; calls that may run at the same
