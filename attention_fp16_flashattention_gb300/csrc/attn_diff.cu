@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int lim = visible(it.n, it.qt * kBM + (warp & 3) * 32 + lane, a.causal) - it.tile0 * kBN;
         int left = it.n_tiles;
         {
-            const float lambda = diff_lambda(a.diff, it.bh % a.Hq, kD / 2, lane);
+            const float lambda = diff_lambda<kD / 2>(a.diff, it.bh % a.Hq, lane);
             if (lane == 0) items.lambda = lambda;
         }
         float m_run = -INFINITY, l = 0.0f;
@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(256) attn_diff_merge_kernel(const DiffPrefillA
     const int row = static_cast<int>(blockIdx.y) * 8 + static_cast<int>(threadIdx.x >> 5);
     const int bh = u / a.q_tiles, row_g = (u - bh * a.q_tiles) * kBM + row;
     const int b = bh / a.Hq, head = bh - b * a.Hq;
-    const float lambda = diff_lambda(a.diff, head, kD / 2, lane);
+    const float lambda = diff_lambda<kD / 2>(a.diff, head, lane);
     // a programmatic dependent of the attention grid
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (row_g >= a.Sq) return;

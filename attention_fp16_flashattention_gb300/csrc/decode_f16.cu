@@ -158,9 +158,15 @@ __device__ __forceinline__ void add_map(float (&out)[V], const float (&so)[V], f
         t.lse[((static_cast<long long>(b) * t.Hq + head) * maps + mp) * t.nq + i] =
             Ls == 0.0f ? -INFINITY : (M + log2f(Ls)) * kLn2;
 }
+// The lane's norm weights, loaded where there is time for it.
+template <int V>
+__device__ __forceinline__ void load_norm(float (&gain)[V], bool diff, const RowOut& t, int lane) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) gain[e] = diff && t.diff.norm ? t.diff.norm[lane * V + e] : 1.0f;
+}
 template <int D>
-__device__ __forceinline__ void store_row(float (&out)[D / 32], bool diff, const RowOut& t, int b,
-                                          int head, int i, int lane) {
+__device__ __forceinline__ void store_row(float (&out)[D / 32], const float (&gain)[D / 32], bool diff,
+                                          const RowOut& t, int b, int head, int i, int lane) {
     constexpr int V = D / 32;
     if (diff && t.diff.norm) {
         float sq = 0.0f;
@@ -168,7 +174,7 @@ __device__ __forceinline__ void store_row(float (&out)[D / 32], bool diff, const
         for (int e = 0; e < V; ++e) sq += out[e] * out[e];
         const float rn = rsqrtf(warp_sum(sq) * (1.0f / D) + t.diff.eps) * (1.0f - t.diff.init);
 #pragma unroll
-        for (int e = 0; e < V; ++e) out[e] *= rn * t.diff.norm[lane * V + e];
+        for (int e = 0; e < V; ++e) out[e] *= rn * gain[e];
     }
     __half* op = t.o + ((static_cast<long long>(b) * t.Hq + head) * t.nq + i) * D + lane * V;
     if constexpr (V == 2) {
@@ -387,17 +393,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const int k_row = lane & 15, k_ch = lane >> 4;
     const int v_row = (lane & 7) + ((lane >> 4) << 3), v_ch = (lane >> 3) & 1;
 
-    // kOne: the warp's first query at the end and its lambda, which need not wait until then
+    // kOne: the warp's first query at the end; what its lambda and norm need is on its way from here
     const int hk_one = one.sis / a.sets, rg_one = one.sis - hk_one * a.sets;
     const int queries = min(R, a.G - rg_one * R) / a.maps;   // R and G are multiples of maps
     const int j_first = static_cast<int>(cta) * C::kWarps + warp;
     const long long one_tile0 = (static_cast<long long>(one.b) * per_seq + one.sis) *
                                 ((a.max_kv + kTile - 1) / kTile);   // the stream's tiles in `scores`
-    float lambda = 0.0f;
+    // (kOne: D == 128 in the differential form)
+    LambdaTerms<64> terms{};
+    float gain[D / 32] = {};
     if constexpr (kOne) {
-        if (a.maps == 2 && j_first < queries)
-            lambda = diff_lambda(a.out.diff, hk_one * (a.Hq / a.Hkv) + (rg_one * (R / 2) + j_first) / a.nq,
-                                 D / 2, lane);
+        const bool diff = D == 128 && a.maps == 2 && j_first < queries;
+        if (diff)
+            terms.load(a.out.diff, hk_one * (a.Hq / a.Hkv) + (rg_one * (R / 2) + j_first) / a.nq, lane);
+        load_norm<D / 32>(gain, diff, a.out, lane);
     }
 
     bool aborted = false;
@@ -668,7 +677,11 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         for (int j = j_first; j < queries; j += C_one * C::kWarps) {
             const int rq = rg_one * (R / a.maps) + j;
             const int head = hk_one * (a.Hq / a.Hkv) + rq / a.nq, i = rq % a.nq;
-            if (j != j_first && a.maps == 2) lambda = diff_lambda(a.out.diff, head, D / 2, lane);
+            float lambda = 0.0f;
+            if (D == 128 && a.maps == 2) {
+                if (j != j_first) terms.load(a.out.diff, head, lane);
+                lambda = terms.value(a.out.diff);
+            }
             // lane c holds CTA c's (max, sum) of the query's row in each map
             float M[2], Ls[2], wt_c[2], so[2][V];
 #pragma unroll
@@ -708,7 +721,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             add_map<V>(out, so[0], M[0], Ls[0], 0, lambda, a.out, one.b, head, i, a.maps, lane);
             if (a.maps == 2)
                 add_map<V>(out, so[1], M[1], Ls[1], 1, lambda, a.out, one.b, head, i, a.maps, lane);
-            store_row<D>(out, a.maps == 2, a.out, one.b, head, i, lane);
+            store_row<D>(out, gain, a.maps == 2, a.out, one.b, head, i, lane);
         }
         cluster.sync();   // nobody leaves while another CTA reads its record
         return;
@@ -788,7 +801,11 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
     const int rg = r / a.R, n = r - rg * a.R;
     const int set = rg >> a.side_bits, per_seq = a.Hkv * a.sets, sis = hk * a.sets + set;
     float lambda = 0.0f;
-    if (kDiff && warp == 0) lambda = diff_lambda(a.out.diff, head, D / 2, lane);
+    float gain[V];
+    load_norm<V>(gain, kDiff && warp == 0, a.out, lane);
+    if constexpr (kDiff) {
+        if (warp == 0) lambda = diff_lambda<D / 2>(a.out.diff, head, lane);
+    }
     // Launched as a programmatic dependent of the decode grid.  With few sequences the tiles before
     // this one's are summed up from the lengths while that runs; else the grid's prefix table is read.
     uint32_t T = 0, before = 0, U = 0;
@@ -904,7 +921,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
             a.row_ml[(static_cast<long long>(b) * a.Hkv + hk) * ((grp * a.nq + 1) & ~1) + r] =
                 make_float2(M, Ls == 0.0f ? 0.0f : 1.0f / Ls);
     }
-    store_row<D>(out, kDiff, a.out, b, head, i, lane);
+    store_row<D>(out, gain, kDiff, a.out, b, head, i, lane);
 }
 
 // weights[slot] += sum over the group's rows of 2^(x - M) / L for every cached

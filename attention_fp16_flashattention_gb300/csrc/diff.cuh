@@ -24,17 +24,38 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// lambda of query head `head`, computed by a whole warp (d = head width of one map).
-__device__ __forceinline__ float diff_lambda(const DiffArgs& f, int head, int d, int lane) {
-    const int h = f.heads == 1 ? 0 : head;
-    const size_t plane = static_cast<size_t>(f.heads) * d;
-    const float* p = f.vecs + static_cast<size_t>(h) * d;
-    float a = 0.0f, b = 0.0f;
-    for (int i = lane; i < d; i += 32) {
-        a = fmaf(p[i], p[plane + i], a);
-        b = fmaf(p[2 * plane + i], p[3 * plane + i], b);
+// lambda of query head `head`, computed by a whole warp (kHalf = head width of one map), in two parts, so
+// that the loads can be under way long before the sums are due.
+template <int kHalf>
+struct LambdaTerms {
+    float q1[kHalf / 32], k1[kHalf / 32], q2[kHalf / 32], k2[kHalf / 32];
+    __device__ __forceinline__ void load(const DiffArgs& f, int head, int lane) {
+        const int h = f.heads == 1 ? 0 : head;
+        const size_t plane = static_cast<size_t>(f.heads) * kHalf;
+        const float* p = f.vecs + static_cast<size_t>(h) * kHalf;
+#pragma unroll
+        for (int i = 0; i < kHalf / 32; ++i) {
+            q1[i] = p[lane + 32 * i];
+            k1[i] = p[plane + lane + 32 * i];
+            q2[i] = p[2 * plane + lane + 32 * i];
+            k2[i] = p[3 * plane + lane + 32 * i];
+        }
     }
-    return expf(warp_sum(a)) - expf(warp_sum(b)) + f.init;
+    __device__ __forceinline__ float value(const DiffArgs& f) const {
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kHalf / 32; ++i) {
+            a = fmaf(q1[i], k1[i], a);
+            b = fmaf(q2[i], k2[i], b);
+        }
+        return expf(warp_sum(a)) - expf(warp_sum(b)) + f.init;
+    }
+};
+template <int kHalf>
+__device__ __forceinline__ float diff_lambda(const DiffArgs& f, int head, int lane) {
+    LambdaTerms<kHalf> t;
+    t.load(f, head, lane);
+    return t.value(f);
 }
 
 }  // namespace gbattn
