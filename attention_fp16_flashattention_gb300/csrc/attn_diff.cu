@@ -1,28 +1,35 @@
 // Differential attention of prompts on sm_103a (D = 128, two maps of width 64 over one V):
 //   O = (softmax(scale q1 k1^T) - lambda_h softmax(scale q2 k2^T)) V, then diff.cuh's normalisation,
-// with FP16 Q/K/V/P/O, FP32 accumulation in tensor memory and an FP32 online softmax per map.  Causal
-// or not, shared-KV heads, ragged query and key lengths, key ranges split over CTAs when there are
-// few query rows.
+// with FP16 Q/K/V/O, P as FP16 hi + lo, FP32 accumulation in tensor memory and an FP32 online softmax
+// per map.  Causal or not, shared-KV heads, ragged query and key lengths, key ranges split over CTAs
+// when there are few query rows.
 //
 // Mathematics and work.  O1 = P1 V and O2 = P2 V are accumulated apart: each map has its own running
 // max and sum, and only O1 / l1 - lambda O2 / l2 at the end joins them.  A visible (query, key) pair
 // costs 2 * 64 FLOPs of QK and 2 * 128 of PV per map: 768 in all, against 512 for an ordinary head,
-// and two exponentials instead of one.  So the tensor pipe bounds it (1536 cycles per 128 x 128 tile)
-// with the softmax close behind.
+// and two exponentials instead of one.
+//
+// P is rounded to two FP16 halves, hi = RNE(p) and lo = RNE(p - hi), 2^-22 of p.  What the maps have
+// in common cancels in the difference and the norm brings the rest back to unit size, so P's rounding
+// grows as the output shrinks: with one FP16 value the error against float64 was 2.6 to 3.2e-4 of
+// unrelated maps' output and 9.9e-4 of maps correlated by 0.999 (lambda 0.78), of which the output's
+// own rounding is 2.1e-4.  The second half costs another PV: 1280 tensor cycles per 64 keys and both
+// maps instead of 768, and a third of the softmax's instructions.
 //
 // Persistent CTAs, one per SM, work through items: a 128-row query tile of one head (a unit) and its
-// 128-key tiles, or a part of them.  A step is one map of one key tile; the steps alternate between
+// 64-key tiles, or a part of them.  A step is one map of one key tile; the steps alternate between
 // the maps, so both maps use each K and V tile while it is in shared memory.  Warp roles (352 threads):
 //   warp 0      TMA producer: Q of each item into one of two buffers, then K_0, V_0, K_1, V_1, ...
-//               through a ring of 32 KB slots, on into the next item.
+//               through a ring of 16 KB slots, on into the next item.
 //   warp 1      allocates tensor memory and issues S_m = Q_m K_m^T (SMEM x SMEM, 4 MMAs).
-//   warp 10     issues O_m += P_m V (P from TMEM).
+//   warp 10     issues O_m += hi_m V + lo_m V (P from TMEM).
 //   warps 2..5, 6..9  softmax of map 0, of map 1: one thread per query row (TMEM lane = row); at an
 //               item's end each takes half of the columns of both O, and the next item's QK runs
 //               under this epilogue.
-// Tensor memory (512 columns): one S, P of each map (FP16 pairs), O of each map.  S is handed back as
-// soon as the softmax has it in registers, so the other map's QK runs under this one's exponentials,
-// and PV of a tile under the next tile's.
+// Tensor memory (512 columns): S of each map (64), P of each map (FP16 pairs: 32 hi, 32 lo), O of each
+// map (128).  With 128 keys a tile, hi and lo would leave no columns for S beside them.  S is handed
+// back as soon as the softmax has it in registers, so the next tile's QK runs under this one's
+// exponentials, and PV of a tile under the next tile's.
 //
 // Which CTA does what: with many units, whole units, the longest (causal) first, in rounds that run
 // over the CTAs forth and back, so that every CTA gets the same work to about one key tile a round.
@@ -30,14 +37,12 @@
 // range of them (as the decode kernels do); the parts of a unit that ranges cut leave unnormalised
 // O_m, max and sum in `workspace`, and a merge kernel joins them.
 //
-// Measured: 16 heads x 8192 causal 272 to 284 us on several GPUs (1450 to 1516 useful TFLOP/s, 0.77 to
-// 0.80 of the measured burst; tensor pipe 66% active under ncu; 310 us in long runs under the power
-// cap), 500 queries on 32,500 keys 162 to 179 us.  How it got there (the first case):
-// both maps' softmax on eight warps in step, P over S 350 us (the softmax alone, without any MMA,
-// took 320); a warpgroup per map and S handed back early into registers 294; persistent CTAs 284;
-// PV in two halves 275.  Without softmax the MMA handshakes take 232 us, and the softmax without
-// MMAs 252.  Slower: 16 softmax warps on one step (372) or eight per map (305), exponentials against
-// the last reference while the max is still being found (336), P released by halves (301).
+// Measured (graph replays): 16 heads x 8192 causal 420 us, 500 queries on 32,500 keys 240 us.  The
+// softmax's chain bounds it: without any softmax the first takes 358 us, without MMAs (one k-step
+// each) 430, without the lo halves in softmax and PV 342.  Of a softmax warp's 1,750 cycles per tile
+// 800 are the exponentials with both roundings, 256 and 211 the waits for S and for the P buffer, 180
+// the maximum, 240 loads and stores.  Slower: P written in two or four chunks between the
+// exponentials (457 to 492), PV's lo half without a gap behind its hi half (434).
 //
 // Every wait is bounded in time (see WaitCtl): a wait that runs out records
 // GBATTN_DEV_WAIT_TIMEOUT in the device status word, the CTA stops, waits a
@@ -58,16 +63,18 @@ namespace {
 
 constexpr int kD = 128;              // head width: two maps of 64, values of 128
 constexpr int kBM = 128;             // query rows per CTA
-constexpr int kBN = 128;             // keys per tile (two halves of 64)
-constexpr int kNS = 4;               // K/V ring slots (even: K tiles, odd: V tiles)
+constexpr int kBN = 64;              // keys per tile
+constexpr int kNS = 8;               // K/V ring slots (even: K tiles, odd: V tiles)
 constexpr int kThreads = 352;
 constexpr int kPvWarp = 10;
 constexpr int kSoftmaxThreads = 128;   // per map
-constexpr int kChunk = 128 * 128;    // 128 rows x 64 FP16 columns
+constexpr int kQChunk = kBM * 128;   // 64 FP16 columns of a Q tile's rows
+constexpr int kKvChunk = kBN * 128;  // and of a K or V tile's
 constexpr int kQBytes = kBM * kD * 2;
 constexpr int kSlotBytes = kBN * kD * 2;
-// Tensor memory columns: S, then P of map 0 and of map 1 (FP16 pairs), then O of map 0 and of map 1.
-constexpr uint32_t kTP = 128, kTO = 256;
+// Tensor memory columns: S of each map, P of each map (FP16 pairs: 32 columns of hi, 32 of lo), O of
+// each map.
+constexpr uint32_t kTS = 64, kTP = 128, kTPMap = 64, kTPLo = 32, kTO = 256;
 constexpr uint32_t kIdescQK = idesc_f16(kBM, kBN, false, false);
 constexpr uint32_t kIdescPV = idesc_f16(kBM, kD, false, true);
 constexpr uint64_t kDrainNs = 200000000ull;   // 0.2 s for draining after an abort
@@ -99,7 +106,7 @@ struct Ctrl {
     uint64_t full[kNS];
     uint64_t empty[kNS];
     uint64_t s_full[2];       // S of a map's tile computed
-    uint64_t s_free;          // S read into registers (once per step)
+    uint64_t s_free[2];       // S of a map read into registers
     uint64_t p_full[2];       // P of a map written
     uint64_t pv_done[2];      // PV of a map done: its P buffer is free, its O up to date
     uint64_t o_free;          // an item's O read into registers
@@ -118,9 +125,10 @@ struct Exchange {
     float norm[128];       // the norm weight * (1 - lambda_init)
 };
 
-constexpr int kCtrlBytes = 256 + static_cast<int>(sizeof(Exchange));
+constexpr int kBarBytes = 320;
+constexpr int kCtrlBytes = kBarBytes + static_cast<int>(sizeof(Exchange));
 constexpr int kItemBytes = 64;       // a warp's place in its items
-static_assert(sizeof(Ctrl) <= 256, "control block");
+static_assert(sizeof(Ctrl) <= kBarBytes, "control block");
 constexpr int kMaxUnits = 512;       // units of a split launch (prefix table in shared memory)
 constexpr int kSmemBytes = 1024 + 2 * kQBytes + kNS * kSlotBytes + kCtrlBytes +
                            kItemBytes * (kThreads / 32) + 4 * (kMaxUnits + 4);
@@ -245,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t* sQ = smem;
     uint8_t* sKV = smem + 2 * kQBytes;
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(sKV + kNS * kSlotBytes);
-    Exchange* ex = reinterpret_cast<Exchange*>(reinterpret_cast<uint8_t*>(ctrl) + 256);
+    Exchange* ex = reinterpret_cast<Exchange*>(reinterpret_cast<uint8_t*>(ctrl) + kBarBytes);
     uint8_t* item_mem = reinterpret_cast<uint8_t*>(ctrl) + kCtrlBytes;
     uint32_t* prefix = reinterpret_cast<uint32_t*>(item_mem + kItemBytes * (kThreads / 32));
 
@@ -261,10 +269,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctrl->q_full[i], 1);
             mbar_init(&ctrl->q_empty[i], 1);
             mbar_init(&ctrl->s_full[i], 1);
+            mbar_init(&ctrl->s_free[i], kSoftmaxThreads);
             mbar_init(&ctrl->p_full[i], kSoftmaxThreads);
             mbar_init(&ctrl->pv_done[i], 1);
         }
-        mbar_init(&ctrl->s_free, kSoftmaxThreads);
         mbar_init(&ctrl->o_free, 2 * kSoftmaxThreads);
         for (int i = 0; i < 4; ++i) mbar_init(&ctrl->xchg[i], 64);
         mbar_init(&ctrl->drain, 1);
@@ -337,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mbar_arrive_expect_tx(&ctrl->q_full[qb], kQBytes);
 #pragma unroll
                 for (int c = 0; c < 2; ++c)
-                    tma_load_4d(sQ + qb * kQBytes + c * kChunk, &tmQ, &ctrl->q_full[qb], c * 64,
+                    tma_load_4d(sQ + qb * kQBytes + c * kQChunk, &tmQ, &ctrl->q_full[qb], c * 64,
                                 it.qt * kBM, head, b);
             }
             __syncwarp();
@@ -357,16 +365,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive_expect_tx(&ctrl->full[slot], kSlotBytes);
 #pragma unroll
                     for (int c = 0; c < 2; ++c)
-                        tma_load_4d(dst + c * kChunk, m, &ctrl->full[slot], c * 64, k0, hk, b);
+                        tma_load_4d(dst + c * kKvChunk, m, &ctrl->full[slot], c * 64, k0, hk, b);
                 }
                 __syncwarp();
             }
         }
     } else if (warp == 1) {
-        // ================= QK issuer.  A step's QK overwrites the S that the step before
-        // it left, as soon as the softmax has that in registers.  K of tile tc sits at ring
-        // position 2 tc; the previous item of its slot, K of tile tc - 2, was waited for
-        // by this warp.
+        // ================= QK issuer.  A step's QK overwrites its map's S of the last tile as
+        // soon as the softmax has that in registers.  K of tile tc sits at ring position 2 tc;
+        // the previous item of its slot, K of tile tc - kNS / 2, was waited for by this warp.
         bool ok = true;
         while (ok && items_next(items, a, prefix)) {
             const int n_tiles = it.n_tiles;
@@ -379,17 +386,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int slot = (2 * tc) % kNS;
                 const uint32_t ka = smem_addr(sKV + slot * kSlotBytes);
                 for (int m = 0; m < 2; ++m) {
-                    const uint32_t s = 2 * tc + m;
                     if (m == 0) ok = wait_warp(&ctrl->full[slot], (2 * tc / kNS) & 1, w);
-                    if (s > 0) ok = ok && wait_warp(&ctrl->s_free, (s - 1) & 1, w);
+                    if (tc > 0) ok = ok && wait_warp(&ctrl->s_free[m], (tc - 1) & 1, w);
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
 #pragma unroll
                         for (int k16 = 0; k16 < 4; ++k16) {
-                            const uint32_t off = m * kChunk + k16 * 32;
-                            mma_ss(tmem, sdesc_sw128(qa + off, 16, 1024),
-                                   sdesc_sw128(ka + off, 16, 1024), kIdescQK, k16 > 0 ? 1u : 0u);
+                            mma_ss(tmem + m * kTS, sdesc_sw128(qa + m * kQChunk + k16 * 32, 16, 1024),
+                                   sdesc_sw128(ka + m * kKvChunk + k16 * 32, 16, 1024), kIdescQK,
+                                   k16 > 0 ? 1u : 0u);
                         }
                         mma_commit(&ctrl->s_full[m]);
                         if (m == 1) mma_commit(&ctrl->empty[slot]);
@@ -401,7 +407,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp == kPvWarp) {
         // ================= PV issuer: waits for P of the step and, once a tile, for V
-        // (ring position 2 tc + 1; the slot's previous item is V of tile tc - 2).  The first
+        // (ring position 2 tc + 1; the slot's previous item is V of tile tc - kNS / 2).  The first
         // PV of an item overwrites O, so it waits until the softmax has read the last item's.
         bool ok = true;
         while (ok && items_next(items, a, prefix)) {
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // a NaN is a NaN: clear them.
                             uint4* v16 = reinterpret_cast<uint4*>(sKV + slot * kSlotBytes);
                             for (int x = live * 8 + lane; x < kBN * 8; x += 32)
-                                v16[x] = v16[kChunk / 16 + x] = make_uint4(0, 0, 0, 0);
+                                v16[x] = v16[kKvChunk / 16 + x] = make_uint4(0, 0, 0, 0);
                             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                             __syncwarp();
                         }
@@ -431,17 +437,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     tc_fence_after();
                     if (elect_one()) {
-                        // In two halves of 256 tensor-core cycles, the second half's issue 128
-                        // cycles behind the first's: the tensor core works in order, and a QK that
-                        // gets ready meanwhile goes in between (8192 x 16 heads 284 -> 275 us).
+                        // hi, then lo, each 256 tensor-core cycles, the second's issue 128 cycles
+                        // behind the first's: the tensor core works in order, and a QK that gets
+                        // ready meanwhile goes in between (8192 x 16 heads 434 -> 420 us).
                         const long long begun = clock64();
 #pragma unroll
-                        for (int k16 = 0; k16 < kBN / 16; ++k16) {
-                            if (k16 == kBN / 32)
+                        for (int half = 0; half < 2; ++half) {
+                            if (half == 1)
                                 while (clock64() - begun < 128) {}
-                            mma_ts(tmem + kTO + m * 128, tmem + kTP + m * 64 + k16 * 8,
-                                   sdesc_sw128(va + k16 * 2048, kChunk, 1024), kIdescPV,
-                                   (t > 0 || k16 > 0) ? 1u : 0u);
+#pragma unroll
+                            for (int k16 = 0; k16 < kBN / 16; ++k16)
+                                mma_ts(tmem + kTO + m * 128,
+                                       tmem + kTP + m * kTPMap + half * kTPLo + k16 * 8,
+                                       sdesc_sw128(va + k16 * 2048, kKvChunk, 1024), kIdescPV,
+                                       (t > 0 || half > 0 || k16 > 0) ? 1u : 0u);
                         }
                         if (m == 1) mma_commit(&ctrl->empty[slot]);
                         mma_commit(&ctrl->pv_done[m]);
@@ -455,12 +464,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // A thread owns one query row of one map (TMEM lane quarter = warp % 4), so nothing is
         // exchanged until the epilogue and the two maps' warps run out of step: while one map's
         // are in their exponentials, the other's load scores or wait for the tensor core.
-        // The 128 scores leave few registers: barriers are named by address, the loop keeps only
-        // what it needs, and the epilogue works its own values out anew.
+        // The scores and both halves of P leave few registers: barriers are named by address, the
+        // loop keeps only what it needs, and the epilogue works its own values out anew.
         const uint32_t bars = smem_addr(&ctrl->s_full[0]) + 8 * ((warp - 2) >> 2);   // of this map
         constexpr uint32_t kPFull = offsetof(Ctrl, p_full) - offsetof(Ctrl, s_full);
         constexpr uint32_t kPvDone = offsetof(Ctrl, pv_done) - offsetof(Ctrl, s_full);
-        const uint32_t s_free = smem_addr(&ctrl->s_free);
+        constexpr uint32_t kSFree = offsetof(Ctrl, s_free) - offsetof(Ctrl, s_full);
         const uint32_t tl = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const float sl2 = a.scale_log2;
         bool ok = true;
@@ -480,10 +489,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             uint32_t x[kBN];
 #pragma unroll
-            for (int c = 0; c < kBN; c += 32) tmem_ld32(tl + c, x + c);
+            for (int c = 0; c < kBN; c += 32) tmem_ld32(tl + ((warp - 2) >> 2) * kTS + c, x + c);
             tmem_ld_wait();
             tc_fence_before();
-            mbar_arrive(s_free);
+            mbar_arrive(bars + kSFree);
 
             if (lim < kBN) {   // keys the row does not see
 #pragma unroll
@@ -495,13 +504,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) m4[k] = __uint_as_float(x[k]);
 #pragma unroll
-            for (int c = 4; c < 124; c += 8) {
+            for (int c = 4; c < kBN - 4; c += 8) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     m4[k] = max3f(m4[k], __uint_as_float(x[c + k]), __uint_as_float(x[c + 4 + k]));
             }
-            m4[0] = max3f(m4[0], __uint_as_float(x[124]), __uint_as_float(x[125]));
-            m4[1] = max3f(m4[1], __uint_as_float(x[126]), __uint_as_float(x[127]));
+            m4[0] = max3f(m4[0], __uint_as_float(x[kBN - 4]), __uint_as_float(x[kBN - 3]));
+            m4[1] = max3f(m4[1], __uint_as_float(x[kBN - 2]), __uint_as_float(x[kBN - 1]));
             const float mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
             const float m_new = fmaxf(m_run, mx * sl2);
             const bool need = m_new > m_run + 8.0f;
@@ -513,31 +522,32 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool warp_need = __any_sync(0xffffffffu, need);
             const float m_use = m_run == -INFINITY ? 0.0f : m_run;
             const uint64_t sl2x2 = f2_pack(sl2, sl2), negm = f2_pack(-m_use, -m_use);
-            const uint32_t pbuf = tl + kTP + ((warp - 2) >> 2) * 64;
+            // P as two FP16 halves, hi = RNE(p) and lo = RNE(p - hi), packed over the keys
+            uint64_t rs[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) rs[k] = f2_pack(0.0f, 0.0f);
+            uint32_t hi[kBN / 2], lo[kBN / 2];
+#pragma unroll
+            for (int i = 0; i < kBN / 2; ++i) {
+                float x0, x1;
+                f2_unpack(f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                 sl2x2, negm),
+                          x0, x1);
+                const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
+                rs[i & 3] = f2_add(rs[i & 3], f2_pack(p0, p1));   // four independent sums
+                const __half2 h = __floats2half2_rn(p0, p1);
+                const float2 f = __half22float2(h);
+                hi[i] = *reinterpret_cast<const uint32_t*>(&h);
+                lo[i] = pack_half2(p0 - f.x, p1 - f.y);
+            }
             if (!first) {   // the P buffer is free and O complete up to the last tile
                 ok = wait_warp(bars + kPvDone, (tc - 1) & 1, w);
                 if (!ok) break;
                 tc_fence_after();
             }
-            uint64_t rs[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) rs[k] = f2_pack(0.0f, 0.0f);
-#pragma unroll
-            for (int c = 0; c < kBN; c += 16) {
-                uint32_t p2[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float x0, x1;
-                    f2_unpack(f2_fma(f2_pack(__uint_as_float(x[c + 2 * i]),
-                                             __uint_as_float(x[c + 2 * i + 1])),
-                                     sl2x2, negm),
-                              x0, x1);
-                    const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-                    rs[i & 3] = f2_add(rs[i & 3], f2_pack(p0, p1));   // four independent sums
-                    p2[i] = pack_half2(p0, p1);
-                }
-                tmem_st8(pbuf + c / 2, p2);
-            }
+            const uint32_t pbuf = tl + kTP + ((warp - 2) >> 2) * kTPMap;
+            tmem_st32(pbuf, hi);
+            tmem_st32(pbuf + kTPLo, lo);
             float r0, r1, r2, r3, r4, r5, r6, r7;
             f2_unpack(rs[0], r0, r1);
             f2_unpack(rs[1], r2, r3);
@@ -799,11 +809,12 @@ __global__ void __launch_bounds__(256) attn_diff_merge_kernel(const DiffPrefillA
 
 size_t record_bytes() { return 2ull * kBM * (kD * 4 + 8); }
 
-// Whether to split the keys, by the time of both ways in key tiles per CTA (1.25 us each): whole
+// Whether to split the keys, by the time of both ways in key tiles per CTA (0.95 to 1.0 us each): whole
 // units cost their rounds (at least the longest unit) and about 6 tiles for the start and the ends; a
-// split costs an even share and about 24 tiles for its start, the records and the merge.  Measured,
-// whole against split: 16 heads, 500 queries on 32,500 keys 324 and 164 us; 8 heads, 128 on 4,000 41
-// and 23 us; 16 heads, 1,024 on 9,000 83 and 93 us; 8 heads x 4,096 causal 44 and 89 us.
+// split costs an even share and about 30 tiles for its start, the records and the merge.  Measured,
+// whole against split: 16 heads, 500 queries on 32,500 keys 522 and 240 us; 8 heads, 128 on 4,000 59
+// and 23 us; 16 heads, 1,024 on 9,000 124 and 124 us; 32 heads, 512 on 8,192 113 and 117 us; 8 heads
+// x 4,096 causal 61 and 99 us.
 bool split_pays(long long units, int Sq, int Skv, int sms) {
     const int longest = (Skv + kBN - 1) / kBN;
     if (units > kMaxUnits || units * longest > 0x7FFFFFFFLL) return false;
@@ -811,7 +822,7 @@ bool split_pays(long long units, int Sq, int Skv, int sms) {
     const double mean = longest - (Sq < Skv ? Sq : Skv) / (2.0 * kBN);
     const double rounds = static_cast<double>((units + sms - 1) / sms);
     const double whole = rounds * mean > longest ? rounds * mean : longest;
-    return units * mean / sms + 24 < whole + 6;
+    return units * mean / sms + 30 < whole + 6;
 }
 
 // Workspace of a split launch: two records per CTA and the units' tile prefix.

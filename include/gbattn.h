@@ -398,7 +398,9 @@ int attn_diff_paged_decode_f16_fwd(const void* q, const void* k_pages, const voi
 
 /*
  * Differential attention of prompts.
- * The mathematics, lambda_vecs, norm_weight and eps are attn_diff_paged_decode_f16_fwd's.
+ * The mathematics, lambda_vecs, norm_weight and eps are attn_diff_paged_decode_f16_fwd's.  So is the
+ * precision: FP32 scores, softmax and accumulation, and each map's probabilities as FP16 hi + lo
+ * halves in the PV product, since what the maps have in common cancels and P's rounding does not.
  *   q, o : [B][Hq][Sq][D] FP16   k, v : [B][Hkv][Skv][D] FP16 (k and v share kv_strides)
  *   q_strides, kv_strides, o_strides: {batch, head, row} element strides or NULL (dense)
  *   q_lens, kv_lens : int32 [B] on the device, or NULL: Sq, Skv.  Only the first kv_lens[b] keys
