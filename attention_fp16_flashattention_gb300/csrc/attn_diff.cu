@@ -9,7 +9,8 @@
 // costs 2 * 64 FLOPs of QK and 2 * 128 of PV per map: 768 in all, against 512 for an ordinary head,
 // and two exponentials instead of one.
 //
-// P is rounded to two FP16 halves, hi = RNE(p) and lo = RNE(p - hi), 2^-22 of p.  What the maps have
+// P is rounded to two FP16 halves, hi = RNE(p) and lo = RNE(p - hi), 2^-22 of p, with the largest p
+// near the top of FP16's range so that small ones keep their bits (kShift in tiles.cuh).  What the maps have
 // in common cancels in the difference and the norm brings the rest back to unit size, so P's rounding
 // grows as the output shrinks: with one FP16 value the error against float64 was 2.6 to 3.2e-4 of
 // unrelated maps' output and 9.9e-4 of maps correlated by 0.999 (lambda 0.78), of which the output's
@@ -37,12 +38,13 @@
 // range of them (as the decode kernels do); the parts of a unit that ranges cut leave unnormalised
 // O_m, max and sum in `workspace`, and a merge kernel joins them.
 //
-// Measured (graph replays): 16 heads x 8192 causal 420 us, 500 queries on 32,500 keys 240 us.  The
-// softmax's chain bounds it: without any softmax the first takes 358 us, without MMAs (one k-step
-// each) 430, without the lo halves in softmax and PV 342.  Of a softmax warp's 1,750 cycles per tile
-// 800 are the exponentials with both roundings, 256 and 211 the waits for S and for the P buffer, 180
-// the maximum, 240 loads and stores.  Slower: P written in two or four chunks between the
-// exponentials (457 to 492), PV's lo half without a gap behind its hi half (434).
+// Measured (graph replays): 16 heads x 8192 causal 464 us (447 with kShift 7, 479 with 13), 500
+// queries on 32,500 keys 243 us.  The softmax's chain bounds it: copies of a version that took 420 us
+// took 358 us without any softmax, 430 without MMAs (one k-step each) and 342 without the lo halves in
+// softmax and PV.  Of a softmax warp's 1,750 cycles per tile 800 are the exponentials with both
+// roundings, 256 and 211 the waits for S and for the P buffer, 180 the maximum, 240 loads and stores.
+// Slower: P written in two or four chunks between the exponentials (457 to 492), PV's lo half without
+// a gap behind its hi half (434).
 //
 // Every wait is bounded in time (see WaitCtl): a wait that runs out records
 // GBATTN_DEV_WAIT_TIMEOUT in the device status word, the CTA stops, waits a
@@ -92,7 +94,7 @@ struct DiffPrefillArgs {
     // split: records 2 c (the unit that CTA c's range begins in) and 2 c + 1 (the one that begins in
     // the range and goes on behind it)
     float* part_o;        // [record][map][128][128], unnormalised
-    float2* part_ml;      // [record][map][128]: (max in log2 units, sum)
+    float2* part_ml;      // [record][map][128]: (reference in log2 units, sum)
     uint32_t* prefix;     // [units + 1]: key tiles of the units before u
     uint32_t* status;
     uint64_t wait_limit;
@@ -119,7 +121,7 @@ struct Ctrl {
 
 // Values exchanged in the epilogue between the two threads of a query row.
 struct Exchange {
-    float mx[2][128];      // [map][row] running max
+    float mx[2][128];      // [map][row] reference of the exponentials
     float l[2][128];       // [map][row] row sum
     float sq[2][128];      // [column half][row] partial sum of squares
     float norm[128];       // the norm weight * (1 - lambda_init)
@@ -481,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float lambda = diff_lambda<kD / 2>(a.diff, it.bh % a.Hq, lane);
             if (lane == 0) items.lambda = lambda;
         }
-        float m_run = -INFINITY, l = 0.0f;
+        float m_run = -INFINITY, l = 0.0f;   // the exponentials' reference (tiles.cuh) and their sum
         bool first = true;
         for (; left > 0; --left, ++tc, lim -= kBN, first = false) {
             ok = wait_warp(bars, tc & 1, w);
@@ -512,12 +514,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             m4[0] = max3f(m4[0], __uint_as_float(x[kBN - 4]), __uint_as_float(x[kBN - 3]));
             m4[1] = max3f(m4[1], __uint_as_float(x[kBN - 2]), __uint_as_float(x[kBN - 1]));
             const float mx = fmaxf(max3f(m4[0], m4[1], m4[2]), m4[3]);
-            const float m_new = fmaxf(m_run, mx * sl2);
-            const bool need = m_new > m_run + 8.0f;
+            const float top = mx * sl2;
+            const bool need = top > m_run + kTop;
             float alpha = 1.0f;
             if (need) {
-                alpha = fast_exp2(m_run - m_new);
-                m_run = m_new;
+                alpha = fast_exp2(m_run - (top - kShift));
+                m_run = top - kShift;
             }
             const bool warp_need = __any_sync(0xffffffffu, need);
             const float m_use = m_run == -INFINITY ? 0.0f : m_run;

@@ -22,10 +22,10 @@
 //     width (PV) fill M, the query rows N (8, or 16 where a group has more).  K and
 //     V fragments come from the swizzled stage by ldmatrix (V transposed).
 //   * Probabilities enter the PV product as two FP16 halves, hi = RNE(p) and
-//     lo = RNE(p - hi), about 22 bits: one FP16 value alone would add an error as
+//     lo = RNE(p - hi), 22 bits: one FP16 value alone would add an error as
 //     large as the output's own rounding, and the extra MMAs are hidden behind the
-//     loads.  Softmax state is FP32 in log2 units; the reference max moves only when
-//     a score passes it by more than 2^8.
+//     loads.  p is 2^(x - reference), where the reference lies kShift below a maximum, so
+//     that the largest p fill FP16's range and the smallest keep their bits (tiles.cuh).
 //   * With `weights` the warps also store their scores (FP32, 1/16 of the cache's
 //     bytes at D = 128 and four rows); when the merge has the rows' final max and
 //     sum, a third kernel adds sum_r 2^(x - max) / sum to every token's weight.
@@ -58,7 +58,6 @@ namespace {
 
 constexpr int kTile = 16;        // tokens per tile (one MMA M block)
 constexpr int kMaxSeqs = 4096;   // sequences per launch (prefix table in shared memory)
-constexpr float kRescale = 8.0f;
 constexpr int kMaxCluster = 8;      // CTAs of a stream's cluster
 constexpr float kLn2 = 0.69314718055994531f;
 
@@ -88,7 +87,7 @@ struct DecodeF16Args {
     const __half* q;
     const int32_t* table;
     const int32_t* kv_lens;
-    // Records of R = 8 NB rows: O [R][D] unnormalised and (max in log2 units, sum) [R], for
+    // Records of R = 8 NB rows: O [R][D] unnormalised and (reference in log2 units, sum) [R], for
     // every row group i of a stream's `side`.  Record (CTA + stream) side + i holds what the
     // ends of the CTA's warp ranges cut of the stream; record (tail0 + stream) side + i what
     // a warp finished inside its range.
@@ -473,9 +472,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, sh));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, sh));
             }
-            const bool up0 = mx0 > m_ref[n][0] + kRescale, up1 = mx1 > m_ref[n][1] + kRescale;
+            const bool up0 = mx0 > m_ref[n][0] + kTop, up1 = mx1 > m_ref[n][1] + kTop;
             if (__any_sync(0xffffffffu, up0 || up1)) {
-                const float n0 = up0 ? mx0 : m_ref[n][0], n1 = up1 ? mx1 : m_ref[n][1];
+                const float n0 = up0 ? mx0 - kShift : m_ref[n][0], n1 = up1 ? mx1 - kShift : m_ref[n][1];
                 const float al0 = up0 ? fast_exp2(m_ref[n][0] - n0) : 1.0f;
                 const float al1 = up1 ? fast_exp2(m_ref[n][1] - n1) : 1.0f;
                 m_ref[n][0] = n0;
@@ -756,7 +755,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     }
 }
 
-// Joins the partial records of every query row: with m_r, l_r the max (log2
+// Joins the partial records of every query row: with m_r, l_r the reference (log2
 // units) and sum of record r, M = max_r m_r, L = sum_r 2^(m_r - M) l_r,
 // O = sum_r 2^(m_r - M) O_r / L and lse = (M + log2 L) ln 2.  One CTA takes one
 // query of one head, its warps every blockDim/32-th record (kBatch in flight each,

@@ -1,5 +1,6 @@
-// Even split of ragged sequences over the warps of a grid, shared by the decode
-// kernels.  A stream is one (sequence, KV head, group of query rows); its work
+// What the decode kernels and the differential prompts share.
+//
+// Even split of ragged sequences over the warps of a grid.  A stream is one (sequence, KV head, group of query rows); its work
 // is the sequence's 16-token tiles.  The streams' tiles are laid end to end
 // (prefix[b] = tiles of all streams of the sequences before b) and warp w of W
 // takes the w-th of W equal contiguous ranges of them.
@@ -8,6 +9,14 @@
 #include <cstdint>
 
 namespace gbattn {
+
+// Where exponentials are rounded to FP16 they are p = 2^(x - m) with the reference m kShift below a
+// maximum of the row: the largest lie at 2^kShift, and m moves when a score passes it by kTop, so
+// that none exceeds 2^15 (FP16 ends at 65504).  FP16's last step is 2^-24 whatever the value: a token
+// whose p is rounded to hi + lo is off by 2^-22 of p or by 2^-25, that is 2^-(25 + kShift) of the
+// row's largest, whichever is more.  With m at the maximum itself everything below 2^-25 of an
+// attention sink was lost, and 2^-14 kept ten bits.  O, the sum and their records are all relative to m.
+constexpr float kShift = 11.0f, kTop = 15.0f;
 
 // First tile of warp w when W warps share U tiles.
 __device__ __forceinline__ uint32_t warp_start(uint32_t w, uint32_t W, uint32_t U) {

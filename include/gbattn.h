@@ -311,8 +311,9 @@ int kv_paged_append_f16(const void* k_new, const void* v_new, void* k_pages, voi
  *                query heads and the nq queries (what kv_paged_evict ranks by)
  *   Query i of sequence b sits at position kv_lens[b] - nq + i and sees the cached tokens t <= that
  *   position; one that sees none (kv_lens[b] < nq) gets O = 0, lse = -inf.  Query head h reads KV
- *   head h / (Hq / Hkv).  Scores, softmax and accumulation are FP32 (probabilities enter the PV
- *   product as FP16 hi + lo halves), O is rounded to FP16 once.
+ *   head h / (Hq / Hkv).  Scores, softmax and accumulation are FP32, O is rounded to FP16 once.
+ *   Probabilities enter the PV product as FP16 hi + lo halves, each off by at most 2^-22 of itself or
+ *   2^-36 of the row's largest.
  *   Slots of a page at or past kv_lens[b] may hold anything.  A cached value within kv_lens[b] that is
  *   infinite or NaN makes that column of the queries that see it infinite or NaN (an infinite one too:
  *   P is a sum of two halves, of which one may be zero or negative); it may also reach queries of the
