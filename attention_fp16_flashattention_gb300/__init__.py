@@ -161,6 +161,13 @@ def _strides(t):
     return _Strides3(b, h, s)
 
 
+def _same_layout(a, b):
+    """Whether two tensors of one shape have the same strides where a stride means anything: along a
+    dimension of one entry it may be any number."""
+    sa, sb = a.stride(), b.stride()
+    return sa == sb or all(x == y or n == 1 for n, x, y in zip(a.shape, sa, sb))
+
+
 def _scale(scale, D):
     return float(1.0 / D ** 0.5) if scale is None else float(scale)
 
@@ -204,7 +211,7 @@ def attn_dense_fwd(q, k, v, o=None, lse=None, scale=None, stream=None):
     Skv = k.shape[2]
     if tuple(k.shape) != (B, H, Skv, D) or tuple(v.shape) != tuple(k.shape):
         raise ValueError("k and v must be [B, H, Skv, D] matching q")
-    if k.stride() != v.stride():
+    if not _same_layout(k, v):
         raise ValueError("k and v must have the same strides")
     o = torch.empty((B, H, Sq, D), dtype=torch.float16, device=q.device) if o is None else o
     _need_view(o, "o", torch.float16)
@@ -265,7 +272,7 @@ def attn_causal_prefill_fwd(q, k, v, q_real=None, o=None, lse=None, scale=None, 
     Hkv, KV = k.shape[1], k.shape[2]
     if tuple(v.shape) != tuple(k.shape) or k.shape[0] != B or k.shape[3] != D:
         raise ValueError("k and v must be [B, Hkv, KV, D] matching q")
-    if k.stride() != v.stride():
+    if not _same_layout(k, v):
         raise ValueError("k and v must have the same strides")
     q_real = Qp if q_real is None else int(q_real)
     o = torch.empty((B, Hq, Qp, D), dtype=torch.float16, device=q.device) if o is None else o
@@ -486,7 +493,7 @@ def kv_paged_append_f16(k_new, v_new, k_pages, v_pages, page_table, kv_lens, new
     _need_view_on(k_new, "k_new", torch.float16, dev)
     _need_view_on(v_new, "v_new", torch.float16, dev)
     B, Hkv, n, D = k_new.shape
-    if v_new.shape != k_new.shape or v_new.stride() != k_new.stride():
+    if v_new.shape != k_new.shape or not _same_layout(k_new, v_new):
         raise ValueError("k_new and v_new must have the same shape and strides")
     P, ps, _, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, Hkv, D, dev)
     if new_lens is not None:
@@ -670,7 +677,7 @@ def attn_diff_prefill_fwd(q, k, v, lambda_vecs, lambda_init, norm_weight=None, e
     Bk, Hkv, Skv, Dk = k.shape
     if v.shape != k.shape or Bk != B or Dk != D:
         raise ValueError("k and v must be [B, Hkv, Skv, D] matching q")
-    if k.stride() != v.stride():
+    if not _same_layout(k, v):
         raise ValueError("k and v must have the same strides")
     heads = _need_diff(lambda_vecs, norm_weight, Hq, D, dev)
     for t, n in ((q_lens, "q_lens"), (kv_lens, "kv_lens")):
