@@ -191,11 +191,20 @@ __device__ __forceinline__ bool evict_select(const EvictArgs& a, uint32_t* s_dyn
         const int at2 = (a.sink + lo + held) >> a.page_bits;
         const int p2 = mid == 0 || held == hi - lo ? 0 : pages_to(a.sink + hi) - at2;
         const int p3 = kInPlace ? 0 : pages_to(n);
+        // A destination that is the sequence's own page of the same place, as in a copy of the page table,
+        // would be written while it is read: refused like a page out of range, wherever the call reads
+        // that page (all of a cache within the budget or with weights to compare, else sinks and recent).
+        const bool read_all = L <= a.budget || want > 0;
+        const int sinks_end = pages_to(a.sink), recent_at = (L - a.recent) >> a.page_bits;
+        auto destination = [&](int x) -> int {
+            const int page = dst_table[x];
+            return page == table[x] && (read_all || x < sinks_end || x >= recent_at) ? -1 : page;
+        };
         auto page_at = [&](int x) -> int {
             if (x < p0) return table[x];
             if ((x -= p0) < p1) return table[at1 + x];
             if ((x -= p1) < p2) return table[at2 + x];
-            return (x -= p2) < p3 ? dst_table[x] : 0;
+            return (x -= p2) < p3 ? destination(x) : 0;
         };
         const int early = page_at(tid);
         // eight weights a thread at a time, so that the loads (each behind a page-table

@@ -360,12 +360,14 @@ int attn_paged_decode_f16_fwd(const void* q, const void* k_pages, const void* v_
  *   their old order.  Everything else in the pool stays as it is.
  *   In place, a page that is moved in must belong to one sequence only.  With other pages, no page
  *   of dst_table may be read or written for another purpose by the same call (so shared pages can be
- *   evicted from, into fresh ones).
+ *   evicted from, into fresh ones); of this a sequence's own page in the same place of both tables,
+ *   as in a copy of page_table, is found and refused with GBATTN_DEV_BAD_PAGE.
  *   D is 64, 128 or 256; page_size a power of two >= 16; num_phys_pages * page_size < 2^31;
  *   sink + recent <= budget; max_kv_len <= max_pages * page_size, 2^30;
  *   min(budget, max_kv_len) <= dst_pages * page_size.  A sequence whose length is outside
  *   [0, max_kv_len] (GBATTN_DEV_BAD_LENGTH) or with a page that it needs outside
- *   [0, num_phys_pages) (GBATTN_DEV_BAD_PAGE) stays as it is: new_lens[b] = kv_lens[b], kept -1.
+ *   [0, num_phys_pages) or refused (GBATTN_DEV_BAD_PAGE) stays as it is: new_lens[b] = kv_lens[b],
+ *   kept -1.
  */
 int kv_paged_evict(void* k_pages, void* v_pages, float* weights, const int32_t* page_table,
                    const int32_t* dst_table, const int32_t* kv_lens, int32_t* new_lens,
