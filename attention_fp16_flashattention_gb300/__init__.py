@@ -464,6 +464,18 @@ def _scratch(nbytes, device, stream):
     return _new_tensor(max(int(nbytes), 16), torch.uint8, device, stream)
 
 
+def _need_workspace(workspace, dev):
+    """A caller's workspace: as many bytes as it counts, on the current device `dev`.  A view with
+    gaps or a repeated (expanded) dimension covers other memory than its byte count says."""
+    import torch
+    if not isinstance(workspace, torch.Tensor) or not workspace.is_cuda:
+        raise ValueError("workspace must be a CUDA tensor")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    if workspace.get_device() != dev:
+        _same_device(workspace)
+
+
 def _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, Hkv, D, dev):
     """Checks an FP16 page pool with its table; returns (pages, page size, KV heads, max pages)."""
     import torch
@@ -542,8 +554,8 @@ def attn_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, max_kv_l
         workspace = _scratch(attn_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len, D,
                                                                   weights is not None),
                              q.device, stream)
-    elif workspace.get_device() != dev:
-        _same_device(workspace)
+    else:
+        _need_workspace(workspace, dev)
     rc = load().attn_paged_decode_f16_fwd(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
                                           page_table.data_ptr(), kv_lens.data_ptr(), o.data_ptr(),
                                           _ptr(lse), _ptr(weights), B, Hq, Hkv, nq, D, P, ps,
@@ -645,8 +657,8 @@ def attn_diff_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, lam
     if workspace is None:
         workspace = _scratch(attn_diff_paged_decode_f16_workspace_size(B, Hq, Hkv, nq, max_kv_len,
                                                                        D), q.device, stream)
-    elif workspace.get_device() != dev:
-        _same_device(workspace)
+    else:
+        _need_workspace(workspace, dev)
     rc = load().attn_diff_paged_decode_f16_fwd(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
         kv_lens.data_ptr(), lambda_vecs.data_ptr(), heads, float(lambda_init), _ptr(norm_weight),
@@ -694,8 +706,8 @@ def attn_diff_prefill_fwd(q, k, v, lambda_vecs, lambda_init, norm_weight=None, e
         _need_shape(lse, "lse", (B, Hq, 2, Sq))
     if workspace is None:
         workspace = _scratch(attn_diff_prefill_workspace_size(B, Hq, Sq, Skv, D), q.device, stream)
-    elif workspace.get_device() != dev:
-        _same_device(workspace)
+    else:
+        _need_workspace(workspace, dev)
     rc = load().attn_diff_prefill_fwd(
         q.data_ptr(), k.data_ptr(), v.data_ptr(), lambda_vecs.data_ptr(), heads, float(lambda_init),
         _ptr(norm_weight), float(eps), _ptr(q_lens), _ptr(kv_lens), o.data_ptr(), _ptr(lse), B, Hq,
