@@ -464,6 +464,14 @@ def _scratch(nbytes, device, stream):
     return _new_tensor(max(int(nbytes), 16), torch.uint8, device, stream)
 
 
+def _int32(x, name):
+    """x as the 32-bit integer that the library takes (ctypes would cut it to 32 bits in silence)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} does not fit 32 bits: {x}")
+    return x
+
+
 def _need_workspace(workspace, dev):
     """A caller's workspace: as many bytes as it counts, on the current device `dev`.  A view with
     gaps or a repeated (expanded) dimension covers other memory than its byte count says."""
@@ -538,7 +546,7 @@ def attn_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, max_kv_l
     _need_on(q, "q", torch.float16, 4, dev)
     B, Hq, nq, D = q.shape
     P, ps, Hkv, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, None, D, dev)
-    max_kv_len = max_pages * ps if max_kv_len is None else int(max_kv_len)
+    max_kv_len = _int32(max_pages * ps if max_kv_len is None else max_kv_len, "max_kv_len")
     if o is None:
         o = _new_like(q, stream)
     else:
@@ -590,8 +598,8 @@ def kv_paged_evict(k_pages, v_pages, weights, page_table, kv_lens, budget, sink=
     _need_on(dst, "dst_table", torch.int32, 2, cur)
     if dst.shape[0] != B:
         raise ValueError("dst_table needs one row per sequence")
-    max_kv_len = max_pages * ps if max_kv_len is None else int(max_kv_len)
-    budget = int(budget)
+    max_kv_len = _int32(max_pages * ps if max_kv_len is None else max_kv_len, "max_kv_len")
+    budget, sink, recent = _int32(budget, "budget"), _int32(sink, "sink"), _int32(recent, "recent")
     if budget <= 0:
         raise ValueError("budget must be positive")
     dev = k_pages.device
@@ -607,7 +615,7 @@ def kv_paged_evict(k_pages, v_pages, weights, page_table, kv_lens, budget, sink=
                                page_table.data_ptr(), dst.data_ptr(), kv_lens.data_ptr(),
                                new_lens.data_ptr(), kept.data_ptr(), B, Hkv, D,
                                k_pages.element_size(), P, ps, max_pages, dst.shape[1], max_kv_len,
-                               budget, int(sink), int(recent), _raw_stream(stream, cur))
+                               budget, sink, recent, _raw_stream(stream, cur))
     _check("kv_paged_evict", rc)
     return new_lens, kept
 
@@ -645,7 +653,7 @@ def attn_diff_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, lam
     B, Hq, nq, D = q.shape
     P, ps, Hkv, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, None, D, dev)
     heads = _need_diff(lambda_vecs, norm_weight, Hq, D, dev)
-    max_kv_len = max_pages * ps if max_kv_len is None else int(max_kv_len)
+    max_kv_len = _int32(max_pages * ps if max_kv_len is None else max_kv_len, "max_kv_len")
     if o is None:
         o = _new_like(q, stream)
     else:
