@@ -540,7 +540,9 @@ def attn_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, max_kv_l
     """Decode over paged FP16 caches. q [B,Hq,nq,D] FP16; pages [P,page,Hkv,D] FP16; page_table
     int32 [B,max_pages]; kv_lens int32 [B] (device).  weights FP32 [P,Hkv,page] grows by the
     attention every cached token receives (what kv_paged_evict ranks by).  max_kv_len defaults to
-    max_pages * page_size (no device read)."""
+    max_pages * page_size (no device read); a bound near the longest cache makes short caches faster,
+    and with weights the workspace (allocated here without one) holds a score for every query row and
+    token up to it."""
     import torch
     dev = _current_device(q, "q")
     _need_on(q, "q", torch.float16, 4, dev)

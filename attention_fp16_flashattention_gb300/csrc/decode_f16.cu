@@ -35,9 +35,9 @@
 //     through its shared memory and adds the weights; one kernel (rule at cluster_of).
 // Measured (graph replays): 4 sequences of 65,571 to 131,072 tokens, 6 query heads on
 // one KV head of 256 (450 MB) 75 us, 6.0 TB/s, 0.89 of the measured copy; 32 of 257
-// to 8,191, 32 on 8 of 128, with weights (581 MB) 110 us, 15 of them for the weights (a
+// to 8,191, 32 on 8 of 128, with weights (581 MB) 109 us, 15 of them for the weights (a
 // kernel of its own, and 17 MB of scores written beside the cache's stream); one sequence of 511
-// 7.3 us in clusters (9.1 with a merge kernel), latency of the loads behind each other.
+// 7.4 us in clusters (9.1 with a merge kernel), latency of the loads behind each other.
 // What the decode kernel loses against the copy rate is its start (lengths, then page
 // table, then the first tiles: three trips to memory) and the joins at its end, 6 us
 // together.

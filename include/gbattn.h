@@ -329,7 +329,7 @@ int kv_paged_append_f16(const void* k_new, const void* v_new, void* k_pages, voi
  *   max_kv_len is small a thread-block cluster takes each stream, in one kernel), and the workspace
  *   rules are the same: attn_paged_decode_f16_workspace_size() gives the full-speed size
  *   (weights != 0 adds about one FP32 score per query row and cached token, for max_kv_len tokens of
- *   every sequence), a smaller one runs fewer warps, and below one CTA's worth the call returns
+ *   every sequence, so a max_kv_len near the longest cache keeps it small), a smaller one runs fewer warps, and below one CTA's worth the call returns
  *   GBATTN_ERR_WORKSPACE.  The workspace needs no initial value; calls that may run at the same
  *   time (two streams, concurrent graph launches) need separate ones.
  */
