@@ -31,7 +31,7 @@ def launches(gb, B, Hkv, D, n, weights, Hq=None):
 
 @pytest.mark.parametrize("B,Hkv,D,n,weights,kernels", [
     (1, 8, 128, 4096, False, 1), (1, 8, 128, 8192, False, 2), (1, 8, 128, 2048, True, 1),
-    (1, 8, 128, 4096, True, 3), (15, 1, 128, 6144, True, 1), (1, 1, 64, 8192, False, 1),
+    (1, 8, 128, 4096, True, 3), (12, 1, 128, 6144, True, 1), (1, 1, 64, 8192, False, 1),
     (1, 1, 64, 12288, False, 2), (8, 1, 64, 12288, False, 1), (1, 1, 256, 512, False, 2),
     (8, 1, 256, 512, False, 1), (1, 1, 256, 512, True, 1), (152, 1, 128, 768, False, 1),
     (153, 1, 128, 64, False, 2)])
@@ -42,7 +42,7 @@ def test_the_form_that_costs_less(gb, B, Hkv, D, n, weights, kernels):
 @pytest.mark.parametrize("D", [64, 128, 256])
 @pytest.mark.parametrize("streams", [14, 15, 16, 19, 20, 36, 37, 38, 76, 77, 151, 152, 153])
 def test_around_the_clusters_that_run_at_once(gb, streams, D):
-    """15, 36, 76 and 152 clusters of 8, 4, 2 and 1 CTAs run at once on 152 SMs."""
+    """About 15, 36, 76 and 152 clusters of 8, 4, 2 and 1 CTAs run at once on 152 SMs."""
     lens = tuple(int(x) for x in np.random.default_rng(streams).integers(0, 120, streams))
     q, kp, vp, table, lens, w = inputs.paged_f16_inputs(streams, 3, 1, 1, lens, D, 98, page_size=16,
                                                         poison=True)
