@@ -55,6 +55,14 @@ _SIGNATURES = {
     "attn_diff_prefill_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "attn_diff_prefill_fwd": (_i, [_vp, _vp, _vp, _vp, _i, _f, _vp, _f, _vp, _vp, _vp, _vp, _i, _i,
                                    _i, _i, _i, _i, _vp, _vp, _vp, _f, _i, _vp, _sz, _vp]),
+    "kv_paged_extend": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                             _i, _vp]),
+    "kv_paged_release": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "qk_norm_rope_f16": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
+                              _vp, _vp, _vp, _vp, _vp, _f, _f, _vp]),
+    "kv_paged_rope_append": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i,
+                                  _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _f, _f, _f,
+                                  _f, _vp]),
     "vsa_select_workspace_size": (_sz, [_i, _i, _i, _i, _i]),
     "vsa_select_blocks": (_i, [_vp, _vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
     "vsa_sparse_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i,
@@ -73,6 +81,7 @@ DEV_WAIT_TIMEOUT = 1
 DEV_BAD_PAGE = 2
 DEV_BAD_INDEX = 4
 DEV_BAD_LENGTH = 8
+DEV_NO_PAGES = 16
 
 _Strides3 = ctypes.c_int64 * 3
 
@@ -725,6 +734,261 @@ def attn_diff_prefill_fwd(q, k, v, lambda_vecs, lambda_init, norm_weight=None, e
         1 if causal else 0, workspace.data_ptr(), workspace.nbytes, _raw_stream(stream, dev))
     _check("attn_diff_prefill_fwd", rc)
     return o
+
+
+def _need_tables(page_table, kv_lens, free_pages, free_count, cur):
+    """Checks what the page-table calls share; returns (B, max_pages, capacity)."""
+    import torch
+    _need_on(page_table, "page_table", torch.int32, 2, cur)
+    _need_on(kv_lens, "kv_lens", torch.int32, 1, cur)
+    _need_on(free_pages, "free_pages", torch.int32, 1, cur)
+    _need_on(free_count, "free_count", torch.int32, 1, cur)
+    B, max_pages = page_table.shape
+    _need_shape(kv_lens, "kv_lens", (B,))
+    _need_shape(free_count, "free_count", (1,))
+    return B, max_pages, free_pages.shape[0]
+
+
+def kv_paged_extend(page_table, kv_lens, new_lens, free_pages, free_count, page_size,
+                    num_phys_pages, max_tokens=None, row_tokens=None, kv_lens_out=None,
+                    free_count_out=None, token_starts=None, positions=None, slots=None,
+                    stream=None):
+    """Pages and slots for the new tokens of a batch, from the stack of free pages: page_table int32
+    [B,max_pages] is extended in place, kv_lens and new_lens int32 [B], free_pages int32 [capacity]
+    with its first free_count[0] entries on the stack (free_count int32 [1]), all on the device.
+    max_tokens (the sequences' new tokens end to end) or row_tokens (every sequence's in a row of
+    its own) asks for the tokens' positions and slots, int32 [max_tokens] or [B,row_tokens], -1
+    where there is no token.  Returns (kv_lens_out [B], free_count_out [1], token_starts [B+1],
+    positions, slots); each may be given, the first two as kv_lens and free_count themselves; the
+    last three are None where neither max_tokens nor row_tokens asks for them."""
+    import torch
+    cur = _current_device(page_table, "page_table")
+    B, max_pages, capacity = _need_tables(page_table, kv_lens, free_pages, free_count, cur)
+    _need_on(new_lens, "new_lens", torch.int32, 1, cur)
+    _need_shape(new_lens, "new_lens", (B,))
+    page_size, num_phys_pages = _int32(page_size, "page_size"), _int32(num_phys_pages, "num_phys_pages")
+    if max_tokens is not None and row_tokens is not None:
+        raise ValueError("max_tokens and row_tokens exclude each other")
+    rows = 0 if row_tokens is None else _int32(row_tokens, "row_tokens")
+    if row_tokens is not None and rows <= 0:
+        raise ValueError("row_tokens must be positive")
+    n = B * rows if row_tokens is not None else 0 if max_tokens is None else max_tokens
+    n = _int32(n, "max_tokens")
+    if max_tokens is not None and n <= 0:
+        raise ValueError("max_tokens must be positive")
+    dev = page_table.device
+    if kv_lens_out is None:
+        kv_lens_out = _new_tensor((B,), torch.int32, dev, stream)
+    if free_count_out is None:
+        free_count_out = _new_tensor((1,), torch.int32, dev, stream)
+    for t, name, shape in ((kv_lens_out, "kv_lens_out", (B,)), (free_count_out, "free_count_out", (1,))):
+        _need_on(t, name, torch.int32, 1, cur)
+        _need_shape(t, name, shape)
+    if n == 0:
+        if token_starts is not None or positions is not None or slots is not None:
+            raise ValueError("token_starts, positions and slots need max_tokens or row_tokens")
+    else:
+        shape = (B, rows) if rows else (n,)
+        if token_starts is None:
+            token_starts = _new_tensor((B + 1,), torch.int32, dev, stream)
+        if positions is None:
+            positions = _new_tensor(shape, torch.int32, dev, stream)
+        if slots is None:
+            slots = _new_tensor(shape, torch.int32, dev, stream)
+        _need_on(token_starts, "token_starts", torch.int32, 1, cur)
+        _need_shape(token_starts, "token_starts", (B + 1,))
+        for t, name in ((positions, "positions"), (slots, "slots")):
+            _need_on(t, name, torch.int32, len(shape), cur)
+            _need_shape(t, name, shape)
+    rc = load().kv_paged_extend(page_table.data_ptr(), kv_lens.data_ptr(), new_lens.data_ptr(),
+                                free_pages.data_ptr(), free_count.data_ptr(), kv_lens_out.data_ptr(),
+                                free_count_out.data_ptr(), _ptr(token_starts), _ptr(positions),
+                                _ptr(slots), B, max_pages, page_size, num_phys_pages, capacity, rows,
+                                n, _raw_stream(stream, cur))
+    _check("kv_paged_extend", rc)
+    return kv_lens_out, free_count_out, token_starts, positions, slots
+
+
+def kv_paged_release(page_table, kv_lens, free_pages, free_count, page_size, num_phys_pages,
+                     keep_lens=None, free_count_out=None, stream=None):
+    """Give pages back to the stack of free pages (kv_paged_extend): those of every sequence's tokens
+    from keep_lens int32 [B] (None: 0) to kv_lens, as far as they hold none that stay.  free_pages is
+    written in place; returns free_count_out int32 [1] (may be free_count itself)."""
+    import torch
+    cur = _current_device(page_table, "page_table")
+    B, max_pages, capacity = _need_tables(page_table, kv_lens, free_pages, free_count, cur)
+    if keep_lens is not None:
+        _need_on(keep_lens, "keep_lens", torch.int32, 1, cur)
+        _need_shape(keep_lens, "keep_lens", (B,))
+    if free_count_out is None:
+        free_count_out = _new_tensor((1,), torch.int32, page_table.device, stream)
+    _need_on(free_count_out, "free_count_out", torch.int32, 1, cur)
+    _need_shape(free_count_out, "free_count_out", (1,))
+    rc = load().kv_paged_release(page_table.data_ptr(), kv_lens.data_ptr(), _ptr(keep_lens),
+                                 free_pages.data_ptr(), free_count.data_ptr(),
+                                 free_count_out.data_ptr(), B, max_pages,
+                                 _int32(page_size, "page_size"),
+                                 _int32(num_phys_pages, "num_phys_pages"), capacity,
+                                 _raw_stream(stream, cur))
+    _check("kv_paged_release", rc)
+    return free_count_out
+
+
+def rope_frequencies(rot, base=10000.0, factor=1.0, trained_len=None, method="linear",
+                     low_turns=1.0, high_turns=32.0, device="cuda"):
+    """Frequencies FP32 [rot/2] for the rotary calls: base^(-2p/rot) radians per position for pair p,
+    scaled for contexts `factor` times as long as those a model was trained on.
+      "linear": every frequency divided by factor
+      "base":   base * factor^(rot/(rot-2)) in place of base: the slowest pair is divided by factor,
+                the fastest stays
+      "turns":  with r = trained_len * frequency / (2 pi), the turns of a pair within the trained length,
+                pairs with r >= high_turns stay, those with r <= low_turns are divided by factor, the
+                ones between weighted by (r - low_turns) / (high_turns - low_turns)
+      "pairs":  the same ends, the weight falling with the pair's number instead, from the (whole)
+                number of the pair that makes high_turns to that of the one that makes low_turns
+    Computed in 64 bits on the host, once for a model."""
+    import numpy as np
+    import torch
+    rot = int(rot)
+    if rot <= 0 or rot % 2 or not base > 1 or not factor > 0:
+        raise ValueError("rot must be even and positive, base above 1, factor positive")
+    pair = np.arange(rot // 2, dtype=np.float64)
+    if method == "base":
+        if rot < 4:
+            raise ValueError('"base" needs rot >= 4')
+        f = (base * factor ** (rot / (rot - 2.0))) ** (-2 * pair / rot)
+    else:
+        f = base ** (-2 * pair / rot)
+        if method == "linear":
+            f = f / factor
+        elif method in ("turns", "pairs"):
+            if trained_len is None or not 0 < low_turns < high_turns:
+                raise ValueError("trained_len and 0 < low_turns < high_turns are needed")
+            turns = trained_len * f / (2 * np.pi)
+            if method == "turns":
+                keep = (turns - low_turns) / (high_turns - low_turns)
+            else:
+                # the pair (not whole) that makes r turns: trained_len base^(-2p/rot) = 2 pi r
+                at = [rot / 2 * np.log(trained_len / (2 * np.pi * r)) / np.log(base)
+                      for r in (high_turns, low_turns)]
+                first, last = max(np.floor(at[0]), 0.0), min(np.ceil(at[1]), rot - 1.0)
+                keep = 1 - (pair - first) / max(last - first, 1e-3)
+            keep = np.clip(keep, 0.0, 1.0)
+            f = f * (keep + (1 - keep) / factor)
+        else:
+            raise ValueError(f"unknown method {method!r}")
+    return torch.from_numpy(f.astype(np.float32)).to(device)
+
+
+def _need_rope(positions, freqs, q_weight, k_weight, sections, B, S, D, dev):
+    """Checks what the rotary calls share; returns (rot, axes, sections for C)."""
+    import torch
+    if freqs is None:
+        rot = 0
+    else:
+        _need_on(freqs, "freqs", torch.float32, 1, dev)
+        rot = 2 * freqs.shape[0]
+    axes = 1
+    if positions is not None:
+        dims = positions.dim() if isinstance(positions, torch.Tensor) else 0
+        _need_on(positions, "positions", torch.int32, 3 if dims == 3 else 2, dev)
+        axes = positions.shape[0] if dims == 3 else 1
+        _need_shape(positions, "positions", (axes, B, S) if dims == 3 else (B, S))
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _need_on(t, name, torch.float32, 1, dev)
+            _need_shape(t, name, (D,))
+    c_sections = None
+    if sections is not None:
+        sections = [_int32(n, "sections") for n in sections]
+        if len(sections) != axes:
+            raise ValueError("sections needs one entry per axis of positions")
+        c_sections = (ctypes.c_int32 * axes)(*sections)
+    return rot, axes, c_sections
+
+
+def qk_norm_rope_f16(q, k, positions, freqs, q_weight=None, k_weight=None, eps=1e-6,
+                     interleaved=False, sections=None, rope_scale=1.0, q_out=None, k_out=None,
+                     stream=None):
+    """Per-head RMS norms (q_weight, k_weight FP32 [D] or None) and rotation by position of queries
+    q [B,Hq,S,D] and keys k [B,Hk,S,D] (or None), FP16 views with a contiguous last dimension.
+    positions int32 [B,S] or [axes,B,S] (with sections: pairs per axis); freqs FP32 [rot/2]
+    (rope_frequencies), the first rot elements of a head are rotated; None: no rotation.
+    interleaved pairs elements (2p, 2p+1), else (p, p + rot/2).  A negative position is padding: its
+    rows are not written.  q_out and k_out may be q and k themselves.  Returns (q_out, k_out)."""
+    import torch
+    dev = _current_device(q, "q")
+    _need_view_on(q, "q", torch.float16, dev)
+    B, Hq, S, D = q.shape
+    rot, axes, c_sections = _need_rope(positions, freqs, q_weight, k_weight, sections, B, S, D, dev)
+    Hk = 0
+    if k is not None:
+        _need_view_on(k, "k", torch.float16, dev)
+        Hk = k.shape[1]
+        _need_shape(k, "k", (B, Hk, S, D))
+        if k_out is None:
+            k_out = _new_tensor((B, Hk, S, D), torch.float16, q.device, stream)
+        _need_view_on(k_out, "k_out", torch.float16, dev)
+        _need_shape(k_out, "k_out", (B, Hk, S, D))
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if q_out is None:
+        q_out = _new_tensor((B, Hq, S, D), torch.float16, q.device, stream)
+    _need_view_on(q_out, "q_out", torch.float16, dev)
+    _need_shape(q_out, "q_out", (B, Hq, S, D))
+    rc = load().qk_norm_rope_f16(
+        q.data_ptr(), _ptr(k), _ptr(positions), _ptr(freqs), _ptr(q_weight), _ptr(k_weight),
+        q_out.data_ptr(), _ptr(k_out), B, Hq, Hk, S, D, rot, 1 if interleaved else 0, axes,
+        c_sections, _strides(q), None if k is None else _strides(k), _strides(q_out),
+        None if k is None else _strides(k_out), float(eps), float(rope_scale),
+        _raw_stream(stream, dev))
+    _check("qk_norm_rope_f16", rc)
+    return q_out, k_out
+
+
+def kv_paged_rope_append(q, k_new, v_new, slots, k_pages, v_pages, positions, freqs, q_weight=None,
+                         k_weight=None, eps=1e-6, interleaved=False, sections=None, rope_scale=1.0,
+                         k_scale=1.0, v_scale=1.0, weights=None, q_out=None, stream=None):
+    """qk_norm_rope_f16 on the way into a paged cache: q [B,Hq,S,D] goes to q_out, k_new [B,Hkv,S,D]
+    to its slots int32 [B,S] (kv_paged_extend; negative: padding) of k_pages [P,page,Hkv,D], and
+    v_new, not rotated, to those of v_pages.  Pages are FP16, or uint8 E4M3 codes of value / scale
+    (k_scale, v_scale).  weights FP32 [P,Hkv,page] gets zeros at the new slots.  Tokens packed end to
+    end are B = 1 and S tokens.  Returns q_out."""
+    import torch
+    dev = _current_device(q, "q")
+    _need_view_on(q, "q", torch.float16, dev)
+    _need_view_on(k_new, "k_new", torch.float16, dev)
+    _need_view_on(v_new, "v_new", torch.float16, dev)
+    B, Hq, S, D = q.shape
+    Hkv = k_new.shape[1]
+    _need_shape(k_new, "k_new", (B, Hkv, S, D))
+    if v_new.shape != k_new.shape or not _same_layout(k_new, v_new):
+        raise ValueError("k_new and v_new must have the same shape and strides")
+    rot, axes, c_sections = _need_rope(positions, freqs, q_weight, k_weight, sections, B, S, D, dev)
+    _need_on(slots, "slots", torch.int32, 2, dev)
+    _need_shape(slots, "slots", (B, S))
+    if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in (torch.float16, torch.uint8):
+        raise ValueError("k_pages must be a float16 or uint8 tensor")
+    _need_on(k_pages, "k_pages", k_pages.dtype, 4, dev)
+    _need_on(v_pages, "v_pages", k_pages.dtype, 4, dev)
+    P, ps = k_pages.shape[:2]
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _need_shape(t, name, (P, ps, Hkv, D))
+    if weights is not None:
+        _need_on(weights, "weights", torch.float32, 3, dev)
+        _need_shape(weights, "weights", (P, Hkv, ps))
+    if q_out is None:
+        q_out = _new_tensor((B, Hq, S, D), torch.float16, q.device, stream)
+    _need_view_on(q_out, "q_out", torch.float16, dev)
+    _need_shape(q_out, "q_out", (B, Hq, S, D))
+    rc = load().kv_paged_rope_append(
+        q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), _ptr(positions),
+        _ptr(freqs), _ptr(q_weight), _ptr(k_weight), q_out.data_ptr(), k_pages.data_ptr(),
+        v_pages.data_ptr(), _ptr(weights), B, Hq, Hkv, S, D, rot, 1 if interleaved else 0, axes,
+        c_sections, _strides(q), _strides(k_new), _strides(q_out), k_pages.element_size(), P, ps,
+        float(eps), float(rope_scale), float(k_scale), float(v_scale), _raw_stream(stream, dev))
+    _check("kv_paged_rope_append", rc)
+    return q_out
 
 
 def vsa_select_workspace_size(B, H, S, D, block):

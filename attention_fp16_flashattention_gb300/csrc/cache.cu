@@ -616,35 +616,12 @@ __global__ void __launch_bounds__(kEvictThreads, 2) kv_evict_copy_kernel(const E
     cp_async_wait<0>();
 }
 
-bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
-
 // log2 of the 16-byte chunks of one row of D elements, or -1.
 int row_chunk_bits(int D, int elem) {
     if ((D != 64 && D != 128 && D != 256) || (elem != 1 && elem != 2)) return -1;
     int bits = 0;
     while ((16 << bits) < D * elem) ++bits;
     return bits;
-}
-
-bool pool_supported(int num_phys, int ps) {
-    return ps >= 16 && (ps & (ps - 1)) == 0 && static_cast<long long>(num_phys) * ps <= 0x7FFFFFFFLL;
-}
-
-struct Range {
-    const void* p;
-    size_t n;
-};
-
-// Whether any of the outputs overlaps an input or another output.
-template <int NI, int NO>
-bool any_overlap(const Range (&in)[NI], const Range (&out)[NO]) {
-    for (int i = 0; i < NO; ++i) {
-        for (int j = 0; j < NI; ++j)
-            if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
-        for (int j = 0; j < i; ++j)
-            if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
-    }
-    return false;
 }
 
 }  // namespace

@@ -133,6 +133,31 @@ inline bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return x < y + nb && y < x + na;
 }
 
+struct Range {
+    const void* p;
+    size_t n;
+};
+
+// Whether any of the outputs overlaps an input or another output.
+template <int NI, int NO>
+bool any_overlap(const Range (&in)[NI], const Range (&out)[NO]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (overlaps(out[i].p, out[i].n, in[j].p, in[j].n)) return true;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return true;
+    }
+    return false;
+}
+
+inline bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+// A page pool that the FP16 cache calls take: pages of a power of two of at least 16 slots, slot numbers
+// within 31 bits.
+inline bool pool_supported(int num_phys, int ps) {
+    return ps >= 16 && (ps & (ps - 1)) == 0 && static_cast<long long>(num_phys) * ps <= 0x7FFFFFFFLL;
+}
+
 inline bool finite_positive(float s) { return s > 0.0f && s <= 3.402823466e38f; }
 
 inline int launch_status() {

@@ -16,6 +16,8 @@
  *   - decode over a paged E4M3 cache: the newest tokens of ragged sequences
  *     against their whole caches (same page, Validation: the E4M3 decode wave
  *     kernels and the 256000-input decode);
+ *   - page tables of either cache, built and given back on the device; queries and keys
+ *     normalised per head and rotated by their positions, for prompts or straight into a cache;
  *   - a paged FP16 cache: new tokens appended, decode over it with the attention
  *     weight of every cached token added up, and eviction of the tokens that
  *     received little (the same page's paged cache, in FP16 and within a budget);
@@ -83,10 +85,13 @@ enum gbattn_device_flag {
                                      that page's tokens were written as zeros */
     GBATTN_DEV_BAD_INDEX = 4u,    /* a VSA cube list was not strictly ascending or held an
                                      index outside [0, S/block); the entry was skipped */
-    GBATTN_DEV_BAD_LENGTH = 8u    /* a sequence length was outside the range that the call states
+    GBATTN_DEV_BAD_LENGTH = 8u,   /* a sequence length was outside the range that the call states
                                      (the E4M3 decode: [nq, max_kv_len]); attention wrote that
-                                     sequence's rows as O = 0, lse = -inf, an append or an
-                                     eviction left it as it was */
+                                     sequence's rows as O = 0, lse = -inf, an append, an eviction
+                                     or a page-table call left it as it was */
+    GBATTN_DEV_NO_PAGES = 16u     /* kv_paged_extend: the stack of free pages had too few for a
+                                     sequence, which got none and stayed as it was;
+                                     kv_paged_release: it had no room for a sequence's pages */
 };
 
 /* Flags of the causal prefill calls. */
@@ -430,6 +435,122 @@ int attn_diff_prefill_fwd(const void* q, const void* k, const void* v, const flo
                           int Hq, int Hkv, int Sq, int Skv, int D, const int64_t* q_strides,
                           const int64_t* kv_strides, const int64_t* o_strides, float scale,
                           int causal, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Pages and slots for new tokens, from a stack of free pages.
+ * Cites: "Integrate FP32 v37 prefill and exact E4M3 bridge", Implementation (paged cache, page table,
+ * live length); the pages do not say where tables come from.
+ *   page_table     : int32 [B][max_pages], in place; a sequence's row holds its cached tokens' pages
+ *   kv_lens        : int32 [B], cached tokens of every sequence; new_lens: int32 [B], how many come
+ *   free_pages     : int32 [capacity], the pages that no sequence holds, a stack: its first
+ *                    free_count[0] entries, the last of them on top.  Only read.
+ *   kv_lens_out    : int32 [B], kv_lens + new_lens; free_count_out: int32 [1], what is left on the
+ *                    stack.  Each may be the input itself (kv_lens_out == kv_lens, free_count_out ==
+ *                    free_count): a captured step then carries its own state.
+ *   positions,
+ *   slots          : int32 [max_tokens] each, or both NULL: the place in its sequence of every new
+ *                    token, and its slot page * page_size + offset in the pool.  With row_tokens = 0
+ *                    the sequences' new tokens lie end to end; with row_tokens = n > 0, token i of
+ *                    sequence b has entry b * n + i, and max_tokens == B * n.  Entries without a token
+ *                    are -1.  The pair is what kv_paged_rope_append takes.
+ *   token_starts   : int32 [B + 1] or NULL: new tokens of the sequences before b, then of all (not
+ *                    beyond 2^31 - 1)
+ *   A sequence takes the pages that its new tokens need beyond the last one it holds, from the stack's
+ *   top, in the order of the sequences; a page's slots are filled in order.  One whose need the stack
+ *   cannot meet after all before it (GBATTN_DEV_NO_PAGES) takes none: its length stays, its tokens'
+ *   entries are -1 (they keep their places between the others).  Sequences that need no page are not
+ *   affected.  A sequence with kv_lens[b] outside [0, max_pages * page_size], or new_lens[b] outside
+ *   [0, what is left of that] (or above row_tokens > 0), sets GBATTN_DEV_BAD_LENGTH, stays as it is and
+ *   has no tokens.  A free_count outside [0, capacity] sets it too and counts as 0, and so do more
+ *   tokens than max_tokens (row_tokens = 0), of which the first are written.  A page outside
+ *   [0, num_phys_pages) sets GBATTN_DEV_BAD_PAGE; its tokens have slot -1.
+ *   B <= 4096; page_size a power of two >= 16; num_phys_pages * page_size < 2^31; max_pages * page_size,
+ *   B * max_pages <= 2^30.
+ */
+int kv_paged_extend(int32_t* page_table, const int32_t* kv_lens, const int32_t* new_lens,
+                    const int32_t* free_pages, const int32_t* free_count, int32_t* kv_lens_out,
+                    int32_t* free_count_out, int32_t* token_starts, int32_t* positions,
+                    int32_t* slots, int B, int max_pages, int page_size, int num_phys_pages,
+                    int capacity, int row_tokens, int max_tokens, void* stream);
+
+/*
+ * Pages given back to the stack of free pages.
+ * Cites: as kv_paged_extend, whose reverse it is.
+ *   keep_lens      : int32 [B] or NULL (0): the tokens that stay.  So 0 ends a sequence, a shared
+ *                    prefix's length ends one whose prefix others still read, and a length
+ *                    below kv_lens[b] takes drafted or evicted tokens back.
+ *   free_count_out : int32 [1], may be free_count itself
+ *   The pages of tokens keep_lens[b] .. kv_lens[b] - 1 that hold none before keep_lens[b] go onto the
+ *   stack, in the order of the sequences and of their rows.  page_table stays as it is (entries
+ *   past a sequence's pages are not read by any call).  A page must not be given back twice.
+ *   A sequence with kv_lens[b] outside [0, max_pages * page_size] or keep_lens[b] outside [0, kv_lens[b]]
+ *   (GBATTN_DEV_BAD_LENGTH), with a page to be given back outside [0, num_phys_pages)
+ *   (GBATTN_DEV_BAD_PAGE), or whose pages no longer fit on the stack (GBATTN_DEV_NO_PAGES; nor do
+ *   those of the sequences behind it) gives none back.  Sizes as for kv_paged_extend.
+ */
+int kv_paged_release(const int32_t* page_table, const int32_t* kv_lens, const int32_t* keep_lens,
+                     int32_t* free_pages, const int32_t* free_count, int32_t* free_count_out, int B,
+                     int max_pages, int page_size, int num_phys_pages, int capacity, void* stream);
+
+/*
+ * Norms of queries and keys for each head and their rotation by position, in one pass.
+ * The pages have no counterpart: it makes the q and k that the attention calls take.
+ *   q, q_out : [B][Hq][S][D] FP16; k, k_out: [B][Hk][S][D] FP16, or both NULL with Hk = 0
+ *   *_strides: {batch, head, row} element strides or NULL (dense)
+ *   positions: int32 [axes][B][S] on the device; freqs: FP32 [rot / 2], the angle in radians that a
+ *              pair turns by per position, finite (scaling for long contexts is in them)
+ *   q_weight, k_weight: FP32 [D] or NULL (no norm)
+ *   With a weight w a row x becomes x / sqrt(mean(x^2) + eps) * w.  Then pair p < rot / 2 of its
+ *   first rot elements -- elements p and p + rot / 2, or with interleaved = 1 elements 2p and 2p + 1 -- is
+ *   turned by the angle t = position * freqs[p] and scaled by rope_scale:
+ *       (a, b) <- rope_scale (a cos t - b sin t, a sin t + b cos t).
+ *   The other elements stay.  With several axes (positions in a video: frame, row, column),
+ *   sections[i] (a host array, summing to rot / 2) of the pairs, one axis after the other, take
+ *   their position from axis i; sections may be NULL with one axis.  FP32 throughout (angles to a
+ *   2^-32 of a turn), rounded to FP16 once.
+ *   A token with a negative position is padding: its rows of q_out and k_out are left as they are.
+ *   rot = 0: no rotation; positions (NULL, or for the padding alone), freqs, sections and rope_scale unused.
+ *   In place: q_out == q with the same strides, k_out == k likewise.  q_out may also lie in one packed
+ *   tensor with k (and k_out with q) where both have the same batch and row strides and their heads lie in
+ *   different parts of every row.  Other overlaps are rejected.
+ *   D is 64, 128 or 256; rot a multiple of 8, at most D; axes 1..3; eps (with a weight) and rope_scale
+ *   finite, > 0; B * S < 2^31.
+ */
+int qk_norm_rope_f16(const void* q, const void* k, const int32_t* positions, const float* freqs,
+                     const float* q_weight, const float* k_weight, void* q_out, void* k_out, int B,
+                     int Hq, int Hk, int S, int D, int rot, int interleaved, int axes,
+                     const int32_t* sections, const int64_t* q_strides, const int64_t* k_strides,
+                     const int64_t* q_out_strides, const int64_t* k_out_strides, float eps,
+                     float rope_scale, void* stream);
+
+/*
+ * The same on the way into a paged cache: q is normalised and rotated to q_out, k to its slots of the
+ * key pages, and v goes to its slots of the value pages, in one kernel.
+ * Cites: "Integrate FP32 v37 prefill and exact E4M3 bridge", Implementation (paged cache; E4M3 codes
+ * with a scale).
+ *   k_new, v_new : [B][Hkv][S][D] FP16 (they share kv_strides)
+ *   slots        : int32 [B][S], where each token goes: page * page_size + offset (kv_paged_extend).  A
+ *                  negative slot is padding, like a negative position: q_out and the pages stay as they are
+ *                  for that token.  No two tokens of a call may have the same slot.
+ *   k_pages,
+ *   v_pages      : [num_phys_pages][page_size][Hkv][D], elem_size 2 (FP16) or 1 (E4M3 bytes), written in place
+ *   weights      : FP32 [num_phys_pages][Hkv][page_size] or NULL; the new tokens' entries become 0
+ *   An E4M3 byte is the code nearest to value / scale (k_scale, v_scale; ties to even, beyond 448 the
+ *   largest code, NaN stays NaN); FP16 values are not scaled (k_scale and v_scale unused).
+ *   A slot at or past num_phys_pages * page_size sets GBATTN_DEV_BAD_PAGE; the token's q_out is
+ *   written, its K and V are not.
+ *   page_size a power of two >= 16; num_phys_pages * page_size < 2^31; everything else as
+ *   qk_norm_rope_f16.
+ */
+int kv_paged_rope_append(const void* q, const void* k_new, const void* v_new, const int32_t* slots,
+                         const int32_t* positions, const float* freqs, const float* q_weight,
+                         const float* k_weight, void* q_out, void* k_pages, void* v_pages,
+                         float* weights, int B, int Hq, int Hkv, int S, int D, int rot,
+                         int interleaved, int axes, const int32_t* sections,
+                         const int64_t* q_strides, const int64_t* kv_strides,
+                         const int64_t* q_out_strides, int elem_size, int num_phys_pages,
+                         int page_size, float eps, float rope_scale, float k_scale, float v_scale,
+                         void* stream);
 
 /*
  * VSA key-cube selection.
