@@ -47,6 +47,9 @@ _SIGNATURES = {
     "attn_paged_decode_f16_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
     "attn_paged_decode_f16_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i,
                                        _i, _i, _i, _i, _f, _vp, _sz, _vp]),
+    "attn_paged_decode_shared_f16_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
+    "attn_paged_decode_shared_f16_fwd": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i,
+                                              _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _sz, _vp]),
     "kv_paged_evict": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i,
                             _i, _i, _i, _i, _vp]),
     "attn_diff_paged_decode_f16_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i]),
@@ -582,6 +585,52 @@ def attn_paged_decode_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, max_kv_l
                                           workspace.data_ptr(), workspace.nbytes,
                                           _raw_stream(stream, dev))
     _check("attn_paged_decode_f16_fwd", rc)
+    return o
+
+
+def attn_paged_decode_shared_f16_workspace_size(B, Hq, Hkv, nq, groups, max_prefix_len, max_own_len, D):
+    return int(load().attn_paged_decode_shared_f16_workspace_size(B, Hq, Hkv, nq, groups,
+                                                                  max_prefix_len, max_own_len, D))
+
+
+def attn_paged_decode_shared_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, group_starts,
+                                     prefix_lens, max_prefix_len=None, max_own_len=None, o=None,
+                                     lse=None, scale=None, workspace=None, stream=None):
+    """attn_paged_decode_f16_fwd for requests that share prefixes: sequences group_starts[g] ..
+    group_starts[g+1]-1 (int32 [groups+1], from 0 to B) have their first prefix_lens[g] tokens (int32
+    [groups], multiples of the page size) in the pages of the first of them, and those are read once.
+    kv_lens counts prefix and own tokens.  max_prefix_len and max_own_len (what is behind the
+    prefix) default to max_pages * page_size."""
+    import torch
+    dev = _current_device(q, "q")
+    _need_on(q, "q", torch.float16, 4, dev)
+    B, Hq, nq, D = q.shape
+    P, ps, Hkv, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, None, D, dev)
+    _need_on(group_starts, "group_starts", torch.int32, 1, dev)
+    _need_on(prefix_lens, "prefix_lens", torch.int32, 1, dev)
+    groups = prefix_lens.shape[0]
+    _need_shape(group_starts, "group_starts", (groups + 1,))
+    max_prefix_len = _int32(max_pages * ps if max_prefix_len is None else max_prefix_len, "max_prefix_len")
+    max_own_len = _int32(max_pages * ps if max_own_len is None else max_own_len, "max_own_len")
+    if o is None:
+        o = _new_like(q, stream)
+    else:
+        _need_on(o, "o", torch.float16, 4, dev)
+        _need_shape(o, "o", q.shape)
+    if lse is not None:
+        _need_on(lse, "lse", torch.float32, 3, dev)
+        _need_shape(lse, "lse", (B, Hq, nq))
+    if workspace is None:
+        workspace = _scratch(attn_paged_decode_shared_f16_workspace_size(
+            B, Hq, Hkv, nq, groups, max_prefix_len, max_own_len, D), q.device, stream)
+    else:
+        _need_workspace(workspace, dev)
+    rc = load().attn_paged_decode_shared_f16_fwd(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(), kv_lens.data_ptr(),
+        group_starts.data_ptr(), prefix_lens.data_ptr(), o.data_ptr(), _ptr(lse), B, Hq, Hkv, nq, D,
+        groups, P, ps, max_pages, max_prefix_len, max_own_len, _scale(scale, D), workspace.data_ptr(),
+        workspace.nbytes, _raw_stream(stream, dev))
+    _check("attn_paged_decode_shared_f16_fwd", rc)
     return o
 
 

@@ -84,7 +84,8 @@ enum gbattn_device_flag {
     GBATTN_DEV_BAD_PAGE = 2u,     /* a page-table entry was outside [0, num_phys_pages);
                                      that page's tokens were written as zeros */
     GBATTN_DEV_BAD_INDEX = 4u,    /* a VSA cube list was not strictly ascending or held an
-                                     index outside [0, S/block); the entry was skipped */
+                                     index outside [0, S/block); the entry was skipped.  Or the
+                                     groups of a shared decode do not cover its sequences */
     GBATTN_DEV_BAD_LENGTH = 8u,   /* a sequence length was outside the range that the call states
                                      (the E4M3 decode: [nq, max_kv_len]); attention wrote that
                                      sequence's rows as O = 0, lse = -inf, an append, an eviction
@@ -345,6 +346,48 @@ int attn_paged_decode_f16_fwd(const void* q, const void* k_pages, const void* v_
                               float* weights, int B, int Hq, int Hkv, int nq, int D,
                               int num_phys_pages, int page_size, int max_pages, int max_kv_len,
                               float scale, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Decode attention over a paged FP16 KV cache for requests that share prefixes: what a group of
+ * sequences has in common is read once for all of them.
+ * Cites: as attn_paged_decode_fwd; prefixes in common have no counterpart there.
+ *   group_starts : int32 [groups + 1] on the device, ascending from 0 to B: sequences
+ *                  group_starts[g] .. group_starts[g + 1] - 1 are group g (none, one or more)
+ *   prefix_lens  : int32 [groups] on the device: the first prefix_lens[g] tokens of every sequence of the
+ *                  group are those in the pages of the group's first sequence; a multiple of page_size, 0
+ *                  for a group with nothing in common
+ *   kv_lens      : int32 [B], cached tokens per sequence, the prefix and the new ones included; what lies
+ *                  behind the prefix is in the sequence's own page-table row, from entry
+ *                  prefix_lens[g] / page_size on (a row's entries before that are read of a group's first
+ *                  sequence only)
+ *   The result is attn_paged_decode_f16_fwd's with these tables: query i of sequence b sits at position
+ *   kv_lens[b] - nq + i (also within the prefix, where there are more queries than own tokens) and sees the
+ *   tokens up to it.  Precision and infinite or NaN values as there; a value within the prefix that is
+ *   infinite or NaN may also reach the queries of the group that sit before it, unless they see no token
+ *   of the prefix at all.
+ *   max_prefix_len bounds the prefixes and max_own_len every kv_lens[b] - prefix_lens[g], both at most
+ *   max_pages * page_size, 2^30; 0 allowed.  A prefix_lens[g] that is negative, above
+ *   max_prefix_len or no multiple of page_size, or a kv_lens[b] outside
+ *   [prefix_lens[g], prefix_lens[g] + max_own_len], sets GBATTN_DEV_BAD_LENGTH and yields O = 0,
+ *   lse = -inf for the group or the sequence.  group_starts that do not ascend from 0 to B set
+ *   GBATTN_DEV_BAD_INDEX and yield O = 0, lse = -inf for all sequences.  Pages as for
+ *   attn_paged_decode_f16_fwd.
+ *   D is 64, 128 or 256; page_size a power of two >= 16; Hq % Hkv == 0; B, groups <= 4096; B * Hq * nq <= 2^30;
+ *   num_phys_pages * page_size < 2^31.
+ *   The workspace (required, 32-byte aligned) holds the FP32 partial results of both kinds of tokens;
+ *   attn_paged_decode_shared_f16_workspace_size() gives the full-speed size, a smaller one runs fewer CTAs, and
+ *   below that of two GBATTN_ERR_WORKSPACE is returned.  It needs no initial value; calls that may
+ *   run at the same time need separate ones.
+ */
+size_t attn_paged_decode_shared_f16_workspace_size(int B, int Hq, int Hkv, int nq, int groups,
+                                                   int max_prefix_len, int max_own_len, int D);
+int attn_paged_decode_shared_f16_fwd(const void* q, const void* k_pages, const void* v_pages,
+                                     const int32_t* page_table, const int32_t* kv_lens,
+                                     const int32_t* group_starts, const int32_t* prefix_lens, void* o,
+                                     float* lse, int B, int Hq, int Hkv, int nq, int D, int groups,
+                                     int num_phys_pages, int page_size, int max_pages,
+                                     int max_prefix_len, int max_own_len, float scale,
+                                     void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Eviction from a paged KV cache by accumulated attention weight.

@@ -9,8 +9,8 @@ import numpy as np
 import pytest
 
 from oracle import rope as OR, tables as OT
-from tests.test_abi_paged import (ALIAS, ALIGN, CUDA, MIS2, MIS8, NULL, OK, SCALE, SHAPE, UNSUPPORTED, A,
-                                  caller, lib)
+from tests.test_abi_paged import (ALIAS, ALIGN, CUDA, MIS2, MIS8, NULL, OK, SCALE, SHAPE, UNSUPPORTED,
+                                  WORKSPACE, A, caller, lib)
 
 assert lib
 
@@ -157,6 +157,51 @@ def test_rope_append_refusals(lib):
     assert call(rot=0, pos=None, freqs=None) in (OK, CUDA)
 
 
+SHARED = ("q", "kp", "vp", "table", "lens", "starts", "pre", "o", "lse", "B", "Hq", "Hkv", "nq", "D",
+          "groups", "P", "ps", "mp", "maxp", "maxo", "scale", "ws", "wsb", "stream")
+
+
+def test_shared_decode_refusals(lib):
+    base = dict(zip(SHARED, [A(i) for i in range(9)] + [4, 4, 2, 1, 128, 2, 16, 16, 8, 64, 128, 0.1, A(20),
+                                                        1 << 28, None]))
+    call = caller(lib.attn_paged_decode_shared_f16_fwd, SHARED, base)
+    for n in SHARED[:8]:
+        assert call(**{n: None}) == NULL
+    for n in ("B", "Hq", "Hkv", "nq", "groups", "P", "ps", "mp"):
+        assert call(**{n: 0}) == SHAPE and call(**{n: -1}) == SHAPE
+    assert call(maxp=-1) == SHAPE and call(maxo=-1) == SHAPE and call(maxp=129) == SHAPE
+    assert call(maxo=129) == SHAPE and call(Hq=5) == SHAPE and call(mp=1 << 28, maxo=(1 << 30) + 1) == SHAPE
+    assert call(Hq=2 ** 30, nq=1) == SHAPE
+    for kw in (dict(D=96), dict(ps=24), dict(ps=8), dict(P=1 << 27), dict(B=4097), dict(groups=4097)):
+        assert call(**kw) == UNSUPPORTED
+    for x in (0.0, -1.0, math.nan, math.inf):
+        assert call(scale=x) == SCALE
+    for n in ("q", "kp", "vp", "o", "ws"):
+        assert call(**{n: MIS8}) == ALIGN
+    assert call(ws=ctypes.c_void_p(A(20).value + 16)) == ALIGN
+    for n in ("table", "lens", "starts", "pre", "lse"):
+        assert call(**{n: MIS2}) == ALIGN
+    assert call(ws=None) == WORKSPACE
+    assert call(wsb=100) in (WORKSPACE, CUDA)
+    for n in ("o", "lse"):
+        for i in range(7):
+            assert call(**{n: A(i)}) == ALIAS
+    assert call(lse=A(7)) == ALIAS
+    assert call() in (OK, CUDA) and call(lse=None, maxp=0, maxo=0) in (OK, CUDA)
+
+
+def test_shared_decode_workspace_sizes(lib):
+    size = lib.attn_paged_decode_shared_f16_workspace_size
+    for bad in ((0, 4, 2, 1, 1, 64, 64, 128), (2, 5, 2, 1, 1, 64, 64, 128), (2, 4, 2, 1, 0, 64, 64, 128),
+                (2, 4, 2, 1, 1, -1, 64, 128), (2, 4, 2, 1, 1, 64, -1, 128)):
+        assert size(*bad) == 0
+    # beside the ordinary decode's, a record of every row and 128 rows a CTA, and the tables
+    plain = lib.attn_paged_decode_f16_workspace_size(64, 32, 8, 1, 2048, 128, 0)
+    rows = 152 * 128 + 64 * 32
+    extra = size(64, 32, 8, 1, 3, 1 << 20, 2048, 128) - plain
+    assert rows * (128 * 4 + 8) <= extra <= rows * (128 * 4 + 8) + 64 * 8 + 200
+
+
 def test_wrappers_refuse_wrong_arguments(lib):
     import torch
     import attention_fp16_flashattention_gb300 as gb
@@ -165,7 +210,8 @@ def test_wrappers_refuse_wrong_arguments(lib):
     for call in (lambda x: gb.kv_paged_extend(x, i, i, i, i, 16, 4),
                  lambda x: gb.kv_paged_release(x, i, i, i, 16, 4),
                  lambda x: gb.qk_norm_rope_f16(x, None, i, z),
-                 lambda x: gb.kv_paged_rope_append(x, z, z, i, z, z, i, z)):
+                 lambda x: gb.kv_paged_rope_append(x, z, z, i, z, z, i, z),
+                 lambda x: gb.attn_paged_decode_shared_f16_fwd(x, z, z, i, i, i, i)):
         for x in (z, i, None):
             with pytest.raises(ValueError):
                 call(x)
