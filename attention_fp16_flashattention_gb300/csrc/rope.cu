@@ -28,6 +28,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxAxes = 3;
+constexpr int kBlocks = 3, kAhead = 4;
 
 struct View {   // [B][H][S][D] rows
     __half* p;
@@ -42,11 +43,12 @@ struct RopeArgs {
     const int32_t* slots;            // [B][S]
     const float *freqs, *q_weight, *k_weight;
     uint32_t* status;
-    long long tokens;                // B * S
-    int B, S, Hq, Hk, rot8;          // rot8: rot / 8, lanes with pairs
-    int axis_end[kMaxAxes];          // pairs before the end of each axis
+    uint32_t tokens, S;              // B * S tokens
+    int Hq, Hk, rot8;                // rot8: rot / 8, lanes with pairs
+    int axis_end[kMaxAxes - 1];      // pairs before the end of each axis
     int axes, slots_total, page_bits;
-    int rows, rows_per, parts;       // rows of a token, of a warp, warps a token
+    int q_steps, k_steps, steps;     // row steps of q, of k (and of v), of a token
+    uint32_t steps_per, parts;       // of a warp; warps a token
     float eps, scale, k_scale, v_scale;
 };
 
@@ -59,32 +61,53 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
     return static_cast<uint32_t>(lo) | (static_cast<uint32_t>(hi) << 16);
 }
 
-// Four elements of a cached row at p (element offset `at`).
-template <Store kStore>
-__device__ __forceinline__ void store_cached(void* p, long long at, const float (&x)[4], float scale) {
-    if constexpr (kStore == kE4m3Pages)
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p) + at) =
-            pack_e4m3(x[0] / scale, x[1] / scale, x[2] / scale, x[3] / scale);
+// The eight elements of a lane as they lie in memory: two groups of four.
+struct Raw {
+    uint2 lo, hi;
+};
+__device__ __forceinline__ float2 unpack_half2(uint32_t u) {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u));
+}
+
+// First and second elements of the lane's pairs, two pairs in each (f32x2).
+struct Pairs {
+    uint64_t a[2], b[2];
+};
+template <bool kInterleaved>
+__device__ __forceinline__ Pairs to_pairs(const Raw& r) {
+    const float2 x = unpack_half2(r.lo.x), y = unpack_half2(r.lo.y);
+    const float2 z = unpack_half2(r.hi.x), w = unpack_half2(r.hi.y);
+    if constexpr (kInterleaved)
+        return Pairs{{f2_pack(x.x, y.x), f2_pack(z.x, w.x)}, {f2_pack(x.y, y.y), f2_pack(z.y, w.y)}};
     else
-        *reinterpret_cast<uint2*>(static_cast<__half*>(p) + at) =
-            make_uint2(pack_half2(x[0], x[1]), pack_half2(x[2], x[3]));
+        return Pairs{{f2_pack(x.x, x.y), f2_pack(y.x, y.y)}, {f2_pack(z.x, z.y), f2_pack(w.x, w.y)}};
+}
+template <bool kInterleaved>
+__device__ __forceinline__ void from_pairs(const Pairs& p, float (&lo)[4], float (&hi)[4]) {
+    float a[4], b[4];
+    f2_unpack(p.a[0], a[0], a[1]);
+    f2_unpack(p.a[1], a[2], a[3]);
+    f2_unpack(p.b[0], b[0], b[1]);
+    f2_unpack(p.b[1], b[2], b[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (kInterleaved) {
+            lo[e] = e % 2 == 0 ? a[e / 2] : b[e / 2];
+            hi[e] = e % 2 == 0 ? a[2 + e / 2] : b[2 + e / 2];
+        } else {
+            lo[e] = a[e];
+            hi[e] = b[e];
+        }
+    }
 }
 
-__device__ __forceinline__ void load4(const __half* p, float (&x)[4]) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&u.x));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&u.y));
-    x[0] = a.x;
-    x[1] = a.y;
-    x[2] = b.x;
-    x[3] = b.y;
-}
-
-// A warp takes rows_per rows (of q, then k, then v) of one token, 32 / (D / 8) of them at a time.
+// A warp takes a range of a token's row steps -- q's, then k's, then v's; a step is 32 / (D / 8) rows -- and loads
+// kAhead of them at a time.
 template <int D, bool kInterleaved, Store kStore>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocks) qk_norm_rope_kernel(const RopeArgs a) {
     constexpr int kLanes = D / 8;          // lanes of a row
-    constexpr int kSide = 32 / kLanes;     // rows of a warp at a time
+    constexpr int kSide = 32 / kLanes;     // rows of a step
+    constexpr int kOwn = 4 / kSide;        // of a lane's four angles, those that it works out itself
     __shared__ unsigned long long s_turn[D / 2];   // parts of a turn per position, in 2^-64
     for (int p = threadIdx.x; p < 4 * a.rot8; p += kThreads) {
         double t = static_cast<double>(a.freqs[p]) * 0.15915494309189535;   // 1 / (2 pi)
@@ -98,108 +121,209 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const RopeArgs a
     const bool turns = lr < a.rot8;
     const int c0 = kInterleaved ? 8 * lr : turns ? 4 * lr : 8 * lr;
     const int c1 = kInterleaved || !turns ? c0 + 4 : c0 + 4 * a.rot8;
-    float wq[8], wk[8];
+    const uint32_t units = a.tokens * a.parts, stride = gridDim.x * kWarps;
+    // What a unit's token needs to know first is loaded for 32 units of the warp at once, a lane each.
+    int my_slot = 0, my_pos[kMaxAxes] = {0, 0, 0};
+    uint32_t turn = 0;
+    for (uint32_t u = blockIdx.x * kWarps + warp; u < units; u += stride, ++turn) {
+        const uint32_t token = u / a.parts, part = u - token * a.parts;
+        if ((turn & 31) == 0) {
+            const unsigned long long ahead = u + static_cast<unsigned long long>(stride) * lane;
+            if (ahead < units) {
+                const uint32_t t = static_cast<uint32_t>(ahead) / a.parts;
+                if (kStore != kDense) my_slot = a.slots[t];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        const int c = e < 4 ? c0 + e : c1 + e - 4;
-        wq[e] = a.q_weight ? a.q_weight[c] : 1.0f;
-        wk[e] = a.k_weight ? a.k_weight[c] : 1.0f;
-    }
-    int axis[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const int p = 4 * lr + e;
-        axis[e] = (p >= a.axis_end[0]) + (p >= a.axis_end[1]);
-    }
-    const long long units = a.tokens * a.parts;
-    for (long long u = static_cast<long long>(blockIdx.x) * kWarps + warp; u < units;
-         u += static_cast<long long>(gridDim.x) * kWarps) {
-        const long long token = u / a.parts;
-        const int part = static_cast<int>(u - token * a.parts);
-        const int b = static_cast<int>(token / a.S), s = static_cast<int>(token - static_cast<long long>(b) * a.S);
-        long long slot = 0;
-        bool cached = true;
-        if constexpr (kStore != kDense) {
-            slot = a.slots[token];
-            if (slot < 0) continue;   // padding
-            if (slot >= a.slots_total) {
-                cached = false;
-                if (lane == 0 && part == 0) atomicOr(a.status, kDevBadPage);
+                for (int i = 0; i < kMaxAxes; ++i)
+                    if (a.positions && i < a.axes)
+                        my_pos[i] = a.positions[static_cast<long long>(i) * a.tokens + t];
             }
         }
-        float cs[4], sn[4];
-        if (a.positions) {
-            const bool skip = lane < a.axes && a.positions[lane * a.tokens + token] < 0;
-            if (__any_sync(0xffffffffu, skip)) continue;   // padding
+        const long long slot = __shfl_sync(0xffffffffu, my_slot, turn & 31);
+        int pos[kMaxAxes];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int pos = a.positions[(turns ? axis[e] : 0) * a.tokens + token];
+        for (int i = 0; i < kMaxAxes; ++i) pos[i] = __shfl_sync(0xffffffffu, my_pos[i], turn & 31);
+        if (slot < 0 || pos[0] < 0 || pos[1] < 0 || pos[2] < 0) continue;   // padding
+        const bool cached = kStore == kDense || slot < a.slots_total;
+        if (!cached && lane == 0 && part == 0) atomicOr(a.status, kDevBadPage);
+        const uint32_t b = token / a.S, s = token - b * a.S;
+        const int t_beg = static_cast<int>(part * a.steps_per);
+        const int t_end = min(t_beg + static_cast<int>(a.steps_per), a.steps);
+        // One tensor's rows from step t on, two pointers a lane.
+        Raw raw[kAhead];
+        const __half *p0 = nullptr, *p1 = nullptr;
+        long long apart = 0;   // of a step's rows
+        int h = 0;             // the row that is loaded next
+        auto load = [&](Raw& r, bool in_range, int H) {
+            if (in_range && h < H) {
+                r.lo = *reinterpret_cast<const uint2*>(p0);
+                r.hi = *reinterpret_cast<const uint2*>(p1);
+            }
+            p0 += apart;
+            p1 += apart;
+            h += kSide;
+        };
+        auto begin = [&](const View& v, int t0, int t1, int H) {
+            h = t0 * kSide + side;
+            const __half* row = v.p + b * v.b + s * v.s + h * v.h;
+            p0 = row + c0;
+            p1 = row + c1;
+            apart = kSide * v.h;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                raw[i] = Raw{};
+                load(raw[i], t0 + i < t1, H);
+            }
+        };
+        const bool has_q = t_beg < a.q_steps;
+        const int q_end = min(t_end, a.q_steps);
+        if (has_q) begin(a.q, t_beg, q_end, a.Hq);
+        float cs[4], sn[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sn[e] = 0.0f, cs[e] = 1.0f;
+        if (a.rot8) {
+            // The rows side by side in the warp share their angles: each side works out its part.
+            float own_c[kOwn], own_s[kOwn];
+#pragma unroll
+            for (int e = 0; e < kOwn; ++e) {
+                const int p = 4 * lr + side * kOwn + e;
+                const int at = p < a.axis_end[0] ? pos[0] : p < a.axis_end[1] ? pos[1] : pos[2];
                 const unsigned long long angle =
-                    turns ? s_turn[turns ? 4 * lr + e : 0] * static_cast<unsigned long long>(static_cast<uint32_t>(pos)) : 0;
+                    s_turn[turns ? p : 0] * static_cast<unsigned long long>(static_cast<uint32_t>(at));
                 // half turns in [-1, 1)
                 const float x = static_cast<float>(static_cast<int>(angle >> 32)) * 4.656612873077393e-10f;
-                sincospif(x, &sn[e], &cs[e]);
-                sn[e] *= a.scale;
-                cs[e] *= a.scale;
+                sincospif(x, &own_s[e], &own_c[e]);
             }
-        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sn[e] = 0.0f, cs[e] = 1.0f;
+            for (int e = 0; e < 4; ++e) {
+                const int from = lr + kLanes * (e / kOwn);
+                const float c = __shfl_sync(0xffffffffu, own_c[e % kOwn], from);
+                const float n = __shfl_sync(0xffffffffu, own_s[e % kOwn], from);
+                if (turns) cs[e] = c * a.scale, sn[e] = n * a.scale;
+            }
         }
-        const int r_end = min((part + 1) * a.rows_per, a.rows);
-#pragma unroll 2
-        for (int r0 = part * a.rows_per; r0 < r_end; r0 += kSide) {
-            const int r = r0 + side;
-            const bool live = r < r_end;
-            const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.Hk;
-            const int h = is_q ? r : is_v ? r - a.Hq - a.Hk : r - a.Hq;
-            const View& in = is_q ? a.q : is_v ? a.v : a.k;
-            float x[8];
-            float lo[4] = {0.0f, 0.0f, 0.0f, 0.0f}, hi[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            if (live) {
-                const __half* row = in.p + b * in.b + h * in.h + s * in.s;
-                load4(row + c0, lo);
-                load4(row + c1, hi);
+        // Steps t0 .. t1 - 1 of the tensor that `begin` began, through `put(row, live, Pairs)`.
+        auto rows = [&](int t0, int t1, int H, const float* weight, auto put) {
+            // Coefficients of the two elements of each pair, the norm's weights in them:
+            // (aa x_a - ab x_b, ba x_a + bb x_b)
+            uint64_t aa[2], ab[2], ba[2], bb[2];
+            float wa[4], wb[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                wa[e] = weight ? weight[kInterleaved ? c0 + 2 * e : c0 + e] : 1.0f;
+                wb[e] = weight ? weight[kInterleaved ? c0 + 2 * e + 1 : c1 + e] : 1.0f;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = lo[e], x[4 + e] = hi[e];
-            float sq = 0.0f;
+            for (int i = 0; i < 2; ++i) {
+                aa[i] = f2_pack(cs[2 * i] * wa[2 * i], cs[2 * i + 1] * wa[2 * i + 1]);
+                ab[i] = f2_pack(-sn[2 * i] * wb[2 * i], -sn[2 * i + 1] * wb[2 * i + 1]);
+                ba[i] = f2_pack(sn[2 * i] * wa[2 * i], sn[2 * i + 1] * wa[2 * i + 1]);
+                bb[i] = f2_pack(cs[2 * i] * wb[2 * i], cs[2 * i + 1] * wb[2 * i + 1]);
+            }
+            for (int t = t0; t < t1; t += kAhead) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) sq += x[e] * x[e];
+                for (int i = 0; i < kAhead; ++i) {
+                    if (t + i >= t1) break;
+                    const Pairs x = to_pairs<kInterleaved>(raw[i]);
+                    load(raw[i], t + i + kAhead < t1, H);
+                    const int row = h - (kAhead + 1) * kSide;   // h is kAhead steps on and one more
+                    Pairs y;
 #pragma unroll
-            for (int sh = 1; sh < kLanes; sh <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, sh);
-            if (!live) continue;
-            if (!is_v) {
-                const bool norm = is_q ? a.q_weight != nullptr : a.k_weight != nullptr;
-                const float rn = norm ? rsqrtf(sq * (1.0f / D) + a.eps) : 1.0f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= rn * (is_q ? wq[e] : wk[e]);
-                if (turns) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        float& m = kInterleaved ? x[2 * e] : x[e];
-                        float& n = kInterleaved ? x[2 * e + 1] : x[4 + e];
-                        const float y = cs[e] * m - sn[e] * n;
-                        n = sn[e] * m + cs[e] * n;
-                        m = y;
+                    for (int j = 0; j < 2; ++j) {
+                        y.a[j] = f2_mul(aa[j], x.a[j]);
+                        y.b[j] = f2_mul(bb[j], x.b[j]);
+                        if (turns) {
+                            y.a[j] = f2_fma(ab[j], x.b[j], y.a[j]);
+                            y.b[j] = f2_fma(ba[j], x.a[j], y.b[j]);
+                        }
                     }
+                    if (weight) {
+                        uint64_t s2 = f2_mul(x.a[0], x.a[0]);
+                        s2 = f2_fma(x.a[1], x.a[1], s2);
+                        s2 = f2_fma(x.b[0], x.b[0], s2);
+                        s2 = f2_fma(x.b[1], x.b[1], s2);
+                        float s0, s1;
+                        f2_unpack(s2, s0, s1);
+                        float sq = s0 + s1;
+#pragma unroll
+                        for (int sh = 1; sh < kLanes; sh <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, sh);
+                        const float rn = rsqrtf(sq * (1.0f / D) + a.eps);
+                        const uint64_t rn2 = f2_pack(rn, rn);
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            y.a[j] = f2_mul(y.a[j], rn2);
+                            y.b[j] = f2_mul(y.b[j], rn2);
+                        }
+                    }
+                    put(row, row < H, y);
                 }
             }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) lo[e] = x[e], hi[e] = x[4 + e];
-            if (is_q || kStore == kDense) {
-                const View& out = is_q ? a.q_out : a.k_out;
-                __half* row = out.p + b * out.b + h * out.h + s * out.s;
+        };
+        // FP16 rows from `out` on, out_h apart
+        auto to_half = [&](__half* out, long long out_h) {
+            return [=](int h, bool live, const Pairs& y) {
+                float lo[4], hi[4];
+                from_pairs<kInterleaved>(y, lo, hi);
+                if (!live) return;
+                __half* row = out + h * out_h;
                 *reinterpret_cast<uint2*>(row + c0) = make_uint2(pack_half2(lo[0], lo[1]), pack_half2(lo[2], lo[3]));
                 *reinterpret_cast<uint2*>(row + c1) = make_uint2(pack_half2(hi[0], hi[1]), pack_half2(hi[2], hi[3]));
-            } else if (cached) {
-                const long long at = (slot * a.Hk + h) * D;
-                void* pages = is_v ? a.v_pages : a.k_pages;
-                store_cached<kStore>(pages, at + c0, lo, is_v ? a.v_scale : a.k_scale);
-                store_cached<kStore>(pages, at + c1, hi, is_v ? a.v_scale : a.k_scale);
-                if (!is_v && lr == 0 && a.weights)
-                    a.weights[((slot >> a.page_bits) * a.Hk + h) * (1LL << a.page_bits) +
-                              (slot & ((1LL << a.page_bits) - 1))] = 0.0f;
+            };
+        };
+        // E4M3 codes of the values over `scale`
+        auto to_codes = [&](void* pages, float scale) {
+            uint8_t* out = static_cast<uint8_t*>(pages) + slot * a.Hk * D;
+            return [=](int h, bool live, const Pairs& y) {
+                float lo[4], hi[4];
+                from_pairs<kInterleaved>(y, lo, hi);
+                if (!live) return;
+                uint8_t* row = out + h * D;
+                *reinterpret_cast<uint32_t*>(row + c0) =
+                    pack_e4m3(lo[0] / scale, lo[1] / scale, lo[2] / scale, lo[3] / scale);
+                *reinterpret_cast<uint32_t*>(row + c1) =
+                    pack_e4m3(hi[0] / scale, hi[1] / scale, hi[2] / scale, hi[3] / scale);
+            };
+        };
+        if (has_q)
+            rows(t_beg, q_end, a.Hq, a.q_weight,
+                 to_half(a.q_out.p + b * a.q_out.b + s * a.q_out.s, a.q_out.h));
+        if (!cached) continue;
+        const int k_beg = max(t_beg - a.q_steps, 0), k_end = min(t_end - a.q_steps, a.k_steps);
+        if (k_beg < k_end) {
+            begin(a.k, k_beg, k_end, a.Hk);
+            if constexpr (kStore == kDense)
+                rows(k_beg, k_end, a.Hk, a.k_weight,
+                     to_half(a.k_out.p + b * a.k_out.b + s * a.k_out.s, a.k_out.h));
+            else if constexpr (kStore == kF16Pages)
+                rows(k_beg, k_end, a.Hk, a.k_weight,
+                     to_half(static_cast<__half*>(a.k_pages) + slot * a.Hk * D, D));
+            else
+                rows(k_beg, k_end, a.Hk, a.k_weight, to_codes(a.k_pages, a.k_scale));
+            if (kStore != kDense && a.weights) {
+                float* w = a.weights + (slot >> a.page_bits) * a.Hk * (1LL << a.page_bits) +
+                           (slot & ((1LL << a.page_bits) - 1));
+                for (int x = k_beg * kSide + lane; x < min(k_end * kSide, a.Hk); x += 32)
+                    w[static_cast<long long>(x) << a.page_bits] = 0.0f;
+            }
+        }
+        if constexpr (kStore != kDense) {   // v: as it is
+            const int v_beg = max(t_beg - a.q_steps - a.k_steps, 0), v_end = t_end - a.q_steps - a.k_steps;
+            if (v_beg < v_end) begin(a.v, v_beg, v_end, a.Hk);
+            for (int t = v_beg; t < v_end; t += kAhead) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (t + i >= v_end) break;
+                    const Raw r = raw[i];
+                    load(raw[i], t + i + kAhead < v_end, a.Hk);
+                    const int row_h = (t + i) * kSide + side;
+                    if (row_h >= a.Hk) continue;
+                    if constexpr (kStore == kF16Pages) {
+                        __half* row = static_cast<__half*>(a.v_pages) + (slot * a.Hk + row_h) * D;
+                        *reinterpret_cast<uint2*>(row + c0) = r.lo;
+                        *reinterpret_cast<uint2*>(row + c1) = r.hi;
+                    } else {
+                        to_codes(a.v_pages, a.v_scale)(row_h, true, to_pairs<kInterleaved>(r));
+                    }
+                }
             }
         }
     }
@@ -349,16 +473,15 @@ int run_rope(const RopeCall& c) {
     a.q_weight = c.q_weight;
     a.k_weight = c.k_weight;
     a.status = dev.status;
-    a.tokens = tokens;
-    a.B = c.B;
-    a.S = c.S;
+    a.tokens = static_cast<uint32_t>(tokens);
+    a.S = static_cast<uint32_t>(c.S);
     a.Hq = c.Hq;
     a.Hk = c.Hk;
     a.rot8 = c.rot / 8;
     int end = 0;
-    for (int i = 0; i < kMaxAxes; ++i) {
+    for (int i = 0; i + 1 < kMaxAxes; ++i) {
         if (c.sections && i < c.axes) end += c.sections[i];
-        a.axis_end[i] = c.axes > 1 && i + 1 < c.axes ? end : 0x7FFFFFFF;
+        a.axis_end[i] = i + 1 < c.axes ? end : 0x7FFFFFFF;
     }
     a.axes = c.axes;
     if (c.append) {
@@ -369,17 +492,18 @@ int run_rope(const RopeCall& c) {
     a.scale = c.rope_scale;
     a.k_scale = c.k_scale;
     a.v_scale = c.v_scale;
-    // A warp takes all rows of a token, or with few tokens a part of them, so that the GPU is filled.
     const int side = 256 / c.D;
-    a.rows = c.Hq + (c.append ? 2 : 1) * c.Hk;
-    const long long warps = 32LL * dev.num_sms;
+    a.q_steps = (c.Hq + side - 1) / side;
+    a.k_steps = (c.Hk + side - 1) / side;
+    a.steps = a.q_steps + (c.append ? 2 : 1) * a.k_steps;
+    // A warp takes all rows of a token, or with few tokens a part of them, so that the GPU is filled.
+    const long long warps = static_cast<long long>(kBlocks) * kWarps * dev.num_sms;
     long long parts = (warps + tokens - 1) / tokens;
-    const long long most = (a.rows + side - 1) / side;
-    if (parts > most) parts = most;
-    a.rows_per = static_cast<int>((most + parts - 1) / parts) * side;
-    a.parts = (a.rows + a.rows_per - 1) / a.rows_per;
+    if (parts > a.steps) parts = a.steps;
+    a.steps_per = static_cast<uint32_t>((a.steps + parts - 1) / parts);
+    a.parts = (a.steps + a.steps_per - 1) / a.steps_per;
     const long long blocks = (tokens * a.parts + kWarps - 1) / kWarps;
-    const long long resident = 8LL * dev.num_sms;
+    const long long resident = static_cast<long long>(kBlocks) * dev.num_sms;
     const int grid = static_cast<int>(blocks < resident ? blocks : resident);
     cudaStream_t s = static_cast<cudaStream_t>(c.stream);
     const bool il = c.interleaved != 0;
