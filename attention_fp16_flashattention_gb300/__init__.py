@@ -825,30 +825,28 @@ def kv_paged_extend(page_table, kv_lens, new_lens, free_pages, free_count, page_
     n = _int32(n, "max_tokens")
     if max_tokens is not None and n <= 0:
         raise ValueError("max_tokens must be positive")
-    dev = page_table.device
-    if kv_lens_out is None:
-        kv_lens_out = _new_tensor((B,), torch.int32, dev, stream)
-    if free_count_out is None:
-        free_count_out = _new_tensor((1,), torch.int32, dev, stream)
-    for t, name, shape in ((kv_lens_out, "kv_lens_out", (B,)), (free_count_out, "free_count_out", (1,))):
-        _need_on(t, name, torch.int32, 1, cur)
-        _need_shape(t, name, shape)
-    if n == 0:
-        if token_starts is not None or positions is not None or slots is not None:
-            raise ValueError("token_starts, positions and slots need max_tokens or row_tokens")
+    if n == 0 and not (token_starts is None and positions is None and slots is None):
+        raise ValueError("token_starts, positions and slots need max_tokens or row_tokens")
+    # What the caller does not give comes out of one allocation (each costs as much as the checks).
+    shape = (B, rows) if rows else (n,)
+    outs = ((kv_lens_out, "kv_lens_out", (B,), B), (free_count_out, "free_count_out", (1,), 1))
+    if n:
+        outs += ((token_starts, "token_starts", (B + 1,), B + 1), (positions, "positions", shape, n),
+                 (slots, "slots", shape, n))
+    for t, name, want, _ in outs:
+        if t is not None:
+            _need_on(t, name, torch.int32, len(want), cur)
+            _need_shape(t, name, want)
+    sizes = [size for t, _, _, size in outs if t is None]
+    if sizes:
+        new = iter(_new_tensor((sum(sizes),), torch.int32, page_table.device,
+                               stream).split_with_sizes(sizes))
+        outs = [next(new) if t is None else t for t, _, _, _ in outs]
     else:
-        shape = (B, rows) if rows else (n,)
-        if token_starts is None:
-            token_starts = _new_tensor((B + 1,), torch.int32, dev, stream)
-        if positions is None:
-            positions = _new_tensor(shape, torch.int32, dev, stream)
-        if slots is None:
-            slots = _new_tensor(shape, torch.int32, dev, stream)
-        _need_on(token_starts, "token_starts", torch.int32, 1, cur)
-        _need_shape(token_starts, "token_starts", (B + 1,))
-        for t, name in ((positions, "positions"), (slots, "slots")):
-            _need_on(t, name, torch.int32, len(shape), cur)
-            _need_shape(t, name, shape)
+        outs = [t for t, _, _, _ in outs]
+    if rows:
+        outs[3:] = [t if t.dim() == 2 else t.view(shape) for t in outs[3:]]
+    kv_lens_out, free_count_out, token_starts, positions, slots = outs + [None] * (5 - len(outs))
     rc = load().kv_paged_extend(page_table.data_ptr(), kv_lens.data_ptr(), new_lens.data_ptr(),
                                 free_pages.data_ptr(), free_count.data_ptr(), kv_lens_out.data_ptr(),
                                 free_count_out.data_ptr(), _ptr(token_starts), _ptr(positions),

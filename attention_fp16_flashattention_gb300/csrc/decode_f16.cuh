@@ -758,24 +758,34 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
 // kShared: besides those of its own tokens (a decode_f16_body's), a row has the records of its group's
 // prefix (decode_shared.cu): one of every CTA whose range of the prefix's tiles meets the row's unit.
 struct PrefixRecords {
-    const float* part_o;     // [row][D] unnormalised: row = 128 * CTA + the row's place among all
+    const float* part_o;     // [row][D] unnormalised: row = unit rows * CTA + the row's place among all
     const float2* part_ml;
-    const uint32_t* tiles;   // [groups + 1]: prefix tiles of the units of the groups before g
+    const uint32_t* work;    // [groups + 1]: prefix steps of the units of the groups before g
     const int2* seq;         // [B]: the prefix's tokens (-1: rejected) and the group
     const uint32_t* total;   // tiles of all sequences' own tokens
-    const int32_t* starts;   // [groups + 1]: first sequence of each group
-    int groups;
+    const int32_t *starts, *lens;   // of the call: [groups + 1], [groups]
+    int groups, max_prefix, ps;
 };
-// Units of a group: tiles of kUnitRows query rows of a KV head, and of kPreTile prefix tokens each.
-constexpr int kUnitRows = 128, kPreTile = 64;
+// A unit: up to kUnit query rows of a group and KV head.  A step: 128 of its rows against kPreTile prefix tokens;
+// a unit of more than 128 rows takes two steps a tile.
+constexpr int kStepRows = 128, kPreTile = 64;
+template <int D>
+struct Unit {
+    static constexpr int kRows = D == 256 ? 128 : 256;
+};
+// Steps that a tile takes with `rows` query rows of a KV head.
+__device__ __forceinline__ uint32_t steps_of_rows(int rows) {
+    return static_cast<uint32_t>((rows + kStepRows - 1) / kStepRows);
+}
 
-// How many of `grid` CTAs work on the prefixes' `pre` tiles of kUnitRows rows and kPreTile tokens when the
-// others work on `own` tiles of kTile tokens.
+// How many of `grid` CTAs work on the prefixes' `pre` steps when the others work on `own` tiles of kTile tokens.
+template <int D>
 __device__ __forceinline__ uint32_t prefix_ctas(uint32_t grid, uint32_t pre, uint32_t own) {
     if (pre == 0) return 0;
     if (own == 0) return min(grid, pre);
+    constexpr uint32_t kCost = D == 256 ? 4 : D == 128 ? 7 : 9;   // of a step, in own tiles
     // (integers: two kernels have to come to the same number)
-    const unsigned long long w = 4ull * pre, all = w + own;
+    const unsigned long long w = static_cast<unsigned long long>(kCost) * pre, all = w + own;
     const uint32_t n = static_cast<uint32_t>((w * grid + all / 2) / all);
     return min(min(max(n, 1u), grid - 1), pre);
 }
@@ -824,47 +834,104 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
     if constexpr (kDiff) {
         if (warp == 0) lambda = diff_lambda<D / 2>(a.out.diff, head, lane);
     }
-    // Launched as a programmatic dependent of the decode grid.  With few sequences the tiles before
-    // this one's are summed up from the lengths while that runs; else the grid's prefix table is read.
+    // Launched as a programmatic dependent of the decode grid.  With few sequences (and groups) the tiles before
+    // this one's are summed up from the lengths while that runs; else the grid's prefix tables are read.
     uint32_t T = 0, before = 0, U = 0;
-    const bool early = !kShared && a.B <= kEarlySeqs;
+    const bool early = a.B <= kEarlySeqs && (!kShared || a.pre.groups <= kEarlySeqs);
+    uint32_t grid = a.grid, pre_c0 = 0, n_pre = 0;   // kShared: CTAs of the own tokens; the prefix's records
+    long long pre_row = 0;
+    // kShared: what the prefix of length p of group g (whose steps begin at `work`) leaves of the row's unit
+    auto place_prefix = [&](int p, int first, int next, uint32_t work, uint32_t Up, uint32_t P) {
+        const int grows = (next - first) * grp * a.nq;
+        const int gr = (b - first) * grp * a.nq + r;   // the row among its KV head's of the group
+        const uint32_t n = (p + kPreTile - 1) / kPreTile, per_tile = steps_of_rows(grows);
+        // the unit's first step, and its steps a tile
+        const uint32_t before_unit = gr / Unit<D>::kRows * (Unit<D>::kRows / kStepRows);
+        const uint32_t u0 = work + (hk * per_tile + before_unit) * n;
+        const uint32_t steps = min(per_tile - before_unit, static_cast<uint32_t>(Unit<D>::kRows / kStepRows)) * n;
+        pre_c0 = warp_of(u0, P, Up);
+        n_pre = warp_of(u0 + steps - 1, P, Up) - pre_c0 + 1;
+        pre_row = static_cast<long long>(first) * a.Hq * a.nq + static_cast<long long>(hk) * grows + gr;
+    };
     if (early) {
-        uint32_t mine = 0, total = 0;
+        int len[kEarlySeqs / 32];   // tokens of sequences lane, lane + 32; -1: rejected
+        int prefix = 0, first = 0, next = 0;   // kShared: of the row's group
+        uint32_t work = 0, Up = 0;
+        bool good = true;
 #pragma unroll
-        for (int e = 0; e < kEarlySeqs; e += 32) {
-            const uint32_t n = e + lane < a.B ? seq_tiles(a.kv_lens[e + lane], a.max_kv) : 0u;
+        for (int e = 0; e < kEarlySeqs / 32; ++e) {
+            const int x = 32 * e + lane;
+            len[e] = x < a.B ? a.kv_lens[x] : 0;
+        }
+        if constexpr (kShared) {
+            int own[kEarlySeqs / 32];
+#pragma unroll
+            for (int e = 0; e < kEarlySeqs / 32; ++e) own[e] = -1;
+            for (int g0 = 0; g0 < a.pre.groups; g0 += 32) {
+                // a group a lane, then each to all lanes
+                const int g = g0 + lane;
+                int s0 = 0, s1 = 0, p = 0;
+                if (g < a.pre.groups) {
+                    s0 = a.pre.starts[g];
+                    s1 = a.pre.starts[g + 1];
+                    p = a.pre.lens[g];
+                    good = good && s0 >= 0 && s0 <= s1 && s1 <= a.B && (g > 0 || s0 == 0) &&
+                           (g + 1 < a.pre.groups || s1 == a.B);
+                    if (p < 0 || p > a.pre.max_prefix || p % a.pre.ps != 0) p = -1;
+                }
+                const uint32_t steps =
+                    p > 0 ? a.Hkv * steps_of_rows((s1 - s0) * grp * a.nq) * ((p + kPreTile - 1) / kPreTile) : 0u;
+                for (int i = 0; i < min(32, a.pre.groups - g0); ++i) {
+                    const int f = __shfl_sync(0xffffffffu, s0, i), t = __shfl_sync(0xffffffffu, s1, i);
+                    const int q = __shfl_sync(0xffffffffu, p, i);
+#pragma unroll
+                    for (int e = 0; e < kEarlySeqs / 32; ++e) {
+                        const int x = 32 * e + lane;
+                        if (x >= f && x < t) own[e] = q < 0 || len[e] < q || len[e] - q > a.max_kv ? -1 : len[e] - q;
+                    }
+                    if (b >= f && b < t) prefix = q, first = f, next = t, work = Up;
+                    Up += __shfl_sync(0xffffffffu, steps, i);
+                }
+            }
+            good = __all_sync(0xffffffffu, good);
+#pragma unroll
+            for (int e = 0; e < kEarlySeqs / 32; ++e) len[e] = good ? own[e] : -1;
+            if (!good) Up = 0;
+        }
+        uint32_t mine = 0, total = 0;
+        bool row_good = true;
+#pragma unroll
+        for (int e = 0; e < kEarlySeqs / 32; ++e) {
+            const int x = 32 * e + lane;
+            const uint32_t n = x < a.B ? seq_tiles(len[e], a.max_kv) : 0u;
             total += n;
-            mine += e + lane < b ? n : 0u;
-            if (e + lane == b) T = n;
+            mine += x < b ? n : 0u;
+            if (x == b) T = n, row_good = len[e] >= 0;
         }
         T = __reduce_add_sync(0xffffffffu, T);
         before = __reduce_add_sync(0xffffffffu, mine) * per_seq;
         U = __reduce_add_sync(0xffffffffu, total) * per_seq;
+        if constexpr (kShared) {
+            row_good = __all_sync(0xffffffffu, row_good);
+            const uint32_t P = prefix_ctas<D>(a.grid, Up, U);
+            grid -= P;
+            if (row_good && prefix > 0) place_prefix(prefix, first, next, work, Up, P);
+        }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    uint32_t grid = a.grid, pre_c0 = 0, n_pre = 0;
-    long long pre_row = 0;
-    if constexpr (kShared) {
+    if (kShared && !early) {
         const int2 seq = a.pre.seq[b];
-        const uint32_t Up = a.pre.tiles[a.pre.groups], own = *a.pre.total;
-        const uint32_t P = prefix_ctas(a.grid, Up, own);
+        const uint32_t Up = a.pre.work[a.pre.groups], own = *a.pre.total;
+        const uint32_t P = prefix_ctas<D>(a.grid, Up, own);
         grid -= P;
         if (seq.x >= 0 && own > 0) {
             before = a.prefix[b];
             T = (a.prefix[b + 1] - before) / per_seq;
             U = a.prefix[a.B];
         }
-        if (seq.x > 0) {
-            const int first = a.pre.starts[seq.y], grows = (a.pre.starts[seq.y + 1] - first) * grp * a.nq;
-            const int gr = (b - first) * grp * a.nq + r;   // the row among its KV head's of the group
-            const uint32_t n = (seq.x + kPreTile - 1) / kPreTile;
-            const uint32_t u0 = a.pre.tiles[seq.y] +
-                                (hk * ((grows + kUnitRows - 1) / kUnitRows) + gr / kUnitRows) * n;
-            pre_c0 = warp_of(u0, P, Up);
-            n_pre = warp_of(u0 + n - 1, P, Up) - pre_c0 + 1;
-            pre_row = static_cast<long long>(first) * a.Hq * a.nq + static_cast<long long>(hk) * grows + gr;
-        }
+        if (seq.x > 0)
+            place_prefix(seq.x, a.pre.starts[seq.y], a.pre.starts[seq.y + 1], a.pre.work[seq.y], Up, P);
     } else if (!early) {
         before = a.prefix[b];
         T = (a.prefix[b + 1] - before) / per_seq;
@@ -903,7 +970,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
                 const float* part_o = a.part_o;
                 const float2* part_ml = a.part_ml;
                 if (kShared && x >= n_rec) {
-                    rec = static_cast<long long>(pre_c0 + x - n_rec) * kUnitRows + pre_row;
+                    rec = static_cast<long long>(pre_c0 + x - n_rec) * Unit<D>::kRows + pre_row;
                     part_o = a.pre.part_o;
                     part_ml = a.pre.part_ml;
                 }

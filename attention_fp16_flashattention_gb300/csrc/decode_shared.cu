@@ -14,17 +14,20 @@
 // of them share the prefixes' tiles evenly, the others the own tokens' (decode_f16_body), each a contiguous
 // range of tiles laid end to end.  A merge kernel joins the records of both.
 //
-// The prefix CTAs.  A unit is 128 query rows of one KV head and group; its prefix goes by in tiles of 64
-// tokens.  Warp roles:
+// The prefix CTAs.  A unit is 256 query rows of one KV head and group (128 at D = 256); its prefix goes by in
+// tiles of 64 tokens, and a step is 128 rows against a tile.  Warp roles:
 //   warp 0     TMA producer: K_0, V_0, K_1, V_1, ... through a ring, the pages looked up 32 boxes at a time.
-//   warp 1     allocates tensor memory and issues S = Q K^T (tcgen05, 128 x 64 x D) into one of two S buffers.
+//   warp 1     allocates tensor memory and issues S = Q K^T (tcgen05, 128 x 64 x D); a buffer is handed back as soon as
+//              the softmax has it in registers.
 //   last warp  issues O += hi V + lo V (P from tensor memory).
-//   the others softmax: one thread per query row (TMEM lane).  D <= 128: two sets of four warps take the tiles in
-//              turn, each with its own running max, sum and O (joined at the unit's end), so that a tile's
-//              exponentials run beside the next one's.  D = 256: O fills half of the tensor memory and
-//              there is one set; a tile's bytes take as long as its softmax.
-// P = hi + lo in FP16 as everywhere in the decode (decode_f16.cu).  Tensor memory: S 2 x 64 columns, P 2 x (32 hi +
-// 32 lo), O 64, 128 per set, 256.
+//   the others softmax: one thread per query row (TMEM lane).  D <= 128: two sets of four warps take the steps in
+//              turn, each with its own running max, sum and O, so that a step's exponentials run beside the
+//              next one's.  With more than 128 rows the sets are the unit's two halves and share every
+//              tile; with fewer they take its tiles in turn and are joined at its end.  D = 256: O fills half of the
+//              tensor memory and there is one set; a tile's bytes take as long as its softmax.
+// P = hi + lo in FP16 as everywhere in the decode (decode_f16.cu).  Tensor memory: S and P (hi, lo) of 64 columns
+// a buffer, one for each set, O of D columns a set, and at D = 256 Q in its 128, so that the 64 KB that it would
+// take of the shared memory hold another tile under way.
 //
 // Every wait is bounded in time (WaitCtl): one that runs out records GBATTN_DEV_WAIT_TIMEOUT, the CTA stops,
 // waits a bounded time for its copies and MMAs in flight, frees tensor memory and exits.
@@ -36,25 +39,31 @@ namespace gbattn {
 namespace {
 
 constexpr uint64_t kDrainNs = 200000000ull;   // 0.2 s for draining after an abort
-constexpr uint32_t kTS = 64, kTP = 128, kTPMap = 64, kTPLo = 32, kTO = 256;   // tensor memory columns
+// Tensor memory columns: S (64 a buffer), P (32 of hi, 32 of lo a buffer), Q where it is kept there, O.
+constexpr uint32_t kTBuf = 64, kTPLo = 32, kTO = 256;
 
 template <int D>
 struct Pre {
     static constexpr int kSets = D == 256 ? 1 : 2;
+    static constexpr int kBufs = kSets;                            // S and P buffers
+    static constexpr bool kQTmem = D == 256;                       // Q in tensor memory
+    static constexpr uint32_t kTP = kBufs * kTBuf, kTQ = 2 * kTP;
     static constexpr int kThreads = 32 * (3 + 4 * kSets);
     static constexpr int kPvWarp = 2 + 4 * kSets;
     static constexpr int kChunks = D / 64;                         // 64-column chunks of a row
-    static constexpr int kQBytes = kUnitRows * D * 2;
+    static constexpr int kQTile = kStepRows * D * 2;
+    static constexpr int kQBytes = kQTmem ? 0 : kSets * kQTile;
     static constexpr int kSlot = kPreTile * D * 2;                 // a K or V tile
-    static constexpr int kNS = D == 256 ? 4 : D == 128 ? 8 : 16;   // ring slots (even: K, odd: V)
-    static constexpr int kQChunk = kUnitRows * 128, kKvChunk = kPreTile * 128;
-    static constexpr uint32_t kIdescQK = idesc_f16(kUnitRows, kPreTile, false, false);
-    static constexpr uint32_t kIdescPV = idesc_f16(kUnitRows, D, false, true);
+    static constexpr int kNS = D == 256 ? 6 : D == 128 ? 8 : 20;   // ring slots (even: K, odd: V)
+    static constexpr int kQChunk = kStepRows * 128, kKvChunk = kPreTile * 128;
+    static constexpr uint32_t kIdescQK = idesc_f16(kStepRows, kPreTile, false, false);
+    static constexpr uint32_t kIdescPV = idesc_f16(kStepRows, D, false, true);
 };
 
+constexpr int kMaxSlots = 20;
 struct Ctrl {
     uint64_t q_full;
-    uint64_t full[16], empty[16];
+    uint64_t full[kMaxSlots], empty[kMaxSlots];
     uint64_t s_full[2];    // S buffer computed
     uint64_t s_free[2];    // and read into registers
     uint64_t p_full[2];    // P buffer written
@@ -66,18 +75,19 @@ struct Ctrl {
     int abort;
 };
 struct Exchange {   // the two sets' (reference, sum) of a row
-    float m[2][kUnitRows], l[2][kUnitRows];
+    float m[2][kStepRows], l[2][kStepRows];
 };
 
 // Shared memory: the role's own part, then two tables: the tile prefix over groups or, in a CTA of the own
-// tokens, over sequences; and every sequence's prefix length.
+// tokens, over sequences; and every sequence's prefix length, which a prefix CTA has no use for and puts the
+// sets' exchange there.
 constexpr int kTable = 4 * (kMaxSeqs + 4);
 constexpr int kCtrlBytes = (static_cast<int>(sizeof(Ctrl)) + 15) / 16 * 16;
 template <int D>
 struct Smem {
     static constexpr int kOwn = Cfg<D>::kRing + Cfg<D>::kBarBytes;
-    static constexpr int kPre = Pre<D>::kQBytes + Pre<D>::kNS * Pre<D>::kSlot + kCtrlBytes +
-                                (Pre<D>::kSets == 2 ? static_cast<int>(sizeof(Exchange)) : 0);
+    static constexpr int kPre = Pre<D>::kQBytes + Pre<D>::kNS * Pre<D>::kSlot + kCtrlBytes;
+    static_assert(Pre<D>::kNS <= kMaxSlots && Pre<D>::kNS % 2 == 0 && sizeof(Exchange) <= kTable, "prefix role");
     static constexpr int kRole = ((kOwn > kPre ? kOwn : kPre) + 15) / 16 * 16;
     static constexpr int kBytes = kRole + 2 * kTable + 1024;
     static_assert(kBytes <= 232448 - 1200, "shared memory of a CTA, beside its static variables");
@@ -88,7 +98,7 @@ struct SharedArgs {
     const int32_t *starts, *prefix_lens;   // [groups + 1], [groups]
     float* pre_o;                          // PrefixRecords
     float2* pre_ml;
-    uint32_t* tiles_out;
+    uint32_t* work_out;
     int2* seq_out;
     uint32_t* total_out;
     int groups, max_prefix, max_own, box_rows, box_bits;
@@ -132,42 +142,50 @@ __device__ __forceinline__ void store_f32x8(float* p, const uint32_t* v) {
                  : "memory");
 }
 
-// A part of a unit: n tiles from tile0 of group g's prefix for rows row0 .. of KV head hk.
+// A part of a unit: steps [s0, s1) of it, for rows row0 .. of KV head hk of group g.
 struct Part {
-    int g, hk, row0, rows;   // rows: of the group and KV head, in all
-    int first, prefix;       // the group's first sequence, its prefix's tokens
-    int tile0, n;
+    int hk, row0, rows;   // rows: of the group and KV head, in all
+    int first, prefix;    // the group's first sequence, its prefix's tokens
+    int pair;             // 1: two steps a tile
+    int s0, s1;
+    __device__ __forceinline__ int tile_of(int step) const { return step >> pair; }
+    __device__ __forceinline__ int tile0() const { return s0 >> pair; }
+    __device__ __forceinline__ int tiles() const { return ((s1 - 1) >> pair) - (s0 >> pair) + 1; }
 };
-// The part that begins with tile `pos` of a range that ends before `end`.
-__device__ __forceinline__ Part part_at(const SharedArgs& a, const uint32_t* tiles, uint32_t pos, uint32_t end) {
-    int lo = 0, hi = a.groups - 1;   // the last group whose tiles begin at or before pos
+// The part that begins with step `pos` of a range that ends before `end`; pos moves behind it.
+template <int D>
+__device__ __forceinline__ Part next_part(const SharedArgs& a, const uint32_t* work, uint32_t& pos, uint32_t end) {
+    int lo = 0, hi = a.groups - 1;   // the last group whose steps begin at or before pos
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
-        if (tiles[mid] <= pos) lo = mid; else hi = mid - 1;
+        if (work[mid] <= pos) lo = mid; else hi = mid - 1;
     }
+    constexpr uint32_t kPer = Unit<D>::kRows / kStepRows;   // steps a tile of a full unit
     Part p;
-    p.g = lo;
     p.first = a.starts[lo];
     p.prefix = a.prefix_lens[lo];
     p.rows = (a.starts[lo + 1] - p.first) * a.dec.G;
-    const uint32_t T = (p.prefix + kPreTile - 1) / kPreTile, per_head = (p.rows + kUnitRows - 1) / kUnitRows;
-    const uint32_t off = pos - tiles[lo], unit = off / T;
-    p.hk = static_cast<int>(unit / per_head);
-    p.row0 = static_cast<int>(unit - p.hk * per_head) * kUnitRows;
-    p.tile0 = static_cast<int>(off - unit * T);
-    p.n = static_cast<int>(min(T - p.tile0, end - pos));
+    const uint32_t T = (p.prefix + kPreTile - 1) / kPreTile, per_tile = steps_of_rows(p.rows);
+    const uint32_t off = pos - work[lo];
+    p.hk = static_cast<int>(off / (per_tile * T));
+    const uint32_t in_head = off - p.hk * (per_tile * T), unit = in_head / (kPer * T);
+    const uint32_t per = min(per_tile - unit * kPer, kPer);
+    p.pair = per == 2;
+    p.row0 = static_cast<int>(unit * Unit<D>::kRows);
+    p.s0 = static_cast<int>(in_head - unit * kPer * T);
+    p.s1 = static_cast<int>(min(per * T, p.s0 + (end - pos)));
+    pos += p.s1 - p.s0;
     return p;
 }
 
 template <int D>
 __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,
-                                            uint8_t* smem, const uint32_t* tiles, uint32_t cta,
-                                            uint32_t n_ctas) {
+                                            uint8_t* smem, const uint32_t* work, Exchange* ex,
+                                            uint32_t cta, uint32_t n_ctas) {
     using C = Pre<D>;
     uint8_t* sQ = smem;
     uint8_t* sKV = smem + C::kQBytes;
     Ctrl* ctrl = reinterpret_cast<Ctrl*>(sKV + C::kNS * C::kSlot);
-    Exchange* ex = reinterpret_cast<Exchange*>(reinterpret_cast<uint8_t*>(ctrl) + kCtrlBytes);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const DecodeF16Args& d = a.dec;
     if (threadIdx.x == 0) {
@@ -198,25 +216,26 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
     tc_fence_after();
     const uint32_t tmem = ctrl->tmem_base;
     const WaitCtl w{d.wait_limit, d.status, &ctrl->abort};
-    const uint32_t Up = tiles[a.groups];
-    const uint32_t beg = warp_start(cta, n_ctas, Up), end = warp_start(cta + 1, n_ctas, Up);
-    // Counts over all parts: tiles (tc; its parity is the S and P buffer and, with two, the set), parts (ic),
-    // ring places (pos).
-    uint32_t tc = 0, ic = 0, ring = 0;
+    const uint32_t Up = work[a.groups];
+    const uint32_t end = warp_start(cta + 1, n_ctas, Up);
+    uint32_t pos = warp_start(cta, n_ctas, Up);
+    // Counts over all parts: steps (sc; its parity is the S and P buffer and, with two, the set), tiles (tc), parts
+    // (ic), ring places.
+    uint32_t sc = 0, tc = 0, ic = 0, ring = 0;
 
     if (warp == 0) {
         // ================= TMA producer
         const int bpt = kPreTile >> a.box_bits;   // boxes of a tile, at most 4
         bool ok = d.fault != 1;                   // test hook
-        for (uint32_t pos = beg; ok && pos < end;) {
-            const Part p = part_at(a, tiles, pos, end);
-            pos += p.n;
+        while (ok && pos < end) {
+            const Part p = next_part<D>(a, work, pos, end);
+            const int tile0 = p.tile0(), n_tiles = p.tiles();
             const int32_t* row = d.table + static_cast<long long>(p.first) * d.max_pages;
             const int boxes = (p.prefix + a.box_rows - 1) >> a.box_bits;
             // the cache row of box 32 c + lane
             auto look_up = [&](int c) -> int {
                 const int box = 32 * c + lane;
-                if (box >= boxes || box >= (p.tile0 + p.n) * bpt || 32 * c + 31 < p.tile0 * bpt) return 0;
+                if (box >= boxes || box >= (tile0 + n_tiles) * bpt || 32 * c + 31 < tile0 * bpt) return 0;
                 const int tok = box << a.box_bits;
                 int page = row[tok / d.ps];
                 if (page < 0 || page >= d.num_phys) {
@@ -225,8 +244,8 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
                 }
                 return page * d.ps + tok % d.ps;
             };
-            int c = p.tile0 * bpt >> 5, cur = look_up(c), next = look_up(c + 1);
-            for (int x = 0; x < 2 * p.n; ++x, ++ring) {
+            int c = tile0 * bpt >> 5, cur = look_up(c), next = look_up(c + 1);
+            for (int x = 0; x < 2 * n_tiles; ++x, ++ring) {
                 if (d.fault == 2 && ring >= 2 * C::kNS) {   // test hook: stop mid-stream, drain, leave
                     ok = false;
                     break;
@@ -234,7 +253,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
                 const int slot = ring % C::kNS;
                 ok = wait_warp(&ctrl->empty[slot], ((ring / C::kNS) & 1) ^ 1u, w);
                 if (!ok) break;
-                const int box0 = (p.tile0 + (x >> 1)) * bpt;
+                const int box0 = (tile0 + (x >> 1)) * bpt;
                 if (box0 >> 5 != c) {
                     ++c;
                     cur = next;
@@ -263,72 +282,82 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
     } else if (warp == 1) {
         // ================= QK issuer: K of tile tc sits at ring place 2 tc
         bool ok = true;
-        const uint32_t qa = smem_addr(sQ);
-        for (uint32_t pos = beg; ok && pos < end; ++ic) {
-            const int n = part_at(a, tiles, pos, end).n;
-            pos += n;
+        for (; ok && pos < end; ++ic) {
+            const Part p = next_part<D>(a, work, pos, end);
             ok = wait_warp(&ctrl->q_full, ic & 1, w);
-            for (int t = 0; ok && t < n; ++t, ++tc) {
-                const int slot = (2 * tc) % C::kNS, buf = tc & 1;
-                const uint32_t ka = smem_addr(sKV + slot * C::kSlot);
-                ok = wait_warp(&ctrl->full[slot], (2 * tc / C::kNS) & 1, w);
-                if (tc >= 2) ok = ok && wait_warp(&ctrl->s_free[buf], ((tc >> 1) - 1) & 1, w);
+            if constexpr (C::kQTmem) tc_fence_after();
+            for (int s = p.s0; ok && s < p.s1; ++s, ++sc) {
+                const int slot = (2 * tc) % C::kNS, buf = sc % C::kBufs;
+                if (s == p.s0 || !p.pair || !(s & 1)) ok = wait_warp(&ctrl->full[slot], (2 * tc / C::kNS) & 1, w);
+                if (sc >= C::kBufs) ok = ok && wait_warp(&ctrl->s_free[buf], (sc / C::kBufs - 1) & 1, w);
                 if (!ok) break;
+                const bool last = s + 1 == p.s1 || !p.pair || (s & 1);   // of the tile, here
+                const uint32_t qa = smem_addr(sQ + (p.pair ? buf : 0) * C::kQTile);
+                const uint32_t ka = smem_addr(sKV + slot * C::kSlot);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
-                    for (int k16 = 0; k16 < D / 16; ++k16)
-                        mma_ss(tmem + buf * kTS,
-                               sdesc_sw128(qa + (k16 >> 2) * C::kQChunk + (k16 & 3) * 32, 16, 1024),
-                               sdesc_sw128(ka + (k16 >> 2) * C::kKvChunk + (k16 & 3) * 32, 16, 1024),
-                               C::kIdescQK, k16 > 0 ? 1u : 0u);
+                    for (int k16 = 0; k16 < D / 16; ++k16) {
+                        const uint64_t kd = sdesc_sw128(ka + (k16 >> 2) * C::kKvChunk + (k16 & 3) * 32, 16, 1024);
+                        if constexpr (C::kQTmem)
+                            mma_ts(tmem + buf * kTBuf, tmem + C::kTQ + k16 * 8, kd, C::kIdescQK, k16 > 0 ? 1u : 0u);
+                        else
+                            mma_ss(tmem + buf * kTBuf,
+                                   sdesc_sw128(qa + (k16 >> 2) * C::kQChunk + (k16 & 3) * 32, 16, 1024), kd,
+                                   C::kIdescQK, k16 > 0 ? 1u : 0u);
+                    }
                     mma_commit(&ctrl->s_full[buf]);
-                    mma_commit(&ctrl->empty[slot]);
+                    if (last) mma_commit(&ctrl->empty[slot]);
                 }
                 __syncwarp();
+                tc += last;
             }
         }
     } else if (warp == C::kPvWarp) {
         // ================= PV issuer: V of tile tc sits at ring place 2 tc + 1.  A part's first PV into an O
         // overwrites it, so the softmax must have read the last part's.
         bool ok = true;
-        for (uint32_t pos = beg; ok && pos < end; ++ic) {
-            const Part p = part_at(a, tiles, pos, end);
-            pos += p.n;
+        for (; ok && pos < end; ++ic) {
+            const Part p = next_part<D>(a, work, pos, end);
             if (ic > 0) ok = wait_warp(&ctrl->o_free, (ic - 1) & 1, w);
-            for (int t = 0; ok && t < p.n; ++t, ++tc) {
-                const int slot = (2 * tc + 1) % C::kNS, buf = tc & 1;
+            for (int s = p.s0; ok && s < p.s1; ++s, ++sc) {
+                const int slot = (2 * tc + 1) % C::kNS, buf = sc % C::kBufs;
                 const uint32_t va = smem_addr(sKV + slot * C::kSlot);
-                ok = wait_warp(&ctrl->full[slot], ((2 * tc + 1) / C::kNS) & 1, w);
-                if (!ok) break;
-                const int live = p.prefix - (p.tile0 + t) * kPreTile;
-                if (live < kPreTile) {
-                    // Rows past the prefix were not loaded and may hold anything; P = 0 times a NaN is one.
-                    uint4* v16 = reinterpret_cast<uint4*>(sKV + slot * C::kSlot);
-                    for (int x = live * 8 + lane; x < kPreTile * 8; x += 32) {
+                if (s == p.s0 || !p.pair || !(s & 1)) {
+                    ok = wait_warp(&ctrl->full[slot], ((2 * tc + 1) / C::kNS) & 1, w);
+                    if (!ok) break;
+                    const int live = p.prefix - p.tile_of(s) * kPreTile;
+                    if (live < kPreTile) {
+                        // Rows past the prefix were not loaded and may hold anything; P = 0 times a NaN is one.
+                        uint4* v16 = reinterpret_cast<uint4*>(sKV + slot * C::kSlot);
+                        for (int x = live * 8 + lane; x < kPreTile * 8; x += 32) {
 #pragma unroll
-                        for (int ch = 0; ch < C::kChunks; ++ch)
-                            v16[ch * (C::kKvChunk / 16) + x] = make_uint4(0, 0, 0, 0);
+                            for (int ch = 0; ch < C::kChunks; ++ch)
+                                v16[ch * (C::kKvChunk / 16) + x] = make_uint4(0, 0, 0, 0);
+                        }
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
                 }
-                ok = wait_warp(&ctrl->p_full[buf], (tc >> 1) & 1, w);
+                ok = wait_warp(&ctrl->p_full[buf], (sc / C::kBufs) & 1, w);
                 if (!ok) break;
                 tc_fence_after();
+                const bool last = s + 1 == p.s1 || !p.pair || (s & 1);
                 const uint32_t o = tmem + kTO + (C::kSets == 2 ? buf * D : 0);
+                const bool begun = s - p.s0 >= C::kSets;   // this O holds a step of the part
                 if (elect_one()) {
 #pragma unroll
                     for (int half = 0; half < 2; ++half)
 #pragma unroll
                         for (int k16 = 0; k16 < kPreTile / 16; ++k16)
-                            mma_ts(o, tmem + kTP + buf * kTPMap + half * kTPLo + k16 * 8,
+                            mma_ts(o, tmem + C::kTP + buf * kTBuf + half * kTPLo + k16 * 8,
                                    sdesc_sw128(va + k16 * 2048, C::kKvChunk, 1024), C::kIdescPV,
-                                   (t >= C::kSets || half > 0 || k16 > 0) ? 1u : 0u);
-                    mma_commit(&ctrl->empty[slot]);
+                                   (begun || half > 0 || k16 > 0) ? 1u : 0u);
+                    if (last) mma_commit(&ctrl->empty[slot]);
                     mma_commit(&ctrl->pv_done[buf]);
                 }
                 __syncwarp();
+                tc += last;
             }
         }
     } else {
@@ -336,47 +365,68 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
         const int set = C::kSets == 2 ? (warp - 2) >> 2 : 0;
         const int quarter = warp & 3, row = quarter * 32 + lane;
         const uint32_t tl = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+        uint32_t xc = 0;   // exchanges between the sets
         bool ok = true;
-        for (uint32_t pos = beg; ok && pos < end; ++ic) {
-            const Part p = part_at(a, tiles, pos, end);
-            pos += p.n;
-            const int gr = p.row0 + row;          // the row among its KV head's of the group
+        for (; ok && pos < end; ++ic) {
+            const Part p = next_part<D>(a, work, pos, end);
+            // The unit's half that the set's steps are of: the buffers' order runs on over the parts.
+            const int half = p.pair ? set ^ static_cast<int>((sc ^ p.s0) & 1) : 0;
+            const int gr = p.row0 + half * kStepRows + row;          // the row among its KV head's of the group
             const bool live = gr < p.rows;
-            const bool warp_live = p.row0 + quarter * 32 < p.rows;
-            // Q of the part: the row, or with two sets half of its columns.  The last part's products
-            // with the old one are done (its epilogue waited for them).
+            const bool warp_live = p.row0 + half * kStepRows + quarter * 32 < p.rows;
+            // Q of the part: the row, or where two sets work on the same rows half of its columns.  The last part's
+            // products with the old one are done (its epilogue waited for them).
             int lim = 0;   // the row sees prefix tokens t < lim
             {
                 const int member = gr / d.G, rem = gr - member * d.G, b = p.first + member;
                 const __half* q = d.q + ((static_cast<long long>(b) * d.Hkv + p.hk) * d.G + rem) * D;
-                constexpr int kCh = C::kChunks / C::kSets > 0 ? C::kChunks / C::kSets : 1;
-                const int ch0 = C::kChunks >= C::kSets ? set * kCh : 0;
-                if (C::kChunks >= C::kSets || set == 0) {
+                uint8_t* dst = sQ + (p.pair ? set : 0) * C::kQTile + row * 128;
+                int ch0 = 0, ch1 = C::kChunks;
+                if (C::kSets == 2 && !p.pair) {
+                    ch0 = set * ((C::kChunks + 1) / 2);
+                    ch1 = min(ch0 + (C::kChunks + 1) / 2, C::kChunks);
+                }
+                if constexpr (C::kQTmem) {
+#pragma unroll 2
+                    for (int ch = 0; ch < C::kChunks; ++ch) {
+                        uint32_t v[32];
 #pragma unroll
-                    for (int ch = ch0; ch < ch0 + kCh; ++ch) {
+                        for (int e = 0; e < 8; ++e) {
+                            const uint4 x = live ? reinterpret_cast<const uint4*>(q + ch * 64)[e] : make_uint4(0, 0, 0, 0);
+                            v[4 * e] = x.x;
+                            v[4 * e + 1] = x.y;
+                            v[4 * e + 2] = x.z;
+                            v[4 * e + 3] = x.w;
+                        }
+                        tmem_st32(tl + C::kTQ + ch * 32, v);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                } else {
+#pragma unroll 2
+                    for (int ch = ch0; ch < ch1; ++ch) {
                         uint4 v[8];
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
                             v[e] = live ? reinterpret_cast<const uint4*>(q + ch * 64)[e] : make_uint4(0, 0, 0, 0);
 #pragma unroll
                         for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<uint4*>(sQ + ch * C::kQChunk + row * 128 + ((e ^ (row & 7)) << 4)) = v[e];
+                            *reinterpret_cast<uint4*>(dst + ch * C::kQChunk + ((e ^ (row & 7)) << 4)) = v[e];
                     }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 if (live) {
                     const int own = d.kv_lens[b] - p.prefix;   // (outside [0, max_own]: the merge drops the row)
                     if (own >= 0 && own <= a.max_own) lim = min(p.prefix, p.prefix + own - d.nq + rem % d.nq + 1);
                 }
             }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             mbar_arrive(&ctrl->q_full);
-            lim -= p.tile0 * kPreTile;
             float m_run = -INFINITY, l = 0.0f;   // the exponentials' reference (tiles.cuh) and their sum
             bool first = true;
-            for (int t = 0; t < p.n; ++t, ++tc, lim -= kPreTile) {
-                const int buf = tc & 1;
+            for (int s = p.s0; s < p.s1; ++s, ++sc) {
+                const int buf = sc % C::kBufs;
                 if (C::kSets == 2 && buf != set) continue;
-                ok = wait_warp(&ctrl->s_full[buf], (tc >> 1) & 1, w);
+                ok = wait_warp(&ctrl->s_full[buf], (sc / C::kBufs) & 1, w);
                 if (!ok) break;
                 tc_fence_after();
                 float alpha = 1.0f;
@@ -385,14 +435,15 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
                 if (warp_live) {
                     uint32_t x[kPreTile];
 #pragma unroll
-                    for (int c = 0; c < kPreTile; c += 32) tmem_ld32(tl + buf * kTS + c, x + c);
+                    for (int c = 0; c < kPreTile; c += 32) tmem_ld32(tl + buf * kTBuf + c, x + c);
                     tmem_ld_wait();
                     tc_fence_before();
                     mbar_arrive(&ctrl->s_free[buf]);
-                    if (lim < kPreTile) {
+                    const int seen = lim - p.tile_of(s) * kPreTile;
+                    if (seen < kPreTile) {
 #pragma unroll
                         for (int c = 0; c < kPreTile; ++c)
-                            if (c >= lim) x[c] = __float_as_uint(-INFINITY);
+                            if (c >= seen) x[c] = __float_as_uint(-INFINITY);
                     }
                     float m4[4];
 #pragma unroll
@@ -440,21 +491,16 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
                     tc_fence_before();
                     mbar_arrive(&ctrl->s_free[buf]);
                 }
-                // the P buffer is free (and with two sets its O up to date)
-                if (tc >= 2) ok = wait_warp(&ctrl->pv_done[buf], ((tc >> 1) - 1) & 1, w);
+                // the P buffer is free and its O up to date
+                if (sc >= C::kBufs) ok = wait_warp(&ctrl->pv_done[buf], (sc / C::kBufs - 1) & 1, w);
                 if (!ok) break;
                 tc_fence_after();
                 if (warp_live) {
-                    const uint32_t pbuf = tl + kTP + buf * kTPMap;
+                    const uint32_t pbuf = tl + C::kTP + buf * kTBuf;
                     tmem_st32(pbuf, hi);
                     tmem_st32(pbuf + kTPLo, lo);
                     tmem_st_wait();
                     if (warp_need && !first) {   // rescale the row of O
-                        if (C::kSets == 1) {     // the last tile's PV goes into it too
-                            ok = wait_warp(&ctrl->pv_done[buf ^ 1], ((tc - 1) >> 1) & 1, w);
-                            if (!ok) break;
-                            tc_fence_after();
-                        }
                         const uint32_t obuf = tl + kTO + set * D;
                         const uint64_t a2 = f2_pack(alpha, alpha);
 #pragma unroll 1
@@ -482,25 +528,26 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
             }
             if (!ok) break;
             // ---- the part's record: unnormalised O, reference and sum
-            // (first the last tile but one: the other set's barrier has then left the phase before its
-            // last tile's, which a wait for that would otherwise take for it)
-            if (tc >= 2) ok = wait_warp(&ctrl->pv_done[tc & 1], ((tc - 2) >> 1) & 1, w);
-            ok = ok && wait_warp(&ctrl->pv_done[(tc - 1) & 1], ((tc - 1) >> 1) & 1, w);
+            // (first the last step but one: the other set's barrier has then left the phase before its
+            // last step's, which a wait for that would otherwise take for it)
+            if (C::kBufs == 2 && sc >= 2) ok = wait_warp(&ctrl->pv_done[sc & 1], ((sc - 2) >> 1) & 1, w);
+            ok = ok && wait_warp(&ctrl->pv_done[(sc - 1) % C::kBufs], ((sc - 1) / C::kBufs) & 1, w);
             if (!ok) break;
             tc_fence_after();
-            const long long rec = static_cast<long long>(cta) * kUnitRows +
+            const long long rec = static_cast<long long>(cta) * Unit<D>::kRows +
                                   static_cast<long long>(p.first) * d.Hq * d.nq +
                                   static_cast<long long>(p.hk) * p.rows + gr;
-            if constexpr (C::kSets == 2) {
+            if (C::kSets == 2 && !p.pair) {
                 ex->m[set][row] = m_run;
                 ex->l[set][row] = l;
                 mbar_arrive(&ctrl->xchg[quarter]);
-                ok = wait_warp(&ctrl->xchg[quarter], ic & 1, w);
+                ok = wait_warp(&ctrl->xchg[quarter], xc & 1, w);
+                ++xc;
                 if (!ok) break;
                 const float2 ml0 = make_float2(ex->m[0][row], ex->l[0][row]);
                 const float2 ml1 = make_float2(ex->m[1][row], ex->l[1][row]);
                 const float M = fmaxf(ml0.x, ml1.x);
-                const bool any0 = ml0.y != 0.0f, any1 = ml1.y != 0.0f;   // (a set without a tile has no O)
+                const bool any0 = ml0.y != 0.0f, any1 = ml1.y != 0.0f;   // (a set without a step has no O)
                 const float f0 = record_weight(ml0, M), f1 = record_weight(ml1, M);
                 constexpr int kCols = D / 2;   // a thread joins half of the columns
                 const uint32_t o_tm = tl + kTO + set * kCols;
@@ -527,7 +574,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o0[32];
-                    tmem_ld32(tl + kTO + c, o0);
+                    tmem_ld32(tl + kTO + set * D + c, o0);
                     tmem_ld_wait();
                     if (live) {
 #pragma unroll
@@ -535,7 +582,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
                     }
                     __syncwarp();
                 }
-                if (live) a.pre_ml[rec] = make_float2(m_run, l);
+                if (live) a.pre_ml[rec] = make_float2(m_run, l);   // (a sum of 0: the record holds no O)
             }
             tc_fence_before();
             mbar_arrive(&ctrl->o_free);
@@ -586,7 +633,8 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
         tma_prefetch_desc(&pk);
         tma_prefetch_desc(&pv);
     }
-    // ---- tiles of every group's prefix
+    const int my_len = d.B <= kThreads && tid < d.B ? d.kv_lens[tid] : 0;   // under way beside the groups
+    // ---- steps over every group's prefix
     const int per_g = (a.groups + kThreads - 1) / kThreads;
     const int g0 = min(tid * per_g, a.groups), g1 = min(g0 + per_g, a.groups);
     bool order = true;
@@ -599,8 +647,7 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
         if (!good && in_order && lead) atomicOr(d.status, kDevBadLength);
         uint32_t n = 0;
         if (in_order && good)
-            n = static_cast<uint32_t>(d.Hkv) * (((e - s) * d.G + kUnitRows - 1) / kUnitRows) *
-                ((p + kPreTile - 1) / kPreTile);
+            n = static_cast<uint32_t>(d.Hkv) * steps_of_rows((e - s) * d.G) * ((p + kPreTile - 1) / kPreTile);
         tiles[g] = n;
         sum += n;
     }
@@ -610,13 +657,13 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
     for (int g = g0; g < g1; ++g) {
         const uint32_t n = order ? tiles[g] : 0;
         tiles[g] = run;
-        if (lead) a.tiles_out[g] = run;
+        if (lead) a.work_out[g] = run;
         run += n;
     }
     if (tid == 0) {
         tiles[a.groups] = Up;
         if (lead) {
-            a.tiles_out[a.groups] = Up;
+            a.work_out[a.groups] = Up;
             if (!order) atomicOr(d.status, kDevBadIndex);
         }
     }
@@ -637,7 +684,7 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
             if (p < 0 || p > a.max_prefix || p % d.ps != 0) {
                 p = -1;
             } else {
-                const int n = d.kv_lens[b];
+                const int n = d.B <= kThreads ? my_len : d.kv_lens[b];
                 if (n < p || n - p > a.max_own) {
                     p = -1;
                     if (lead) atomicOr(d.status, kDevBadLength);
@@ -654,9 +701,9 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
     if (lead && tid == 0) *a.total_out = own;
     // The merge grid may start launching now; it waits for this grid to finish.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t P = prefix_ctas(gridDim.x, Up, own);
+    const uint32_t P = prefix_ctas<D>(gridDim.x, Up, own);
     if (blockIdx.x < P) {
-        prefix_body<D>(pk, pv, a, smem, tiles, blockIdx.x, P);
+        prefix_body<D>(pk, pv, a, smem, tiles, reinterpret_cast<Exchange*>(pre), blockIdx.x, P);
         return;
     }
     if (own == 0) return;
@@ -675,23 +722,24 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
     decode_f16_body<D, NB, false, true>(tk, tv, d, smem, tiles, pre, blockIdx.x - P, gridDim.x - P);
 }
 
-// Workspace: the own tokens' records and tile prefix (decode_layout), then the prefixes' records, 128 rows a
-// CTA and one for every row of the call, their tile prefix, the sequences' prefixes and the total.
+// Workspace: the own tokens' records and tile prefix (decode_layout), then the prefixes' records, a unit's rows a
+// CTA and one for every row of the call, the groups' steps, the sequences' prefixes and the total.
 struct SharedLayout {
     Layout dec;
-    size_t o, ml, tiles, seq, total_at, total;
+    size_t o, ml, work, seq, total_at, total;
 };
 SharedLayout shared_layout(long long ctas, int B, int Hkv, int G, int groups, int max_own, int D) {
     SharedLayout l{};
     l.dec = decode_layout(ctas, B, Hkv, G, max_own, D, false);
-    const size_t rows = static_cast<size_t>(ctas) * kUnitRows + static_cast<size_t>(B) * Hkv * G;
+    const size_t rows = static_cast<size_t>(ctas) * (D == 256 ? Unit<256>::kRows : Unit<128>::kRows) +
+                        static_cast<size_t>(B) * Hkv * G;
     size_t at = round16(l.dec.total);
     at = (at + 31) & ~static_cast<size_t>(31);
     l.o = at;
     at += rows * D * 4;
     l.ml = at;
     at += round16(rows * 8);
-    l.tiles = at;
+    l.work = at;
     at += round16((static_cast<size_t>(groups) + 1) * 4);
     l.seq = at;
     at += round16(static_cast<size_t>(B) * 8);
@@ -764,8 +812,8 @@ extern "C" int attn_paged_decode_shared_f16_fwd(const void* q, const void* k_pag
     const int R = plan.R;
     const long long streams = static_cast<long long>(B) * Hkv * plan.sets * plan.side;
     const long long own_tiles = (max_own_len + kTile - 1LL) / kTile;
-    // units of all groups, each at most one unit short of a whole number of them per KV head
-    const long long units = (static_cast<long long>(B) * G / kUnitRows + groups) * Hkv;
+    // steps a tile of all groups, each at most one short of a whole number of them per KV head
+    const long long units = (static_cast<long long>(B) * G / kStepRows + groups) * Hkv;
     const long long pre_tiles = (max_prefix_len + kPreTile - 1LL) / kPreTile;
     if (streams > 0x7FFFFFFFLL || streams * own_tiles > 0x7FFFFFFFLL || units > 0x7FFFFFFFLL ||
         units * pre_tiles > 0x7FFFFFFFLL)
@@ -840,7 +888,7 @@ extern "C" int attn_paged_decode_shared_f16_fwd(const void* q, const void* k_pag
     a.prefix_lens = prefix_lens;
     a.pre_o = reinterpret_cast<float*>(wsp + lay.o);
     a.pre_ml = reinterpret_cast<float2*>(wsp + lay.ml);
-    a.tiles_out = reinterpret_cast<uint32_t*>(wsp + lay.tiles);
+    a.work_out = reinterpret_cast<uint32_t*>(wsp + lay.work);
     a.seq_out = reinterpret_cast<int2*>(wsp + lay.seq);
     a.total_out = reinterpret_cast<uint32_t*>(wsp + lay.total_at);
     a.groups = groups;
@@ -872,7 +920,8 @@ extern "C" int attn_paged_decode_shared_f16_fwd(const void* q, const void* k_pag
     m.grid = static_cast<uint32_t>(ctas);
     m.parts = static_cast<uint32_t>(warps_of(D) / plan.side);
     m.out = d.out;
-    m.pre = PrefixRecords{a.pre_o, a.pre_ml, a.tiles_out, a.seq_out, a.total_out, group_starts, groups};
+    m.pre = PrefixRecords{a.pre_o, a.pre_ml, a.work_out, a.seq_out, a.total_out, group_starts, prefix_lens,
+                          groups, max_prefix_len, page_size};
     // Warps per row by the records of an average row, of either kind.
     const long long recs = ctas * plan.side / streams + ctas / (units < 1 ? 1 : units) + 2;
     const int mw = recs > 32 ? 8 : recs > 8 ? 4 : 1;

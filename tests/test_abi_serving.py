@@ -195,9 +195,9 @@ def test_shared_decode_workspace_sizes(lib):
     for bad in ((0, 4, 2, 1, 1, 64, 64, 128), (2, 5, 2, 1, 1, 64, 64, 128), (2, 4, 2, 1, 0, 64, 64, 128),
                 (2, 4, 2, 1, 1, -1, 64, 128), (2, 4, 2, 1, 1, 64, -1, 128)):
         assert size(*bad) == 0
-    # beside the ordinary decode's, a record of every row and 128 rows a CTA, and the tables
+    # beside the ordinary decode's, a record of every row and 256 rows a CTA, and the tables
     plain = lib.attn_paged_decode_f16_workspace_size(64, 32, 8, 1, 2048, 128, 0)
-    rows = 152 * 128 + 64 * 32
+    rows = 152 * 256 + 64 * 32
     extra = size(64, 32, 8, 1, 3, 1 << 20, 2048, 128) - plain
     assert rows * (128 * 4 + 8) <= extra <= rows * (128 * 4 + 8) + 64 * 8 + 200
 
