@@ -778,16 +778,23 @@ __device__ __forceinline__ uint32_t steps_of_rows(int rows) {
     return static_cast<uint32_t>((rows + kStepRows - 1) / kStepRows);
 }
 
-// How many of `grid` CTAs work on the prefixes' `pre` steps when the others work on `own` tiles of kTile tokens.
+// How many of `grid` CTAs work on the prefixes' `pre` steps when the others work on `own` tiles of kTile tokens: by
+// what a step costs (in halves of an own tile; measured where both kinds end together), and with few steps
+// a CTA the same whole number of them for all, an even one where two sets of warps take them in turn, so
+// that none begins a second unit for one step.  (Integers: two kernels have to come to the same number.)
 template <int D>
 __device__ __forceinline__ uint32_t prefix_ctas(uint32_t grid, uint32_t pre, uint32_t own) {
     if (pre == 0) return 0;
-    if (own == 0) return min(grid, pre);
-    constexpr uint32_t kCost = D == 256 ? 4 : D == 128 ? 7 : 9;   // of a step, in own tiles
-    // (integers: two kernels have to come to the same number)
-    const unsigned long long w = static_cast<unsigned long long>(kCost) * pre, all = w + own;
-    const uint32_t n = static_cast<uint32_t>((w * grid + all / 2) / all);
-    return min(min(max(n, 1u), grid - 1), pre);
+    constexpr uint32_t kCost = D == 256 ? 4 : D == 128 ? 11 : 18;
+    const unsigned long long w = static_cast<unsigned long long>(kCost) * pre, all = w + 2ull * own;
+    uint32_t n = static_cast<uint32_t>((w * grid + all / 2) / all);
+    n = min(max(n, 1u), own > 0 ? grid - 1 : grid);
+    uint32_t each = (pre + n - 1) / n;
+    if (each <= 8) {
+        if (D != 256) each += each & 1;
+        n = (pre + each - 1) / each;
+    }
+    return n;
 }
 
 struct MergeArgs {

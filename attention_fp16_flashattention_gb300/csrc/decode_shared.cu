@@ -142,6 +142,36 @@ __device__ __forceinline__ void store_f32x8(float* p, const uint32_t* v) {
                  : "memory");
 }
 
+// 32 columns of each of the warp's 32 rows (a lane a row, at `out`, where live): by way of `stage` in shared memory,
+// so that a store writes whole lines of four rows and not a sector of 32.  Without a stage (Q in tensor memory) a
+// lane stores its own.
+constexpr int kStageBytes = 32 * 32 * 4;
+template <int D>
+__device__ __forceinline__ void store_rows(uint8_t* stage, const uint32_t (&o)[32], float* out, bool live, int lane) {
+    if constexpr (Pre<D>::kQTmem) {
+        if (live) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) store_f32x8(out + e, o + e);
+        }
+        __syncwarp();
+    } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)   // 16-byte pieces, exchanged within the row so that eight lanes meet all banks
+            *reinterpret_cast<uint4*>(stage + lane * 128 + ((e ^ (lane & 7)) << 4)) =
+                make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+        __syncwarp();
+        const long long to = live ? reinterpret_cast<long long>(out) : 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = 4 * i + (lane >> 3), e = lane & 7;
+            const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 128 + ((e ^ (r & 7)) << 4));
+            float* row = reinterpret_cast<float*>(__shfl_sync(0xffffffffu, to, r));
+            if (row) *reinterpret_cast<uint4*>(row + 4 * e) = v;
+        }
+        __syncwarp();
+    }
+}
+
 // A part of a unit: steps [s0, s1) of it, for rows row0 .. of KV head hk of group g.
 struct Part {
     int hk, row0, rows;   // rows: of the group and KV head, in all
@@ -374,18 +404,15 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
             const int gr = p.row0 + half * kStepRows + row;          // the row among its KV head's of the group
             const bool live = gr < p.rows;
             const bool warp_live = p.row0 + half * kStepRows + quarter * 32 < p.rows;
-            // Q of the part: the row, or where two sets work on the same rows half of its columns.  The last part's
-            // products with the old one are done (its epilogue waited for them).
+            // Q of the part.  The last part's products with the old one are done (its epilogue waited for them); that
+            // its rows no longer pass through the Q tiles has to be waited for.
+            if (!C::kQTmem && ic > 0) ok = wait_warp(&ctrl->o_free, (ic - 1) & 1, w);
+            if (!ok) break;
             int lim = 0;   // the row sees prefix tokens t < lim
             {
                 const int member = gr / d.G, rem = gr - member * d.G, b = p.first + member;
+                const int len = live ? d.kv_lens[b] : 0;   // under way beside Q
                 const __half* q = d.q + ((static_cast<long long>(b) * d.Hkv + p.hk) * d.G + rem) * D;
-                uint8_t* dst = sQ + (p.pair ? set : 0) * C::kQTile + row * 128;
-                int ch0 = 0, ch1 = C::kChunks;
-                if (C::kSets == 2 && !p.pair) {
-                    ch0 = set * ((C::kChunks + 1) / 2);
-                    ch1 = min(ch0 + (C::kChunks + 1) / 2, C::kChunks);
-                }
                 if constexpr (C::kQTmem) {
 #pragma unroll 2
                     for (int ch = 0; ch < C::kChunks; ++ch) {
@@ -402,21 +429,47 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
                     }
                     tmem_st_wait();
                     tc_fence_before();
-                } else {
-#pragma unroll 2
-                    for (int ch = ch0; ch < ch1; ++ch) {
+                } else if (p.pair) {
+                    // The warp's 32 rows, kRowLanes lanes a row, so that a load takes whole lines (a thread a row takes
+                    // 32 lines a load).
+                    constexpr int kRowLanes = D / 8, kAt = 32 / kRowLanes;
+                    uint8_t* dst = sQ + set * C::kQTile;
+                    const int c16 = lane % kRowLanes;
+                    const long long at = live ? q - d.q : -1;
+#pragma unroll 1
+                    for (int i = 0; i < 32; i += 8 * kAt) {
                         uint4 v[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            v[e] = live ? reinterpret_cast<const uint4*>(q + ch * 64)[e] : make_uint4(0, 0, 0, 0);
+                        for (int e = 0; e < 8; ++e) {
+                            const long long from = __shfl_sync(0xffffffffu, at, i + e * kAt + lane / kRowLanes);
+                            v[e] = make_uint4(0, 0, 0, 0);
+                            if (from >= 0) v[e] = reinterpret_cast<const uint4*>(d.q + from)[c16];
+                        }
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<uint4*>(dst + ch * C::kQChunk + ((e ^ (row & 7)) << 4)) = v[e];
+                        for (int e = 0; e < 8; ++e) {
+                            const int qrow = quarter * 32 + i + e * kAt + lane / kRowLanes;
+                            *reinterpret_cast<uint4*>(dst + (c16 >> 3) * C::kQChunk + qrow * 128 +
+                                                      (((c16 & 7) ^ (qrow & 7)) << 4)) = v[e];
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                } else {
+                    // Two sets on the same rows, often few of them: a thread a row, half of the row's pieces.
+                    constexpr int kPieces = D / 16;
+                    uint4 v[kPieces];
+#pragma unroll
+                    for (int e = 0; e < kPieces; ++e)
+                        v[e] = live ? reinterpret_cast<const uint4*>(q)[set * kPieces + e] : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int e = 0; e < kPieces; ++e) {
+                        const int c16 = set * kPieces + e;
+                        *reinterpret_cast<uint4*>(sQ + (c16 >> 3) * C::kQChunk + row * 128 +
+                                                  (((c16 & 7) ^ (row & 7)) << 4)) = v[e];
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 }
                 if (live) {
-                    const int own = d.kv_lens[b] - p.prefix;   // (outside [0, max_own]: the merge drops the row)
+                    const int own = len - p.prefix;   // (outside [0, max_own]: the merge drops the row)
                     if (own >= 0 && own <= a.max_own) lim = min(p.prefix, p.prefix + own - d.nq + rem % d.nq + 1);
                 }
             }
@@ -551,7 +604,6 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
                 const float f0 = record_weight(ml0, M), f1 = record_weight(ml1, M);
                 constexpr int kCols = D / 2;   // a thread joins half of the columns
                 const uint32_t o_tm = tl + kTO + set * kCols;
-                float* out = a.pre_o + rec * D + set * kCols;
 #pragma unroll 1
                 for (int c = 0; c < kCols; c += 32) {
                     uint32_t o0[32], o1[32];
@@ -564,23 +616,21 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
                                                 (any1 ? f1 * __uint_as_float(o1[e]) : 0.0f));
                     if (live) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) store_f32x8(out + c + e, o0 + e);
+                        for (int e = 0; e < 32; e += 8)
+                            store_f32x8(a.pre_o + rec * D + set * kCols + c + e, o0 + e);
                     }
                     __syncwarp();
                 }
                 if (live && set == 0) a.pre_ml[rec] = make_float2(M, f0 * ml0.y + f1 * ml1.y);
             } else {
-                float* out = a.pre_o + rec * D;
+                // (through the warp's part of the Q tiles, which no product reads any more)
+                uint8_t* stage = sQ + (warp - 2) * kStageBytes;
 #pragma unroll 1
                 for (int c = 0; c < D; c += 32) {
                     uint32_t o0[32];
                     tmem_ld32(tl + kTO + set * D + c, o0);
                     tmem_ld_wait();
-                    if (live) {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 8) store_f32x8(out + c + e, o0 + e);
-                    }
-                    __syncwarp();
+                    store_rows<D>(stage, o0, a.pre_o + rec * D + c, live, lane);
                 }
                 if (live) a.pre_ml[rec] = make_float2(m_run, l);   // (a sum of 0: the record holds no O)
             }
