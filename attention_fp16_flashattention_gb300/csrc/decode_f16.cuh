@@ -762,7 +762,7 @@ struct PrefixRecords {
     const float2* part_ml;
     const uint32_t* work;    // [groups + 1]: prefix steps of the units of the groups before g
     const int2* seq;         // [B]: the prefix's tokens (-1: rejected) and the group
-    const uint32_t* total;   // tiles of all sequences' own tokens
+    const uint32_t* total;   // tiles of all sequences' own tokens; CTAs that worked on the prefixes
     const int32_t *starts, *lens;   // of the call: [groups + 1], [groups]
     int groups, max_prefix, ps;
 };
@@ -778,21 +778,38 @@ __device__ __forceinline__ uint32_t steps_of_rows(int rows) {
     return static_cast<uint32_t>((rows + kStepRows - 1) / kStepRows);
 }
 
-// How many of `grid` CTAs work on the prefixes' `pre` steps when the others work on `own` tiles of kTile tokens: by
-// what a step costs (in halves of an own tile; measured where both kinds end together), and with few steps
-// a CTA the same whole number of them for all, an even one where two sets of warps take them in turn, so
-// that none begins a second unit for one step.  (Integers: two kernels have to come to the same number.)
+// Steps of each unit of a group with `rows` query rows of a KV head and `tiles` prefix tiles, 0 if they differ.
 template <int D>
-__device__ __forceinline__ uint32_t prefix_ctas(uint32_t grid, uint32_t pre, uint32_t own) {
+__device__ __forceinline__ uint32_t unit_steps(int rows, uint32_t tiles) {
+    constexpr uint32_t kPer = Unit<D>::kRows / kStepRows;
+    const uint32_t per_tile = steps_of_rows(rows);
+    return per_tile % kPer == 0 ? kPer * tiles : per_tile < kPer ? per_tile * tiles : 0u;
+}
+
+// How many of `grid` CTAs work on the prefixes' `pre` steps when the others work on `own` tiles of kTile tokens: by
+// what a step costs (in halves of an own tile; measured where both kinds end together), and so that no CTA
+// begins a second unit for the rest of its steps where that can be had: with few steps a CTA the same whole
+// number of them for all (an even one where two sets of warps take them in turn), and with units of one length
+// (`unit` steps, else 0) the same number of CTAs for each.  (64 sequences behind 32,768 tokens: 74 us with such
+// CTAs, 66 without: O out and Q in pass the SM's port to memory beside the caches' stream.)  Integers: two
+// kernels have to come to the same number.
+template <int D>
+__device__ __forceinline__ uint32_t prefix_ctas(uint32_t grid, uint32_t pre, uint32_t own, uint32_t unit) {
     if (pre == 0) return 0;
-    constexpr uint32_t kCost = D == 256 ? 4 : D == 128 ? 11 : 18;
+    constexpr uint32_t kCost = D == 256 ? 5 : D == 128 ? 10 : 16;
     const unsigned long long w = static_cast<unsigned long long>(kCost) * pre, all = w + 2ull * own;
+    const uint32_t most = own > 0 ? grid - 1 : grid;
     uint32_t n = static_cast<uint32_t>((w * grid + all / 2) / all);
-    n = min(max(n, 1u), own > 0 ? grid - 1 : grid);
+    n = min(max(n, 1u), most);
     uint32_t each = (pre + n - 1) / n;
     if (each <= 8) {
         if (D != 256) each += each & 1;
         n = (pre + each - 1) / each;
+    } else if (unit > 0) {
+        const uint32_t units = pre / unit;
+        uint32_t k = (n + units / 2) / units;
+        if (k * units > most) --k;
+        if (k > 0) n = k * units;
     }
     return n;
 }
@@ -863,7 +880,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
     if (early) {
         int len[kEarlySeqs / 32];   // tokens of sequences lane, lane + 32; -1: rejected
         int prefix = 0, first = 0, next = 0;   // kShared: of the row's group
-        uint32_t work = 0, Up = 0;
+        uint32_t work = 0, Up = 0, shortest = 0xFFFFFFFFu, longest = 0;
         bool good = true;
 #pragma unroll
         for (int e = 0; e < kEarlySeqs / 32; ++e) {
@@ -888,6 +905,11 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
                 }
                 const uint32_t steps =
                     p > 0 ? a.Hkv * steps_of_rows((s1 - s0) * grp * a.nq) * ((p + kPreTile - 1) / kPreTile) : 0u;
+                if (steps > 0) {
+                    const uint32_t u = unit_steps<D>((s1 - s0) * grp * a.nq, (p + kPreTile - 1) / kPreTile);
+                    shortest = min(shortest, u);
+                    longest = max(longest, u);
+                }
                 for (int i = 0; i < min(32, a.pre.groups - g0); ++i) {
                     const int f = __shfl_sync(0xffffffffu, s0, i), t = __shfl_sync(0xffffffffu, s1, i);
                     const int q = __shfl_sync(0xffffffffu, p, i);
@@ -920,7 +942,9 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
         U = __reduce_add_sync(0xffffffffu, total) * per_seq;
         if constexpr (kShared) {
             row_good = __all_sync(0xffffffffu, row_good);
-            const uint32_t P = prefix_ctas<D>(a.grid, Up, U);
+            shortest = __reduce_min_sync(0xffffffffu, shortest);
+            longest = __reduce_max_sync(0xffffffffu, longest);
+            const uint32_t P = prefix_ctas<D>(a.grid, Up, U, shortest == longest ? longest : 0u);
             grid -= P;
             if (row_good && prefix > 0) place_prefix(prefix, first, next, work, Up, P);
         }
@@ -929,8 +953,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (kShared && !early) {
         const int2 seq = a.pre.seq[b];
-        const uint32_t Up = a.pre.work[a.pre.groups], own = *a.pre.total;
-        const uint32_t P = prefix_ctas<D>(a.grid, Up, own);
+        const uint32_t Up = a.pre.work[a.pre.groups], own = a.pre.total[0], P = a.pre.total[1];
         grid -= P;
         if (seq.x >= 0 && own > 0) {
             before = a.prefix[b];

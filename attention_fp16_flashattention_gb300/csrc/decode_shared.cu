@@ -687,8 +687,10 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
     // ---- steps over every group's prefix
     const int per_g = (a.groups + kThreads - 1) / kThreads;
     const int g0 = min(tid * per_g, a.groups), g1 = min(g0 + per_g, a.groups);
+    __shared__ uint32_t s_shortest, s_longest;   // units
+    if (tid == 0) s_shortest = 0xFFFFFFFFu, s_longest = 0;
     bool order = true;
-    uint32_t sum = 0;
+    uint32_t sum = 0, shortest = 0xFFFFFFFFu, longest = 0;
     for (int g = g0; g < g1; ++g) {
         const int s = a.starts[g], e = a.starts[g + 1], p = a.prefix_lens[g];
         const bool in_order = s >= 0 && s <= e && e <= d.B && (g > 0 || s == 0) && (g + 1 < a.groups || e == d.B);
@@ -698,10 +700,19 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
         uint32_t n = 0;
         if (in_order && good)
             n = static_cast<uint32_t>(d.Hkv) * steps_of_rows((e - s) * d.G) * ((p + kPreTile - 1) / kPreTile);
+        if (n > 0) {
+            const uint32_t u = unit_steps<D>((e - s) * d.G, (p + kPreTile - 1) / kPreTile);
+            shortest = min(shortest, u);
+            longest = max(longest, u);
+        }
         tiles[g] = n;
         sum += n;
     }
     order = __syncthreads_and(order);
+    if (order && longest > 0) {
+        atomicMin(&s_shortest, shortest);
+        atomicMax(&s_longest, longest);
+    }
     uint32_t Up = 0;
     uint32_t run = block_sum<kThreads>(order ? sum : 0, Up);
     for (int g = g0; g < g1; ++g) {
@@ -748,10 +759,13 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
     }
     uint32_t own = 0;
     run = block_sum<kThreads>(sum, own);   // (its barriers also make `tiles` and `pre` whole)
-    if (lead && tid == 0) *a.total_out = own;
     // The merge grid may start launching now; it waits for this grid to finish.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t P = prefix_ctas<D>(gridDim.x, Up, own);
+    const uint32_t P = prefix_ctas<D>(gridDim.x, Up, own, s_shortest == s_longest ? s_longest : 0u);
+    if (lead && tid == 0) {
+        a.total_out[0] = own;
+        a.total_out[1] = P;
+    }
     if (blockIdx.x < P) {
         prefix_body<D>(pk, pv, a, smem, tiles, reinterpret_cast<Exchange*>(pre), blockIdx.x, P);
         return;

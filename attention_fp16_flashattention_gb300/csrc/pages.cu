@@ -262,31 +262,46 @@ __global__ void __launch_bounds__(kThreads) kv_release_kernel(const TableArgs a)
         return at.all_y;
     };
     int total = place(sum);
-    auto entry = [&](int x, int& b) -> int {
-        b = find(first, a.B, x);
-        return a.table[static_cast<long long>(b) * a.max_pages + from[b] + x - first[b]];
-    };
     const int step = kThreads * gridDim.x, self = blockIdx.x * kThreads + tid;
-    int kept[kKeep];
-    auto check = [&](int x) -> int {
-        int b;
-        const int page = entry(x, b);
-        if (page < 0 || page >= a.num_phys) {   // the sequence keeps all of its pages
-            atomicOr(a.status, kDevBadPage);
-            for (unsigned r = 0; r < gridDim.x; ++r) {
+    // Entries x0, x0 + step, ... below `end`, all under way at once.
+    auto load = [&](int (&page)[kKeep], int x0, int end) {
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u) {
+            const int x = x0 + u * step;
+            page[u] = 0;
+            if (x >= end) continue;
+            const int b = find(first, a.B, x);
+            page[u] = a.table[static_cast<long long>(b) * a.max_pages + from[b] + x - first[b]];
+        }
+    };
+    auto check = [&](const int (&page)[kKeep], int x0) {
+        bool bad = false;
+#pragma unroll
+        for (int u = 0; u < kKeep; ++u) bad |= page[u] < 0 || page[u] >= a.num_phys;
+        if (!bad) return;
+        atomicOr(a.status, kDevBadPage);
+#pragma unroll 1
+        for (int u = 0; u < kKeep; ++u) {
+            const int x = x0 + u * step;
+            if (x >= total) break;
+            const int b = find(first, a.B, x);
+            const int page_x = a.table[static_cast<long long>(b) * a.max_pages + from[b] + x - first[b]];
+            if (page_x >= 0 && page_x < a.num_phys) continue;
+            for (unsigned r = 0; r < gridDim.x; ++r) {   // the sequence keeps all of its pages
                 cluster.map_shared_rank(count, r)[b] = 0;
                 *cluster.map_shared_rank(&s_bad, r) = 1;
             }
         }
-        return page;
     };
+    int kept[kKeep];
+    load(kept, self, total);
     cluster.sync();   // every CTA's tables are laid out before another marks a sequence in them
-#pragma unroll
-    for (int u = 0; u < kKeep; ++u) {
-        const int x = self + u * step;
-        kept[u] = x < total ? check(x) : 0;
+    check(kept, self);
+    for (int x0 = self + kKeep * step; x0 < total; x0 += kKeep * step) {
+        int page[kKeep];
+        load(page, x0, total);
+        check(page, x0);
     }
-    for (int x = self + kKeep * step; x < total; x += step) check(x);
     cluster.sync();   // (and every CTA has read the old count)
     const bool again = s_bad != 0;
     if (again) {
@@ -306,16 +321,13 @@ __global__ void __launch_bounds__(kThreads) kv_release_kernel(const TableArgs a)
     __syncthreads();
     given = s_given;
     if (lead && tid == 0) *a.count_out = stack + given;
-    if (!again) {
+    for (int x0 = self; x0 < given; x0 += kKeep * step) {
+        if (again || x0 != self) load(kept, x0, given);
 #pragma unroll
         for (int u = 0; u < kKeep; ++u) {
-            const int x = self + u * step;
+            const int x = x0 + u * step;
             if (x < given) a.free_pages[stack + x] = kept[u];
         }
-    }
-    for (int x = again ? self : self + kKeep * step; x < given; x += step) {
-        int b;
-        a.free_pages[stack + x] = entry(x, b);
     }
 }
 
