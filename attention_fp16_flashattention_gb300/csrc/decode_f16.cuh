@@ -762,7 +762,7 @@ struct PrefixRecords {
     const float2* part_ml;
     const uint32_t* work;    // [groups + 1]: prefix steps of the units of the groups before g
     const int2* seq;         // [B]: the prefix's tokens (-1: rejected) and the group
-    const uint32_t* total;   // tiles of all sequences' own tokens; CTAs that worked on the prefixes
+    const uint32_t* total;   // tiles of all sequences' own tokens; PreSplit
     const int32_t *starts, *lens;   // of the call: [groups + 1], [groups]
     int groups, max_prefix, ps;
 };
@@ -786,32 +786,35 @@ __device__ __forceinline__ uint32_t unit_steps(int rows, uint32_t tiles) {
     return per_tile % kPer == 0 ? kPer * tiles : per_tile < kPer ? per_tile * tiles : 0u;
 }
 
-// How many of `grid` CTAs work on the prefixes' `pre` steps when the others work on `own` tiles of kTile tokens: by
-// what a step costs (in halves of an own tile; measured where both kinds end together), and so that no CTA
-// begins a second unit for the rest of its steps where that can be had: with few steps a CTA the same whole
-// number of them for all (an even one where two sets of warps take them in turn), and with units of one length
-// (`unit` steps, else 0) the same number of CTAs for each.  (64 sequences behind 32,768 tokens: 74 us with such
-// CTAs, 66 without: O out and Q in pass the SM's port to memory beside the caches' stream.)  Integers: two
-// kernels have to come to the same number.
+// How the prefixes' `pre` steps are shared when the others of `grid` CTAs work on `own` tiles of kTile tokens:
+// `ctas` of them take equal ranges of `total` steps (>= pre, the last may be short).  How many, by what a step costs
+// (in halves of an own tile; measured where both kinds end together), and such that ranges and units begin together
+// where that can be had: with units of one length (`unit` steps, else 0) the same number of CTAs for each, else
+// the same whole number of steps (with few an even one where two sets of warps take them in turn).  A second unit
+// in a range costs O out and Q in, which pass the SM's port to memory beside the caches' stream (64 sequences behind
+// 32,768 tokens: 74 us, 66 without), and units of one KV head that begin together share their tiles in L2.
+// Integers: two kernels have to come to the same numbers.
+struct PreSplit {
+    uint32_t ctas, total;
+};
 template <int D>
-__device__ __forceinline__ uint32_t prefix_ctas(uint32_t grid, uint32_t pre, uint32_t own, uint32_t unit) {
-    if (pre == 0) return 0;
+__device__ __forceinline__ PreSplit prefix_split(uint32_t grid, uint32_t pre, uint32_t own, uint32_t unit) {
+    if (pre == 0) return PreSplit{0, 0};
     constexpr uint32_t kCost = D == 256 ? 5 : D == 128 ? 10 : 16;
     const unsigned long long w = static_cast<unsigned long long>(kCost) * pre, all = w + 2ull * own;
     const uint32_t most = own > 0 ? grid - 1 : grid;
     uint32_t n = static_cast<uint32_t>((w * grid + all / 2) / all);
     n = min(max(n, 1u), most);
     uint32_t each = (pre + n - 1) / n;
-    if (each <= 8) {
-        if (D != 256) each += each & 1;
-        n = (pre + each - 1) / each;
-    } else if (unit > 0) {
+    if (each > 8 && unit > 0) {
         const uint32_t units = pre / unit;
         uint32_t k = (n + units / 2) / units;
         if (k * units > most) --k;
-        if (k > 0) n = k * units;
+        if (k > 0) return PreSplit{k * units, pre};
     }
-    return n;
+    if (each <= 8 && D != 256) each += each & 1;
+    n = (pre + each - 1) / each;
+    return PreSplit{n, n * each};
 }
 
 struct MergeArgs {
@@ -865,7 +868,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
     uint32_t grid = a.grid, pre_c0 = 0, n_pre = 0;   // kShared: CTAs of the own tokens; the prefix's records
     long long pre_row = 0;
     // kShared: what the prefix of length p of group g (whose steps begin at `work`) leaves of the row's unit
-    auto place_prefix = [&](int p, int first, int next, uint32_t work, uint32_t Up, uint32_t P) {
+    auto place_prefix = [&](int p, int first, int next, uint32_t work, const PreSplit& ps) {
         const int grows = (next - first) * grp * a.nq;
         const int gr = (b - first) * grp * a.nq + r;   // the row among its KV head's of the group
         const uint32_t n = (p + kPreTile - 1) / kPreTile, per_tile = steps_of_rows(grows);
@@ -873,8 +876,8 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
         const uint32_t before_unit = gr / Unit<D>::kRows * (Unit<D>::kRows / kStepRows);
         const uint32_t u0 = work + (hk * per_tile + before_unit) * n;
         const uint32_t steps = min(per_tile - before_unit, static_cast<uint32_t>(Unit<D>::kRows / kStepRows)) * n;
-        pre_c0 = warp_of(u0, P, Up);
-        n_pre = warp_of(u0 + steps - 1, P, Up) - pre_c0 + 1;
+        pre_c0 = warp_of(u0, ps.ctas, ps.total);
+        n_pre = warp_of(u0 + steps - 1, ps.ctas, ps.total) - pre_c0 + 1;
         pre_row = static_cast<long long>(first) * a.Hq * a.nq + static_cast<long long>(hk) * grows + gr;
     };
     if (early) {
@@ -944,24 +947,25 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
             row_good = __all_sync(0xffffffffu, row_good);
             shortest = __reduce_min_sync(0xffffffffu, shortest);
             longest = __reduce_max_sync(0xffffffffu, longest);
-            const uint32_t P = prefix_ctas<D>(a.grid, Up, U, shortest == longest ? longest : 0u);
-            grid -= P;
-            if (row_good && prefix > 0) place_prefix(prefix, first, next, work, Up, P);
+            const PreSplit ps = prefix_split<D>(a.grid, Up, U, shortest == longest ? longest : 0u);
+            grid -= ps.ctas;
+            if (row_good && prefix > 0) place_prefix(prefix, first, next, work, ps);
         }
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (kShared && !early) {
         const int2 seq = a.pre.seq[b];
-        const uint32_t Up = a.pre.work[a.pre.groups], own = a.pre.total[0], P = a.pre.total[1];
-        grid -= P;
+        const uint32_t own = a.pre.total[0];
+        const PreSplit ps{a.pre.total[1], a.pre.total[2]};
+        grid -= ps.ctas;
         if (seq.x >= 0 && own > 0) {
             before = a.prefix[b];
             T = (a.prefix[b + 1] - before) / per_seq;
             U = a.prefix[a.B];
         }
         if (seq.x > 0)
-            place_prefix(seq.x, a.pre.starts[seq.y], a.pre.starts[seq.y + 1], a.pre.work[seq.y], Up, P);
+            place_prefix(seq.x, a.pre.starts[seq.y], a.pre.starts[seq.y + 1], a.pre.work[seq.y], ps);
     } else if (!early) {
         before = a.prefix[b];
         T = (a.prefix[b + 1] - before) / per_seq;

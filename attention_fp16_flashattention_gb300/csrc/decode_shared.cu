@@ -10,7 +10,7 @@
 // (with P in two halves) the tensor cores bound it, below them the bytes.
 //
 // One grid, one CTA per SM, and two kinds of work, so that the one's memory time runs beside the other's
-// arithmetic.  Every CTA works out the same tile counts from the lengths (a few loads, two scans): `prefix_ctas`
+// arithmetic.  Every CTA works out the same tile counts from the lengths (a few loads, two scans): `prefix_split`
 // of them share the prefixes' tiles evenly, the others the own tokens' (decode_f16_body), each a contiguous
 // range of tiles laid end to end.  A merge kernel joins the records of both.
 //
@@ -211,7 +211,7 @@ __device__ __forceinline__ Part next_part(const SharedArgs& a, const uint32_t* w
 template <int D>
 __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtensorMap& tv, const SharedArgs& a,
                                             uint8_t* smem, const uint32_t* work, Exchange* ex,
-                                            uint32_t cta, uint32_t n_ctas) {
+                                            uint32_t cta, const PreSplit& split) {
     using C = Pre<D>;
     uint8_t* sQ = smem;
     uint8_t* sKV = smem + C::kQBytes;
@@ -246,9 +246,8 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
     tc_fence_after();
     const uint32_t tmem = ctrl->tmem_base;
     const WaitCtl w{d.wait_limit, d.status, &ctrl->abort};
-    const uint32_t Up = work[a.groups];
-    const uint32_t end = warp_start(cta + 1, n_ctas, Up);
-    uint32_t pos = warp_start(cta, n_ctas, Up);
+    const uint32_t end = min(warp_start(cta + 1, split.ctas, split.total), work[a.groups]);
+    uint32_t pos = warp_start(cta, split.ctas, split.total);
     // Counts over all parts: steps (sc; its parity is the S and P buffer and, with two, the set), tiles (tc), parts
     // (ic), ring places.
     uint32_t sc = 0, tc = 0, ic = 0, ring = 0;
@@ -761,13 +760,15 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
     run = block_sum<kThreads>(sum, own);   // (its barriers also make `tiles` and `pre` whole)
     // The merge grid may start launching now; it waits for this grid to finish.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const uint32_t P = prefix_ctas<D>(gridDim.x, Up, own, s_shortest == s_longest ? s_longest : 0u);
+    const PreSplit split = prefix_split<D>(gridDim.x, Up, own, s_shortest == s_longest ? s_longest : 0u);
+    const uint32_t P = split.ctas;
     if (lead && tid == 0) {
         a.total_out[0] = own;
-        a.total_out[1] = P;
+        a.total_out[1] = split.ctas;
+        a.total_out[2] = split.total;
     }
     if (blockIdx.x < P) {
-        prefix_body<D>(pk, pv, a, smem, tiles, reinterpret_cast<Exchange*>(pre), blockIdx.x, P);
+        prefix_body<D>(pk, pv, a, smem, tiles, reinterpret_cast<Exchange*>(pre), blockIdx.x, split);
         return;
     }
     if (own == 0) return;
