@@ -396,7 +396,7 @@ int run_rope(const RopeCall& c) {
     if (c.rot > c.D || c.Hq > (1 << 24) || c.Hk > (1 << 24) ||
         static_cast<long long>(c.B) * c.S > 0x7FFFFFFFLL)
         return GBATTN_ERR_SHAPE;
-    if (c.axes > 1 && !c.sections) return GBATTN_ERR_NULL;
+    if (c.rot > 0 && c.axes > 1 && !c.sections) return GBATTN_ERR_NULL;
     long long pairs = 0;
     if (c.sections && c.rot > 0) {
         for (int i = 0; i < c.axes; ++i) {

@@ -108,6 +108,7 @@ def test_rope_refusals(lib):
     assert call(qo=A(0)) in good and call(qo=A(0), ko=A(1)) in good
     assert call(k=None, ko=None, Hk=0) in good and call(axes=3, sections=sections(32, 16, 16)) in good
     assert call(rot=0, pos=None, freqs=None, scale=0.0) in good
+    assert call(rot=0, axes=3, freqs=None) in good and call(rot=0, sections=sections(9)) in good
     assert call(qw=None, kw=None, eps=0.0) in good and call(axes=2, sections=sections(0, 64)) in good
     # heads of one packed tensor [B][S][4 + 2 + 2][128]: apart, and not
     row = 8 * 128
