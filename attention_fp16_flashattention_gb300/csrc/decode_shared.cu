@@ -47,7 +47,7 @@ struct Pre {
     static constexpr int kSets = D == 256 ? 1 : 2;
     static constexpr int kBufs = kSets;                            // S and P buffers
     static constexpr bool kQTmem = D == 256;                       // Q in tensor memory
-    static constexpr uint32_t kTP = kBufs * kTBuf, kTQ = 2 * kTP;
+    static constexpr uint32_t kTP = kBufs * kTBuf;                 // tensor memory columns of P and, behind it, Q
     static constexpr int kThreads = 32 * (3 + 4 * kSets);
     static constexpr int kPvWarp = 2 + 4 * kSets;
     static constexpr int kChunks = D / 64;                         // 64-column chunks of a row
@@ -321,18 +321,18 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
                 if (sc >= C::kBufs) ok = ok && wait_warp(&ctrl->s_free[buf], (sc / C::kBufs - 1) & 1, w);
                 if (!ok) break;
                 const bool last = s + 1 == p.s1 || !p.pair || (s & 1);   // of the tile, here
-                const uint32_t qa = smem_addr(sQ + (p.pair ? buf : 0) * C::kQTile);
-                const uint32_t ka = smem_addr(sKV + slot * C::kSlot);
+                const uint64_t qd = sdesc_sw128(smem_addr(sQ + (p.pair ? buf : 0) * C::kQTile), 16, 1024);
+                const uint64_t kd = sdesc_sw128(smem_addr(sKV + slot * C::kSlot), 16, 1024);
                 tc_fence_after();
                 if (elect_one()) {
 #pragma unroll
                     for (int k16 = 0; k16 < D / 16; ++k16) {
-                        const uint64_t kd = sdesc_sw128(ka + (k16 >> 2) * C::kKvChunk + (k16 & 3) * 32, 16, 1024);
+                        // (descriptors by addition to their address fields, in units of 16 bytes)
+                        const uint64_t k = kd + (k16 >> 2) * (C::kKvChunk / 16) + (k16 & 3) * 2;
                         if constexpr (C::kQTmem)
-                            mma_ts(tmem + buf * kTBuf, tmem + C::kTQ + k16 * 8, kd, C::kIdescQK, k16 > 0 ? 1u : 0u);
+                            mma_ts(tmem + buf * kTBuf, tmem + 2 * C::kTP + k16 * 8, k, C::kIdescQK, k16 > 0 ? 1u : 0u);
                         else
-                            mma_ss(tmem + buf * kTBuf,
-                                   sdesc_sw128(qa + (k16 >> 2) * C::kQChunk + (k16 & 3) * 32, 16, 1024), kd,
+                            mma_ss(tmem + buf * kTBuf, qd + (k16 >> 2) * (C::kQChunk / 16) + (k16 & 3) * 2, k,
                                    C::kIdescQK, k16 > 0 ? 1u : 0u);
                     }
                     mma_commit(&ctrl->s_full[buf]);
@@ -351,7 +351,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
             if (ic > 0) ok = wait_warp(&ctrl->o_free, (ic - 1) & 1, w);
             for (int s = p.s0; ok && s < p.s1; ++s, ++sc) {
                 const int slot = (2 * tc + 1) % C::kNS, buf = sc % C::kBufs;
-                const uint32_t va = smem_addr(sKV + slot * C::kSlot);
+                const uint64_t vd = sdesc_sw128(smem_addr(sKV + slot * C::kSlot), C::kKvChunk, 1024);
                 if (s == p.s0 || !p.pair || !(s & 1)) {
                     ok = wait_warp(&ctrl->full[slot], ((2 * tc + 1) / C::kNS) & 1, w);
                     if (!ok) break;
@@ -380,7 +380,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
 #pragma unroll
                         for (int k16 = 0; k16 < kPreTile / 16; ++k16)
                             mma_ts(o, tmem + C::kTP + buf * kTBuf + half * kTPLo + k16 * 8,
-                                   sdesc_sw128(va + k16 * 2048, C::kKvChunk, 1024), C::kIdescPV,
+                                   vd + k16 * (2048 / 16), C::kIdescPV,
                                    (begun || half > 0 || k16 > 0) ? 1u : 0u);
                     if (last) mma_commit(&ctrl->empty[slot]);
                     mma_commit(&ctrl->pv_done[buf]);
@@ -424,7 +424,7 @@ __device__ __forceinline__ void prefix_body(const CUtensorMap& tk, const CUtenso
                             v[4 * e + 2] = x.z;
                             v[4 * e + 3] = x.w;
                         }
-                        tmem_st32(tl + C::kTQ + ch * 32, v);
+                        tmem_st32(tl + 2 * C::kTP + ch * 32, v);
                     }
                     tmem_st_wait();
                     tc_fence_before();
