@@ -13,7 +13,9 @@
 // have read them first: then one cluster does the work, and its barrier comes in between.
 //
 // Bound by latency: the lengths, the stack's or the table's entries and the stores, one
-// behind the other; 8 bytes a token and 8 a page are nothing beside that.
+// behind the other; 8 bytes a token and 8 a page are nothing beside that.  Measured (graph replays): one
+// token for 64 sequences 4.0 us, 32 prompts of 131,000 tokens 4.6, drafted tokens of 64 sequences back 4.0,
+// 100,000 pages back 14.0 (eight SMs look at each of them; with 1024 threads a CTA 9.7, but 5.0 for the few).
 #include <cooperative_groups.h>
 
 #include <mutex>
