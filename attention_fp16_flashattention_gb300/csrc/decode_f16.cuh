@@ -764,7 +764,7 @@ struct PrefixRecords {
     const int2* seq;         // [B]: the prefix's tokens (-1: rejected) and the group
     const uint32_t* total;   // tiles of all sequences' own tokens; PreSplit
     const int32_t *starts, *lens;   // of the call: [groups + 1], [groups]
-    int groups, max_prefix, ps;
+    int groups, max_prefix, ps, cap;   // cap: slots of a page-table row
 };
 // A unit: up to kUnit query rows of a group and KV head.  A step: 128 of its rows against kPreTile prefix tokens;
 // a unit of more than 128 rows takes two steps a tile.
@@ -919,7 +919,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
 #pragma unroll
                     for (int e = 0; e < kEarlySeqs / 32; ++e) {
                         const int x = 32 * e + lane;
-                        if (x >= f && x < t) own[e] = q < 0 || len[e] < q || len[e] - q > a.max_kv ? -1 : len[e] - q;
+                        if (x >= f && x < t) own[e] = q < 0 || len[e] < q || len[e] - q > a.max_kv || len[e] > a.pre.cap ? -1 : len[e] - q;
                     }
                     if (b >= f && b < t) prefix = q, first = f, next = t, work = Up;
                     Up += __shfl_sync(0xffffffffu, steps, i);

@@ -108,6 +108,7 @@ struct SharedArgs {
     int2* seq_out;
     uint32_t* total_out;
     int groups, max_prefix, max_own, box_rows, box_bits;
+    int cap;                               // slots of a page-table row
 };
 
 // Exclusive sums over the block; `all` gets the total.  One barrier before and one inside.
@@ -706,7 +707,7 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
         const bool in_order = s >= 0 && s <= e && e <= d.B && (g > 0 || s == 0) && (g + 1 < a.groups || e == d.B);
         const bool good = p >= 0 && p <= a.max_prefix && p % d.ps == 0;
         order = order && in_order;
-        if (!good && in_order && lead) atomicOr(d.status, kDevBadLength);
+        if (!good && lead) atomicOr(d.status, kDevBadLength);
         uint32_t n = 0;
         if (in_order && good)
             n = static_cast<uint32_t>(d.Hkv) * steps_of_rows((e - s) * d.G) * ((p + kPreTile - 1) / kPreTile);
@@ -756,7 +757,7 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
                 p = -1;
             } else {
                 const int n = d.B <= kThreads ? my_len : d.kv_lens[b];
-                if (n < p || n - p > a.max_own) {
+                if (n < p || n - p > a.max_own || n > a.cap) {
                     p = -1;
                     if (lead) atomicOr(d.status, kDevBadLength);
                 } else {
@@ -970,6 +971,7 @@ extern "C" int attn_paged_decode_shared_f16_fwd(const void* q, const void* k_pag
     a.groups = groups;
     a.max_prefix = max_prefix_len;
     a.max_own = max_own_len;
+    a.cap = slots_row < 0x7FFFFFFFLL ? static_cast<int>(slots_row) : 0x7FFFFFFF;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int n = static_cast<int>(ctas);
     auto go = [&](auto launch) { return launch(tk, tv, pk, pv, n, dev.device, a, s); };
@@ -997,7 +999,7 @@ extern "C" int attn_paged_decode_shared_f16_fwd(const void* q, const void* k_pag
     m.parts = static_cast<uint32_t>(warps_of(D) / plan.side);
     m.out = d.out;
     m.pre = PrefixRecords{a.pre_o, a.pre_ml, a.work_out, a.seq_out, a.total_out, group_starts, prefix_lens,
-                          groups, max_prefix_len, page_size};
+                          groups, max_prefix_len, page_size, a.cap};
     // Warps per row by the records of an average row, of either kind, as long as all of them fit the GPU at once:
     // every warp places its row's records by itself (1024 rows 29.4 us with two warps, 33.0 with four; 512 rows 38.8
     // and 35.8; 2048 rows 73.5 with one, 77.9 with two).

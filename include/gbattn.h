@@ -368,8 +368,8 @@ int attn_paged_decode_f16_fwd(const void* q, const void* k_pages, const void* v_
  *   max_prefix_len bounds the prefixes and max_own_len every kv_lens[b] - prefix_lens[g], both at most
  *   max_pages * page_size, 2^30; 0 allowed.  A prefix_lens[g] that is negative, above
  *   max_prefix_len or no multiple of page_size, or a kv_lens[b] outside
- *   [prefix_lens[g], prefix_lens[g] + max_own_len], sets GBATTN_DEV_BAD_LENGTH and yields O = 0,
- *   lse = -inf for the group or the sequence.  group_starts that do not ascend from 0 to B set
+ *   [prefix_lens[g], prefix_lens[g] + max_own_len] or above max_pages * page_size, sets
+ *   GBATTN_DEV_BAD_LENGTH and yields O = 0, lse = -inf for the group or the sequence.  group_starts that do not ascend from 0 to B set
  *   GBATTN_DEV_BAD_INDEX and yield O = 0, lse = -inf for all sequences.  Pages as for
  *   attn_paged_decode_f16_fwd.
  *   D is 64, 128 or 256; page_size a power of two >= 16; Hq % Hkv == 0; B, groups <= 4096; B * Hq * nq <= 2^30;

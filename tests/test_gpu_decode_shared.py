@@ -205,6 +205,11 @@ def test_bad_lengths(gb):
     x[5] = x[5].copy()
     x[5][1], x[5][2], x[5][5] = 63, 128 + 61, -1       # below the prefix, above max_own_len, negative
     rejected(gb, x, [0, 3, 4], gb.DEV_BAD_LENGTH, max_own_len=60, max_prefix_len=128)
+    x = fresh()                                        # a length past the table's row
+    x[5] = x[5].copy()
+    cap = 16 * x[3].shape[1]                           # (its own part alone would fit)
+    x[5][5], x[5][4], x[5][3] = cap + 1, 2 ** 31 - 1, cap + 10
+    rejected(gb, x, [0, 1, 2], gb.DEV_BAD_LENGTH)
     for bad in (-16, 136, 144, 2 ** 31 - 1):           # a prefix that is none
         x = fresh()
         x[7] = x[7].copy()
@@ -215,6 +220,19 @@ def test_bad_lengths(gb):
         x = fresh()
         x[6] = np.array(starts, dtype=np.int32)
         rejected(gb, x, [], gb.DEV_BAD_INDEX)
+
+
+def test_bad_lengths_among_many_sequences(gb):
+    """As above where the merge reads the tables that the decode kernel left (more than 64 sequences)."""
+    x = list(shared_inputs([(60, 64), (20, 32), (5, 0)], [3 + i % 30 for i in range(85)], 2, 1, 1, 64, 16, 21))
+    x[5] = x[5].copy()
+    x[5][7], x[5][70], x[5][84] = 63, 16 * x[3].shape[1] + 5, -9
+    good = np.setdiff1d(np.arange(85), [7, 70, 84])
+    rejected(gb, x, good, gb.DEV_BAD_LENGTH)
+    x[7] = np.array([64, 33, 0], dtype=np.int32)
+    rejected(gb, x, np.setdiff1d(good, np.arange(60, 80)), gb.DEV_BAD_LENGTH)
+    x[6] = np.array([0, 60, 59, 85], dtype=np.int32)
+    rejected(gb, x, [], gb.DEV_BAD_INDEX | gb.DEV_BAD_LENGTH)
 
 
 def test_bad_pages(gb):
