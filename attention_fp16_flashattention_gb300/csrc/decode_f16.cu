@@ -130,69 +130,14 @@ size_t decode_workspace_size(int B, int Hq, int Hkv, int nq, int max_kv, int D, 
     return decode_layout(sm_count_or_default(), B, Hkv, static_cast<int>(G), max_kv, D, weights).total;
 }
 
-// How many clusters of 1, 2, 4 and 8 CTAs of the one-kernel form run at once on a device: a CTA takes an SM,
-// and a cluster's SMs lie in one GPC (152 SMs hold 152, 76, 36 and 15).  null: the device refused.
 template <int D, int NB>
 const int* resident_clusters(int device) {
-    static std::once_flag once[64];
-    static int n[64][4];
-    static bool ok[64];
-    if (device < 0 || device >= 64) return nullptr;
-    std::call_once(once[device], [&] {
-        auto* kernel = decode_f16_kernel<D, NB, true>;
-        ok[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          Cfg<D>::kSmem) == cudaSuccess;
-        for (int i = 0; i < 4 && ok[device]; ++i) {
-            cudaLaunchConfig_t cfg{};
-            cfg.gridDim = dim3(1u << i);
-            cfg.blockDim = dim3(Cfg<D>::kThreads);
-            cfg.dynamicSmemBytes = Cfg<D>::kSmem;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 1u << i;
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            ok[device] = cudaOccupancyMaxActiveClusters(&n[device][i], kernel, &cfg) == cudaSuccess;
-        }
-        if (!ok[device]) cudaGetLastError();
-    });
-    return ok[device] ? n[device] : nullptr;
+    return resident_clusters<D, NB, decode_f16_kernel<D, NB, true>>(device);
 }
 const int* resident_clusters(int D, int R, int device) {
     if (D == 64) return R == 8 ? resident_clusters<64, 1>(device) : resident_clusters<64, 2>(device);
     if (D == 128) return R == 8 ? resident_clusters<128, 1>(device) : resident_clusters<128, 2>(device);
     return R == 8 ? resident_clusters<256, 1>(device) : resident_clusters<256, 2>(device);
-}
-
-// CTAs of a cluster when every stream gets one (kOne), 0 when the streams' tiles are laid end to end.  A
-// cluster saves the merge kernel, the tile prefix and the records' way through memory, but its SMs read
-// one stream only, whatever the others' lengths, and its warps add the weights of their own tiles one
-// after the other.  So where all clusters run at once, the largest that do, and max_kv_len gives a warp
-// at most `per_warp` tiles.  Measured, clusters against laid end to end, in us (streams: sequences with
-// one KV head of four rows, one length unless said):
-//   D = 128   1 stream 4,096 tokens 9.7 and 11.1, 8,192 11.9 and 11.2; 15 streams 6,144 13.0 and 16.1; 32
-//             of half to all of 2,048 9.7 and 13.7; 152 of half to all of 768 11.8 and 17.0
-//   D = 64    1 stream 8,192 9.9 and 10.8, 12,288 12.1 and 11.1; 8 streams 12,288 12.1 and 13.1; 152 of
-//             half to all of 1,536 13.2 and 18.5
-//   D = 256   1 stream 512 8.8 and 8.2; 8 streams 8.9 and 9.5; 15 streams 9.4 and 10.3
-//   weights   D = 128: 8 streams 2,048 11.1 and 12.1, 4,096 13.8 and 12.8; 15 of 6,144 6% less, 8 tiles a
-//             warp no gain; 152 of half to all of 768 16.4 and 19.3, of 1,536 27.3 and 25.8.  D = 64 alike.
-//             D = 256: 1 stream 512 10.6 and 10.7, 8 streams 11.0 and 11.9
-// With clusters of eight for up to 19 streams (152 SMs, of which 15 such clusters fit) 16 streams of half to
-// all of 512 took 13.2 us, in two waves; end to end takes 10.1, clusters of four 7.2.
-int cluster_of(long long streams, int max_kv, int D, bool weights, const int* resident) {
-    static_assert(kMaxCluster == 8, "resident_clusters asks for up to eight CTAs");
-    int bits = 3;
-    while (bits > 0 && streams > resident[bits]) --bits;
-    if (streams > resident[bits]) return 0;
-    const int per_warp = weights    ? D == 256 ? 1 : streams < 12 ? 2 : 6
-                         : D == 64  ? streams < 8 ? 8 : 12
-                         : D == 128 ? 6
-                                    : streams < 8 ? 0 : 1;
-    const int tiles = (max_kv + kTile - 1) / kTile;
-    return tiles <= per_warp * (warps_of(D) << bits) ? 1 << bits : 0;
 }
 
 template <int D, int NB, bool kOne>

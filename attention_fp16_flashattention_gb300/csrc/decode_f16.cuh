@@ -148,25 +148,30 @@ __device__ __forceinline__ void store_row(float (&out)[D / 32], const float (&ga
     }
 }
 
-// The cached tokens that the call at hand reads of sequence b, and the first entry of its page-table
-// row that they lie in.  kShared: those behind the prefix, whose length (-1: the sequence's or its group's
-// lengths were rejected) the kernel has laid out in shared memory.
-template <bool kShared>
-__device__ __forceinline__ int seq_len(const DecodeF16Args& a, const int* pre, int b) {
-    if constexpr (kShared) return pre[b] < 0 ? 0 : a.kv_lens[b] - pre[b];
+// Which tokens of a sequence decode_f16_body reads.  kWhole: all of them.  kOwn: those behind its group's prefix, whose
+// length (-1: the sequence's or its group's lengths were rejected) the kernel has laid out in shared memory.
+// kFlat: all of the one sequence of a cluster (kOne), the first `prefix` of them in the pages of row `lead`.
+enum Tokens { kWhole, kOwn, kFlat };
+struct FlatSeq {
+    int len, prefix, lead;
+};
+template <Tokens kTokens>
+__device__ __forceinline__ int seq_len(const DecodeF16Args& a, const int* pre, const FlatSeq& flat, int b) {
+    if constexpr (kTokens == kOwn) return pre[b] < 0 ? 0 : a.kv_lens[b] - pre[b];
+    else if constexpr (kTokens == kFlat) return flat.len;
     else return a.kv_lens[b];
 }
 
 // kOne: a cluster takes one stream, its CTAs' warps equal shares of the stream's tiles, and joins the
 // partials in its shared memory: short caches, where the merge kernel would cost more than an uneven
 // split (rule and times at cluster_of).
-// kShared: a part of a larger kernel's CTAs (this one is `cta_id` of `n_ctas`), which has made the tile
-// prefix; no weights, one map.
-template <int D, int NB, bool kOne, bool kShared>
+// kOwn: a part of a larger kernel's CTAs (this one is `cta_id` of `n_ctas`), which has made the tile
+// prefix.  kOwn and kFlat: no weights, one map.
+template <int D, int NB, bool kOne, Tokens kTokens>
 __device__ __forceinline__ void decode_f16_body(const CUtensorMap& tk, const CUtensorMap& tv,
                                                 const DecodeF16Args& a, uint8_t* smem,
-                                                uint32_t* prefix, const int* pre, uint32_t cta_id,
-                                                uint32_t n_ctas) {
+                                                uint32_t* prefix, const int* pre, const FlatSeq& flat,
+                                                uint32_t cta_id, uint32_t n_ctas) {
     using C = Cfg<D>;
     constexpr int R = 8 * NB;
     __shared__ uint32_t warp_sums[C::kWarps];
@@ -174,8 +179,8 @@ __device__ __forceinline__ void decode_f16_body(const CUtensorMap& tk, const CUt
     __shared__ long long s_stream[C::kWarps];  // its stream, -1 for an idle warp
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + C::kRing);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(prefix + kMaxSeqs + 1);
-    const bool scored = !kShared && a.scores;
-    const int maps = kShared ? 1 : a.maps;
+    const bool scored = kTokens == kWhole && a.scores;
+    const int maps = kTokens == kWhole ? a.maps : 1;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int part = warp >> a.side_bits, beside = warp & ((1 << a.side_bits) - 1);
     const int per_seq = a.Hkv * a.sets;
@@ -191,7 +196,7 @@ __device__ __forceinline__ void decode_f16_body(const CUtensorMap& tk, const CUt
         const int stream = static_cast<int>(blockIdx.x) / C_one;
         one.b = stream / per_seq;
         one.sis = stream - one.b * per_seq;
-        const int len = a.kv_lens[one.b];
+        const int len = seq_len<kTokens>(a, pre, flat, one.b);
         if ((len < 0 || len > a.max_kv) && threadIdx.x == 0) atomicOr(a.status, kDevBadLength);
         one.s_end = seq_tiles(len, a.max_kv);
         if (threadIdx.x == 0) {
@@ -200,7 +205,7 @@ __device__ __forceinline__ void decode_f16_body(const CUtensorMap& tk, const CUt
             mbar_init_fence();
         }
         __syncthreads();
-    } else if constexpr (kShared) {
+    } else if constexpr (kTokens == kOwn) {
         if (threadIdx.x == 0) {
             for (int s = 0; s < C::kWarps * C::kStages; ++s) mbar_init(&bars[s], 1);
             *abort_flag = 0;
@@ -243,7 +248,7 @@ __device__ __forceinline__ void decode_f16_body(const CUtensorMap& tk, const CUt
             for (int b = threadIdx.x; b <= a.B; b += C::kThreads) a.prefix_out[b] = prefix[b];
     }
     // The merge grid may start launching now; it waits for this grid to finish.
-    if constexpr (!kOne && !kShared) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (!kOne && kTokens == kWhole) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const uint32_t U = kOne ? one.s_end : prefix[a.B];
     const Split sp = kOne ? Split{static_cast<uint32_t>(C_one), static_cast<uint32_t>(C::kWarps)}
                           : split_of(U, n_ctas, C::kWarps >> a.side_bits);
@@ -274,7 +279,9 @@ __device__ __forceinline__ void decode_f16_body(const CUtensorMap& tk, const CUt
         if (u >= u_end) return 0;
         const TileLoc L = place(u);
         const int tok = L.t * kTile;
-        int page = a.table[static_cast<long long>(L.b) * a.max_pages + (tok + (kShared ? pre[L.b] : 0)) / a.ps];
+        const int row = kTokens == kFlat && tok < flat.prefix ? flat.lead : L.b;
+        int page = a.table[static_cast<long long>(row) * a.max_pages +
+                           (tok + (kTokens == kOwn ? pre[L.b] : 0)) / a.ps];
         const bool bad = page < 0 || page >= a.num_phys;
         if (bad) {
             atomicOr(a.status, kDevBadPage);
@@ -330,7 +337,7 @@ __device__ __forceinline__ void decode_f16_body(const CUtensorMap& tk, const CUt
     int kv_len = 0, lim[NB][2], first_masked = 0;
     // Start of a stream segment: state reset and the Q operand of the stream's rows.
     auto begin_stream = [&]() {
-        kv_len = seq_len<kShared>(a, pre, L.b);
+        kv_len = seq_len<kTokens>(a, pre, flat, L.b);
         const int hk = L.sis / a.sets, rg = ((L.sis - hk * a.sets) << a.side_bits) + beside;
         first_masked = kv_len - a.nq + 1;
 #pragma unroll
@@ -607,7 +614,7 @@ __device__ __forceinline__ void decode_f16_body(const CUtensorMap& tk, const CUt
             if (d == 0) s_rec[r] = make_float2(M, l);
         }
         cluster.sync();
-        if (a.scores) {
+        if (scored) {
             // The weights, by the lanes that hold the scores: every row's joint max and sum, then
             // sum_r 2^(x - max) / sum over the lane's rows and the four lanes of a token.
             __shared__ float2 s_row[R];
@@ -742,9 +749,9 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                ~static_cast<uintptr_t>(1023));
     using C = Cfg<D>;
-    decode_f16_body<D, NB, kOne, false>(tk, tv, a, smem,
-                                        reinterpret_cast<uint32_t*>(smem + C::kRing + C::kBarBytes),
-                                        nullptr, blockIdx.x, gridDim.x);
+    decode_f16_body<D, NB, kOne, kWhole>(tk, tv, a, smem,
+                                         reinterpret_cast<uint32_t*>(smem + C::kRing + C::kBarBytes),
+                                         nullptr, FlatSeq{}, blockIdx.x, gridDim.x);
 }
 
 // Joins the partial records of every query row: with m_r, l_r the reference (log2
@@ -1136,6 +1143,64 @@ inline Layout decode_layout(long long ctas, int B, int Hkv, int G, int max_kv, i
 inline int sm_count_or_default() {
     DeviceState d;
     return current_device(&d) == GBATTN_OK ? d.num_sms : 152;
+}
+
+// How many clusters of 1, 2, 4 and 8 CTAs of the one-kernel form run at once on a device: a CTA takes an SM,
+// and a cluster's SMs lie in one GPC (152 SMs hold 152, 76, 36 and 15).  null: the device refused.
+template <int D, int NB, auto* kernel>
+const int* resident_clusters(int device) {
+    static std::once_flag once[64];
+    static int n[64][4];
+    static bool ok[64];
+    if (device < 0 || device >= 64) return nullptr;
+    std::call_once(once[device], [&] {
+        ok[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                          Cfg<D>::kSmem) == cudaSuccess;
+        for (int i = 0; i < 4 && ok[device]; ++i) {
+            cudaLaunchConfig_t cfg{};
+            cfg.gridDim = dim3(1u << i);
+            cfg.blockDim = dim3(Cfg<D>::kThreads);
+            cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << i;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            ok[device] = cudaOccupancyMaxActiveClusters(&n[device][i], kernel, &cfg) == cudaSuccess;
+        }
+        if (!ok[device]) cudaGetLastError();
+    });
+    return ok[device] ? n[device] : nullptr;
+}
+// CTAs of a cluster when every stream gets one (kOne), 0 when the streams' tiles are laid end to end.  A
+// cluster saves the merge kernel, the tile prefix and the records' way through memory, but its SMs read
+// one stream only, whatever the others' lengths, and its warps add the weights of their own tiles one
+// after the other.  So where all clusters run at once, the largest that do, and max_kv_len gives a warp
+// at most `per_warp` tiles.  Measured, clusters against laid end to end, in us (streams: sequences with
+// one KV head of four rows, one length unless said):
+//   D = 128   1 stream 4,096 tokens 9.7 and 11.1, 8,192 11.9 and 11.2; 15 streams 6,144 13.0 and 16.1; 32
+//             of half to all of 2,048 9.7 and 13.7; 152 of half to all of 768 11.8 and 17.0
+//   D = 64    1 stream 8,192 9.9 and 10.8, 12,288 12.1 and 11.1; 8 streams 12,288 12.1 and 13.1; 152 of
+//             half to all of 1,536 13.2 and 18.5
+//   D = 256   1 stream 512 8.8 and 8.2; 8 streams 8.9 and 9.5; 15 streams 9.4 and 10.3
+//   weights   D = 128: 8 streams 2,048 11.1 and 12.1, 4,096 13.8 and 12.8; 15 of 6,144 6% less, 8 tiles a
+//             warp no gain; 152 of half to all of 768 16.4 and 19.3, of 1,536 27.3 and 25.8.  D = 64 alike.
+//             D = 256: 1 stream 512 10.6 and 10.7, 8 streams 11.0 and 11.9
+// With clusters of eight for up to 19 streams (152 SMs, of which 15 such clusters fit) 16 streams of half to
+// all of 512 took 13.2 us, in two waves; end to end takes 10.1, clusters of four 7.2.
+inline int cluster_of(long long streams, int max_kv, int D, bool weights, const int* resident) {
+    static_assert(kMaxCluster == 8, "resident_clusters asks for up to eight CTAs");
+    int bits = 3;
+    while (bits > 0 && streams > resident[bits]) --bits;
+    if (streams > resident[bits]) return 0;
+    const int per_warp = weights    ? D == 256 ? 1 : streams < 12 ? 2 : 6
+                         : D == 64  ? streams < 8 ? 8 : 12
+                         : D == 128 ? 6
+                                    : streams < 8 ? 0 : 1;
+    const int tiles = (max_kv + kTile - 1) / kTile;
+    return tiles <= per_warp * (warps_of(D) << bits) ? 1 << bits : 0;
 }
 
 // A launch whose CTAs may be placed while the grid before it on the stream still

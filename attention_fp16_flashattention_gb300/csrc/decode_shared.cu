@@ -30,10 +30,10 @@
 // take of the shared memory hold another tile under way.
 //
 // Measured (graph replays): 64 sequences behind 16,384 tokens with 100 to 2,001 of their own, 32 on 8 heads of 128
-// (351 MB; 67 of them the prefix) 72 to 76 us, where an ordinary decode reads 4.6 GB; 8 behind 131,072 (32 rows a
+// (351 MB; 67 of them the prefix) 72 to 76 us, where the ordinary decode, to which that is 4.6 GB, takes 345; 8 behind 131,072 (32 rows a
 // KV head) 91.5 us, 0.86 of the measured copy; 64 behind as many (256 rows) 147 us, 490 TFLOP/s without the lo
-// halves, a step of 128 rows and 64 tokens in 1,030 cycles of which the tensor pipe has 900 to do; 8 behind 1,024 14.5 us,
-// latency of the lengths, the first tile, the records and the merge behind each other.
+// halves, a step of 128 rows and 64 tokens in 1,030 cycles of which the tensor pipe has 900 to do.  8 behind 1,024 with
+// up to 300 of their own in the form for short caches 10.7 us (the ordinary decode 10.5).
 //
 // Every wait is bounded in time (WaitCtl): one that runs out records GBATTN_DEV_WAIT_TIMEOUT, the CTA stops,
 // waits a bounded time for its copies and MMAs in flight, frees tensor memory and exits.
@@ -788,7 +788,7 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
     for (int b = b0; b < b1; ++b) {
         tiles[b] = run;
         if (blockIdx.x == P) d.prefix_out[b] = run;
-        run += seq_tiles(seq_len<true>(d, pre, b), a.max_own) * static_cast<uint32_t>(per_seq);
+        run += seq_tiles(seq_len<kOwn>(d, pre, FlatSeq{}, b), a.max_own) * static_cast<uint32_t>(per_seq);
     }
     if (tid == 0) {
         tiles[d.B] = own;
@@ -796,7 +796,52 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
     }
     __syncthreads();
     if (tid >= Cfg<D>::kThreads) return;
-    decode_f16_body<D, NB, false, true>(tk, tv, d, smem, tiles, pre, blockIdx.x - P, gridDim.x - P);
+    decode_f16_body<D, NB, false, kOwn>(tk, tv, d, smem, tiles, pre, FlatSeq{}, blockIdx.x - P, gridDim.x - P);
+}
+
+// Short caches: clusters as in the FP16 decode's short form, one for each stream, which read the prefix for each
+// sequence; the rule is that form's (cluster_of), for the longest prefix and own part together.  8 sequences behind
+// 1,024 tokens: 10.7 us, where two kinds of CTAs and a merge take 14.5.
+template <int D, int NB>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+    decode_shared_flat_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv,
+                              const SharedArgs a) {
+    using C = Cfg<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                               ~static_cast<uintptr_t>(1023));
+    const DecodeF16Args& d = a.dec;
+    const bool lead = blockIdx.x == 0;
+    const int b = static_cast<int>(blockIdx.x / cg::this_cluster().num_blocks()) / (d.Hkv * d.sets);
+    const int n = d.kv_lens[b];
+    bool order = true;
+    for (int g = threadIdx.x; g < a.groups; g += C::kThreads) {
+        const int s = a.starts[g], e = a.starts[g + 1];
+        order = order && s >= 0 && s <= e && e <= d.B && (g > 0 || s == 0) && (g + 1 < a.groups || e == d.B);
+        if (lead) {
+            const int p = a.prefix_lens[g];
+            if (p < 0 || p > a.max_prefix || p % d.ps != 0) atomicOr(d.status, kDevBadLength);
+        }
+    }
+    order = __syncthreads_and(order);
+    FlatSeq flat{0, 0, b};
+    if (order) {
+        int g = 0, hi = a.groups - 1;   // the last group that begins at or before b
+        while (g < hi) {
+            const int mid = (g + hi + 1) >> 1;
+            if (a.starts[mid] <= b) g = mid; else hi = mid - 1;
+        }
+        const int p = a.prefix_lens[g];
+        if (p >= 0 && p <= a.max_prefix && p % d.ps == 0) {
+            if (n >= p && n - p <= a.max_own && n <= a.cap) flat = FlatSeq{n, p, a.starts[g]};
+            else if (threadIdx.x == 0) atomicOr(d.status, kDevBadLength);
+        }
+    } else if (lead && threadIdx.x == 0) {
+        atomicOr(d.status, kDevBadIndex);
+    }
+    decode_f16_body<D, NB, true, kFlat>(tk, tv, d, smem,
+                                        reinterpret_cast<uint32_t*>(smem + C::kRing + C::kBarBytes), nullptr,
+                                        flat, blockIdx.x, gridDim.x);
 }
 
 // Workspace: the own tokens' records and tile prefix (decode_layout), then the prefixes' records, a unit's rows a
@@ -842,6 +887,41 @@ int launch_shared(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMa
     if (rc[device] != GBATTN_OK) return rc[device];
     kernel<<<ctas, Pre<D>::kThreads, Smem<D>::kBytes, s>>>(tk, tv, pk, pv, a);
     count_launches(1);
+    return launch_status();
+}
+
+// The short form, where its rule takes it: `launched` says whether.
+template <int D, int NB>
+int launch_flat(const CUtensorMap& tk, const CUtensorMap& tv, long long streams, int device, const SharedArgs& a,
+                cudaStream_t s, bool& launched) {
+    launched = false;
+    const long long most = static_cast<long long>(a.max_prefix) + a.max_own;
+    if (most > (1 << 30)) return GBATTN_OK;
+    const int* resident = resident_clusters<D, NB, decode_shared_flat_kernel<D, NB>>(device);
+    if (!resident) return GBATTN_ERR_CUDA;
+    const int cl = cluster_of(streams, static_cast<int>(most), D, false, resident);
+    if (cl == 0) return GBATTN_OK;
+    launched = true;
+    SharedArgs f = a;
+    f.dec.max_kv = static_cast<int>(most);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(streams * cl));
+    cfg.blockDim = dim3(Cfg<D>::kThreads);
+    cfg.dynamicSmemBytes = Cfg<D>::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(cl);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, decode_shared_flat_kernel<D, NB>, tk, tv, f);
+    count_launches(1);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return GBATTN_ERR_CUDA;
+    }
     return launch_status();
 }
 
@@ -930,9 +1010,7 @@ extern "C" int attn_paged_decode_shared_f16_fwd(const void* q, const void* k_pag
     CUtensorMap tk, tv, pk, pv;
     const uint64_t total_rows = static_cast<uint64_t>(num_phys_pages) * page_size;
     if (encode_tmap_f16_pages(&tk, k_pages, D, Hkv, total_rows, kTile) != GBATTN_OK ||
-        encode_tmap_f16_pages(&tv, v_pages, D, Hkv, total_rows, kTile) != GBATTN_OK ||
-        encode_tmap_f16_pages(&pk, k_pages, D, Hkv, total_rows, a.box_rows) != GBATTN_OK ||
-        encode_tmap_f16_pages(&pv, v_pages, D, Hkv, total_rows, a.box_rows) != GBATTN_OK)
+        encode_tmap_f16_pages(&tv, v_pages, D, Hkv, total_rows, kTile) != GBATTN_OK)
         return GBATTN_ERR_CUDA;
     uint8_t* wsp = static_cast<uint8_t*>(workspace);
     DecodeF16Args& d = a.dec;
@@ -973,6 +1051,18 @@ extern "C" int attn_paged_decode_shared_f16_fwd(const void* q, const void* k_pag
     a.max_own = max_own_len;
     a.cap = slots_row < 0x7FFFFFFFLL ? static_cast<int>(slots_row) : 0x7FFFFFFF;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (plan.side == 1) {   // short caches (row groups as streams of their own read the cache again, as there)
+        bool launched = false;
+        auto flat = [&](auto launch) { return launch(tk, tv, streams, dev.device, a, s, launched); };
+        if (R == 8)
+            rc = D == 64 ? flat(launch_flat<64, 1>) : D == 128 ? flat(launch_flat<128, 1>) : flat(launch_flat<256, 1>);
+        else
+            rc = D == 64 ? flat(launch_flat<64, 2>) : D == 128 ? flat(launch_flat<128, 2>) : flat(launch_flat<256, 2>);
+        if (rc != GBATTN_OK || launched) return rc;
+    }
+    if (encode_tmap_f16_pages(&pk, k_pages, D, Hkv, total_rows, a.box_rows) != GBATTN_OK ||
+        encode_tmap_f16_pages(&pv, v_pages, D, Hkv, total_rows, a.box_rows) != GBATTN_OK)
+        return GBATTN_ERR_CUDA;
     const int n = static_cast<int>(ctas);
     auto go = [&](auto launch) { return launch(tk, tv, pk, pv, n, dev.device, a, s); };
     if (R == 8)
