@@ -720,7 +720,7 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
         sum += n;
     }
     order = __syncthreads_and(order);
-    if (order && longest > 0) {
+    if (order && shortest <= longest) {   // (a group of unlike units has 0 for its length: neither may be left out)
         atomicMin(&s_shortest, shortest);
         atomicMax(&s_longest, longest);
     }
