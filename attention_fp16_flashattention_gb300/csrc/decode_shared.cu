@@ -1092,9 +1092,11 @@ extern "C" int attn_paged_decode_shared_f16_fwd(const void* q, const void* k_pag
                           groups, max_prefix_len, page_size, a.cap};
     // Warps per row by the records of an average row, of either kind, as long as all of them fit the GPU at once:
     // every warp places its row's records by itself (1024 rows 29.4 us with two warps, 33.0 with four; 512 rows 38.8
-    // and 35.8; 2048 rows 73.5 with one, 77.9 with two).
+    // and 35.8; 2048 rows 73.5 with one, 77.9 with two).  Eight records a warp are one trip to L2: 16 warps instead of
+    // eight for 152 records took 5 sequences behind 196,608 tokens of one KV head from 49.6 to 47.4 us, 16 behind 65,536 at
+    // D = 64 from 24.9 to 22.3; eight instead of four for 31 records, six groups behind 16,384, from 21.6 to 20.7.
     const long long recs = ctas * plan.side / streams + ctas / (units < 1 ? 1 : units) + 2;
-    int mw = recs > 32 ? 8 : recs > 8 ? 4 : 1;
+    int mw = recs > 64 ? 16 : recs > 16 ? 8 : recs > 8 ? 4 : 1;
     while (mw > 1 && rows * mw > 2048) mw /= 2;
     const dim3 mgrid(static_cast<unsigned>(rows));
     const size_t msmem = static_cast<size_t>(mw) * (D * sizeof(float) + sizeof(float2));
