@@ -845,7 +845,9 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
     decode_f16_merge_kernel(const MergeArgs a) {
     constexpr int V = D / 32;
     constexpr int kMaps = kDiff ? 2 : 1;
-    constexpr int kBatch = 8;
+    // Records under way in a warp.  (Shared, D = 64: 12, 2 to 3 us less than 8, 32 sequences behind 65,536 tokens 36.3 of 39.7 us;
+    // at D = 128 and 256 the registers of 10 or 12 cost as much and more.)
+    constexpr int kBatch = kShared && D == 64 ? 12 : 8;
     // Sized by the launch, so that as many CTAs as can be wait beside the decode's: with this and the early
     // sums below a call of 16 sequences to 16,001 went from 54.2 to 52.5 us, 4 to 131,072 from 76.5 to 75.5.
     extern __shared__ float s_merge[];   // [warps][D] O, then [warps] (max, sum)
