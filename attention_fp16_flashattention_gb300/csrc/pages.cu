@@ -15,7 +15,8 @@
 // Bound by latency: the lengths, the stack's or the table's entries and the stores, one
 // behind the other; 8 bytes a token and 8 a page are nothing beside that.  Measured (graph replays): one
 // token for 64 sequences 4.0 us, 32 prompts of 131,000 tokens 4.6, drafted tokens of 64 sequences back 4.0,
-// 100,000 pages back 14.0 (eight SMs look at each of them; with 1024 threads a CTA 9.7, but 5.0 for the few).
+// 100,000 pages back 7.3, 262,000 27 (a cluster of 16 CTAs looks at each of them; of eight 13.8 and 56, with 1024 threads
+// a CTA 9.5 and 34, but then 4.9 for the few).
 #include <cooperative_groups.h>
 
 #include <mutex>
@@ -31,7 +32,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSeqs = 4096;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 16;
 constexpr int kUnroll = 4;   // tokens (or pages) a thread has under way at once
 
 __device__ __forceinline__ int sat_add(int a, int b) {   // of counts >= 0
@@ -333,18 +334,40 @@ __global__ void __launch_bounds__(kThreads) kv_release_kernel(const TableArgs a)
     }
 }
 
-// Shared memory above the default: asked for once per device.
-template <typename Kernel>
-int set_smem(Kernel* kernel, int device, std::once_flag* once, int* rc) {
+// What a device allows a kernel, asked for once: shared memory above the default, and clusters of 16 CTAs, which need
+// a GPC with as many SMs, or of eight, which every one has.
+struct Allowed {
+    std::once_flag once;
+    int rc, cluster;
+};
+int allow(void (*kernel)(TableArgs), int device, Allowed* all, int& cluster) {
     if (device < 0 || device >= 64) return GBATTN_ERR_CUDA;
-    std::call_once(once[device], [&] {
-        rc[device] = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                          4 * kMaxSeqs * static_cast<int>(sizeof(int))) == cudaSuccess
-                         ? GBATTN_OK
-                         : GBATTN_ERR_CUDA;
-        if (rc[device] != GBATTN_OK) cudaGetLastError();
+    Allowed& d = all[device];
+    std::call_once(d.once, [&] {
+        constexpr int kSmem = 4 * kMaxSeqs * static_cast<int>(sizeof(int));
+        d.cluster = 8;
+        d.rc = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess
+                   ? GBATTN_OK
+                   : GBATTN_ERR_CUDA;
+        cudaLaunchConfig_t cfg{};
+        cfg.gridDim = dim3(kMaxCluster);
+        cfg.blockDim = dim3(kThreads);
+        cfg.dynamicSmemBytes = kSmem;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = kMaxCluster;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        int n = 0;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) == cudaSuccess && n > 0)
+            d.cluster = kMaxCluster;
+        cudaGetLastError();
     });
-    return rc[device];
+    cluster = d.cluster;
+    return d.rc;
 }
 
 int launch(void (*kernel)(TableArgs), int ctas, int cluster, size_t smem, cudaStream_t s,
@@ -456,12 +479,12 @@ extern "C" int kv_paged_extend(int32_t* page_table, const int32_t* kv_lens, cons
     a.row_tokens = row_tokens;
     a.max_tokens = slots ? max_tokens : 0;
     a.in_place = same_lens || same_count;
-    static std::once_flag once[64];
-    static int attr_rc[64];
-    rc = set_smem(kv_extend_kernel, dev.device, once, attr_rc);
+    static Allowed allowed[64];
+    int cluster = 0;
+    rc = allow(kv_extend_kernel, dev.device, allowed, cluster);
     if (rc != GBATTN_OK) return rc;
     const int ctas = ctas_for(max_tokens > B ? max_tokens : B, kThreads * kUnroll,
-                              a.in_place ? kMaxCluster : 128);
+                              a.in_place ? cluster : 128);
     return launch(kv_extend_kernel, ctas, a.in_place ? ctas : 1, 4 * b4,
                   static_cast<cudaStream_t>(stream), a);
 }
@@ -502,11 +525,11 @@ extern "C" int kv_paged_release(const int32_t* page_table, const int32_t* kv_len
     a.page_bits = page_bits_of(page_size);
     a.num_phys = num_phys_pages;
     a.capacity = capacity;
-    static std::once_flag once[64];
-    static int attr_rc[64];
-    rc = set_smem(kv_release_kernel, dev.device, once, attr_rc);
+    static Allowed allowed[64];
+    int cluster = 0;
+    rc = allow(kv_release_kernel, dev.device, allowed, cluster);
     if (rc != GBATTN_OK) return rc;
     // how many pages go is known on the device only; the table's size bounds it
-    const int ctas = ctas_for(static_cast<long long>(B) * max_pages, kThreads * kUnroll, kMaxCluster);
+    const int ctas = ctas_for(static_cast<long long>(B) * max_pages, kThreads * kUnroll, cluster);
     return launch(kv_release_kernel, ctas, ctas, 3 * b4, static_cast<cudaStream_t>(stream), a);
 }

@@ -195,6 +195,29 @@ def test_lengths_as_two_arguments(gb):
         gb.kv_paged_extend(gt, gl, gl, gp, gc, 16, P, kv_lens_out=gl)
 
 
+@pytest.mark.parametrize("B,width", [(300, 600), (33, 8000)])
+def test_bad_pages_among_very_many(gb, B, width):
+    """More pages than the cluster keeps in registers at once: sequences with a bad one, first or last looked at, keep
+    all of theirs."""
+    rng = np.random.default_rng(B)
+    P = B * width
+    table = rng.permutation(P).astype(np.int32).reshape(B, width)
+    lens = rng.integers(0, 16 * width + 1, B)
+    lens[[0, 5, B - 1]] = 16 * width
+    bad = sorted({0, 5, B - 1, *rng.integers(0, B, 4).tolist()})
+    for b in bad:
+        held = -(-int(lens[b]) // 16)
+        if held:
+            table[b, rng.choice([0, held - 1, held // 2])] = rng.choice([-1, P, 2 ** 31 - 1])
+    count, pages = t(np.array([3], np.int32)), t(np.full(P + 5, 77, np.int32))
+    out = gb.kv_paged_release(t(table), t(lens.astype(np.int32)), pages, count, 16, P)
+    assert gb.device_status() == gb.DEV_BAD_PAGE
+    want = np.concatenate([table[b, :-(-int(lens[b]) // 16)] for b in range(B) if b not in bad])
+    got = pages.cpu().numpy()
+    assert out.item() == 3 + len(want) and np.array_equal(got[3:3 + len(want)], want)
+    assert (got[:3] == 77).all() and (got[3 + len(want):] == 77).all()
+
+
 # ---------------------------------------------------------------- rotary positions
 
 @pytest.mark.parametrize("D,rot,inter", [(64, 24, False), (128, 128, True), (256, 72, False)])
