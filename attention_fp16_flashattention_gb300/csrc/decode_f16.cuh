@@ -795,7 +795,9 @@ __device__ __forceinline__ uint32_t unit_steps(int rows, uint32_t tiles) {
 
 // How the prefixes' `pre` steps are shared when the others of `grid` CTAs work on `own` tiles of kTile tokens:
 // `ctas` of them take equal ranges of `total` steps (>= pre, the last may be short).  How many, by what a step costs
-// (in halves of an own tile; measured where both kinds end together), and such that ranges and units begin together
+// (in halves of an own tile of R = 8 or 16 rows; measured over batches of 8 to 128 sequences: at D = 64 12 and 10 took 0 to
+// 20% less than 16 for both, at D = 128 8 for R = 16 3 to 9% less than 10, at D = 256 8 for R = 8 8% less than 5 in the
+// mean), and such that ranges and units begin together
 // where that can be had: with units of one length (`unit` steps, else 0) the same number of CTAs for each, else
 // the same whole number of steps (with few an even one where two sets of warps take them in turn).  A second unit
 // in a range costs O out and Q in, which pass the SM's port to memory beside the caches' stream (64 sequences behind
@@ -805,10 +807,10 @@ struct PreSplit {
     uint32_t ctas, total;
 };
 template <int D>
-__device__ __forceinline__ PreSplit prefix_split(uint32_t grid, uint32_t pre, uint32_t own, uint32_t unit) {
+__device__ __forceinline__ PreSplit prefix_split(uint32_t grid, uint32_t pre, uint32_t own, uint32_t unit, int R) {
     if (pre == 0) return PreSplit{0, 0};
-    constexpr uint32_t kCost = D == 256 ? 5 : D == 128 ? 10 : 16;
-    const unsigned long long w = static_cast<unsigned long long>(kCost) * pre, all = w + 2ull * own;
+    const uint32_t cost = R == 8 ? (D == 256 ? 8 : D == 128 ? 10 : 12) : (D == 256 ? 5 : D == 128 ? 8 : 10);
+    const unsigned long long w = static_cast<unsigned long long>(cost) * pre, all = w + 2ull * own;
     const uint32_t most = own > 0 ? grid - 1 : grid;
     uint32_t n = static_cast<uint32_t>((w * grid + all / 2) / all);
     n = min(max(n, 1u), most);
@@ -956,7 +958,7 @@ __global__ void __launch_bounds__(32 * kMergeMaxWarps)
             row_good = __all_sync(0xffffffffu, row_good);
             shortest = __reduce_min_sync(0xffffffffu, shortest);
             longest = __reduce_max_sync(0xffffffffu, longest);
-            const PreSplit ps = prefix_split<D>(a.grid, Up, U, shortest == longest ? longest : 0u);
+            const PreSplit ps = prefix_split<D>(a.grid, Up, U, shortest == longest ? longest : 0u, a.R);
             grid -= ps.ctas;
             if (row_good && prefix > 0) place_prefix(prefix, first, next, work, ps);
         }

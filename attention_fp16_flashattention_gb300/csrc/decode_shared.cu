@@ -772,7 +772,7 @@ __global__ void __launch_bounds__(Pre<D>::kThreads, 1)
     run = block_sum<kThreads>(sum, own);   // (its barriers also make `tiles` and `pre` whole)
     // The merge grid may start launching now; it waits for this grid to finish.
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const PreSplit split = prefix_split<D>(gridDim.x, Up, own, s_shortest == s_longest ? s_longest : 0u);
+    const PreSplit split = prefix_split<D>(gridDim.x, Up, own, s_shortest == s_longest ? s_longest : 0u, 8 * NB);
     const uint32_t P = split.ctas;
     if (lead && tid == 0) {
         a.total_out[0] = own;
