@@ -30,8 +30,8 @@
 // take of the shared memory hold another tile under way.
 //
 // Measured (graph replays): 64 sequences behind 16,384 tokens with 100 to 2,001 of their own, 32 on 8 heads of 128
-// (351 MB; 67 of them the prefix) 72 to 76 us, where the ordinary decode, to which that is 4.6 GB, takes 345; 8 behind 131,072 (32 rows a
-// KV head) 91.5 us, 0.86 of the measured copy; 64 behind as many (256 rows) 147 us, 490 TFLOP/s without the lo
+// (351 MB; 67 of them the prefix) 71 to 76 us, where the ordinary decode, to which that is 4.6 GB, takes 345; at D = 64 48;
+// 8 behind 131,072 (32 rows a KV head) 91 us, 0.87 of the measured copy; 64 behind as many (256 rows) 147 us, 490 TFLOP/s without the lo
 // halves, a step of 128 rows and 64 tokens in 1,030 cycles of which the tensor pipe has 900 to do.  8 behind 1,024 with
 // up to 300 of their own in the form for short caches 10.7 us (the ordinary decode 10.5).
 //
