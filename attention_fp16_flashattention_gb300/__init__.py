@@ -437,6 +437,18 @@ def _need_on(t, name, dtype, ndim, dev):
     _same_device(t)
 
 
+def _need_is(t, name, dtype, shape, dev):
+    """_need_on and _need_shape (a tuple) in one."""
+    try:
+        if (t.dtype is dtype and t.shape == shape and t.get_device() == dev
+                and t.is_contiguous()):
+            return
+    except AttributeError:
+        pass
+    _need_on(t, name, dtype, len(shape), dev)
+    _need_shape(t, name, shape)
+
+
 def _need_view_on(t, name, dtype, dev):
     """_need_view, and on the current device `dev`."""
     try:
@@ -462,6 +474,14 @@ def _new_tensor(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _maker(stream):
+    """_new_tensor for `stream`, called as torch.empty, which it is without one."""
+    import torch
+    if stream is None:
+        return torch.empty
+    return lambda shape, dtype, device: _new_tensor(shape, dtype, device, stream)
 
 
 def _new_like(t, stream):
@@ -606,20 +626,17 @@ def attn_paged_decode_shared_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, g
     _need_on(q, "q", torch.float16, 4, dev)
     B, Hq, nq, D = q.shape
     P, ps, Hkv, max_pages = _need_paged_f16(k_pages, v_pages, page_table, kv_lens, B, None, D, dev)
-    _need_on(group_starts, "group_starts", torch.int32, 1, dev)
     _need_on(prefix_lens, "prefix_lens", torch.int32, 1, dev)
     groups = prefix_lens.shape[0]
-    _need_shape(group_starts, "group_starts", (groups + 1,))
+    _need_is(group_starts, "group_starts", torch.int32, (groups + 1,), dev)
     max_prefix_len = _int32(max_pages * ps if max_prefix_len is None else max_prefix_len, "max_prefix_len")
     max_own_len = _int32(max_pages * ps if max_own_len is None else max_own_len, "max_own_len")
     if o is None:
         o = _new_like(q, stream)
     else:
-        _need_on(o, "o", torch.float16, 4, dev)
-        _need_shape(o, "o", q.shape)
+        _need_is(o, "o", torch.float16, q.shape, dev)
     if lse is not None:
-        _need_on(lse, "lse", torch.float32, 3, dev)
-        _need_shape(lse, "lse", (B, Hq, nq))
+        _need_is(lse, "lse", torch.float32, (B, Hq, nq), dev)
     if workspace is None:
         workspace = _scratch(attn_paged_decode_shared_f16_workspace_size(
             B, Hq, Hkv, nq, groups, max_prefix_len, max_own_len, D), q.device, stream)
@@ -789,12 +806,10 @@ def _need_tables(page_table, kv_lens, free_pages, free_count, cur):
     """Checks what the page-table calls share; returns (B, max_pages, capacity)."""
     import torch
     _need_on(page_table, "page_table", torch.int32, 2, cur)
-    _need_on(kv_lens, "kv_lens", torch.int32, 1, cur)
     _need_on(free_pages, "free_pages", torch.int32, 1, cur)
-    _need_on(free_count, "free_count", torch.int32, 1, cur)
     B, max_pages = page_table.shape
-    _need_shape(kv_lens, "kv_lens", (B,))
-    _need_shape(free_count, "free_count", (1,))
+    _need_is(kv_lens, "kv_lens", torch.int32, (B,), cur)
+    _need_is(free_count, "free_count", torch.int32, (1,), cur)
     return B, max_pages, free_pages.shape[0]
 
 
@@ -813,8 +828,7 @@ def kv_paged_extend(page_table, kv_lens, new_lens, free_pages, free_count, page_
     import torch
     cur = _current_device(page_table, "page_table")
     B, max_pages, capacity = _need_tables(page_table, kv_lens, free_pages, free_count, cur)
-    _need_on(new_lens, "new_lens", torch.int32, 1, cur)
-    _need_shape(new_lens, "new_lens", (B,))
+    _need_is(new_lens, "new_lens", torch.int32, (B,), cur)
     page_size, num_phys_pages = _int32(page_size, "page_size"), _int32(num_phys_pages, "num_phys_pages")
     if max_tokens is not None and row_tokens is not None:
         raise ValueError("max_tokens and row_tokens exclude each other")
@@ -828,33 +842,28 @@ def kv_paged_extend(page_table, kv_lens, new_lens, free_pages, free_count, page_
     if n == 0 and not (token_starts is None and positions is None and slots is None):
         raise ValueError("token_starts, positions and slots need max_tokens or row_tokens")
     # Five tensors are quicker to make than five views of one (20 and 25 us a call).
-    dev, shape = page_table.device, (B, rows) if rows else (n,)
+    dev, shape, new = page_table.device, (B, rows) if rows else (n,), _maker(stream)
     if kv_lens_out is None:
-        kv_lens_out = _new_tensor((B,), torch.int32, dev, stream)
+        kv_lens_out = new((B,), dtype=torch.int32, device=dev)
     else:
-        _need_on(kv_lens_out, "kv_lens_out", torch.int32, 1, cur)
-        _need_shape(kv_lens_out, "kv_lens_out", (B,))
+        _need_is(kv_lens_out, "kv_lens_out", torch.int32, (B,), cur)
     if free_count_out is None:
-        free_count_out = _new_tensor((1,), torch.int32, dev, stream)
+        free_count_out = new((1,), dtype=torch.int32, device=dev)
     else:
-        _need_on(free_count_out, "free_count_out", torch.int32, 1, cur)
-        _need_shape(free_count_out, "free_count_out", (1,))
+        _need_is(free_count_out, "free_count_out", torch.int32, (1,), cur)
     if n:
         if token_starts is None:
-            token_starts = _new_tensor((B + 1,), torch.int32, dev, stream)
+            token_starts = new((B + 1,), dtype=torch.int32, device=dev)
         else:
-            _need_on(token_starts, "token_starts", torch.int32, 1, cur)
-            _need_shape(token_starts, "token_starts", (B + 1,))
+            _need_is(token_starts, "token_starts", torch.int32, (B + 1,), cur)
         if positions is None:
-            positions = _new_tensor(shape, torch.int32, dev, stream)
+            positions = new(shape, dtype=torch.int32, device=dev)
         else:
-            _need_on(positions, "positions", torch.int32, len(shape), cur)
-            _need_shape(positions, "positions", shape)
+            _need_is(positions, "positions", torch.int32, shape, cur)
         if slots is None:
-            slots = _new_tensor(shape, torch.int32, dev, stream)
+            slots = new(shape, dtype=torch.int32, device=dev)
         else:
-            _need_on(slots, "slots", torch.int32, len(shape), cur)
-            _need_shape(slots, "slots", shape)
+            _need_is(slots, "slots", torch.int32, shape, cur)
     rc = load().kv_paged_extend(page_table.data_ptr(), kv_lens.data_ptr(), new_lens.data_ptr(),
                                 free_pages.data_ptr(), free_count.data_ptr(), kv_lens_out.data_ptr(),
                                 free_count_out.data_ptr(), _ptr(token_starts), _ptr(positions),
@@ -873,13 +882,11 @@ def kv_paged_release(page_table, kv_lens, free_pages, free_count, page_size, num
     cur = _current_device(page_table, "page_table")
     B, max_pages, capacity = _need_tables(page_table, kv_lens, free_pages, free_count, cur)
     if keep_lens is not None:
-        _need_on(keep_lens, "keep_lens", torch.int32, 1, cur)
-        _need_shape(keep_lens, "keep_lens", (B,))
+        _need_is(keep_lens, "keep_lens", torch.int32, (B,), cur)
     if free_count_out is None:
-        free_count_out = _new_tensor((1,), torch.int32, page_table.device, stream)
+        free_count_out = _maker(stream)((1,), dtype=torch.int32, device=page_table.device)
     else:
-        _need_on(free_count_out, "free_count_out", torch.int32, 1, cur)
-        _need_shape(free_count_out, "free_count_out", (1,))
+        _need_is(free_count_out, "free_count_out", torch.int32, (1,), cur)
     rc = load().kv_paged_release(page_table.data_ptr(), kv_lens.data_ptr(), _ptr(keep_lens),
                                  free_pages.data_ptr(), free_count.data_ptr(),
                                  free_count_out.data_ptr(), B, max_pages,
@@ -946,14 +953,15 @@ def _need_rope(positions, freqs, q_weight, k_weight, sections, B, S, D, dev):
         rot = 2 * freqs.shape[0]
     axes = 1
     if positions is not None:
-        dims = positions.dim() if isinstance(positions, torch.Tensor) else 0
-        _need_on(positions, "positions", torch.int32, 3 if dims == 3 else 2, dev)
-        axes = positions.shape[0] if dims == 3 else 1
-        _need_shape(positions, "positions", (axes, B, S) if dims == 3 else (B, S))
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _need_on(t, name, torch.float32, 1, dev)
-            _need_shape(t, name, (D,))
+        shape = (B, S)
+        if isinstance(positions, torch.Tensor) and positions.dim() == 3:
+            axes = positions.shape[0]
+            shape = (axes, B, S)
+        _need_is(positions, "positions", torch.int32, shape, dev)
+    if q_weight is not None:
+        _need_is(q_weight, "q_weight", torch.float32, (D,), dev)
+    if k_weight is not None:
+        _need_is(k_weight, "k_weight", torch.float32, (D,), dev)
     c_sections = None
     if sections is not None:
         sections = [_int32(n, "sections") for n in sections]
@@ -983,14 +991,14 @@ def qk_norm_rope_f16(q, k, positions, freqs, q_weight=None, k_weight=None, eps=1
         Hk = k.shape[1]
         _need_shape(k, "k", (B, Hk, S, D))
         if k_out is None:
-            k_out = _new_tensor((B, Hk, S, D), torch.float16, q.device, stream)
+            k_out = _maker(stream)((B, Hk, S, D), dtype=torch.float16, device=q.device)
         else:
             _need_view_on(k_out, "k_out", torch.float16, dev)
             _need_shape(k_out, "k_out", (B, Hk, S, D))
     elif k_out is not None:
         raise ValueError("k_out without k")
     if q_out is None:
-        q_out = _new_tensor((B, Hq, S, D), torch.float16, q.device, stream)
+        q_out = _maker(stream)((B, Hq, S, D), dtype=torch.float16, device=q.device)
     else:
         _need_view_on(q_out, "q_out", torch.float16, dev)
         _need_shape(q_out, "q_out", (B, Hq, S, D))
@@ -1023,20 +1031,18 @@ def kv_paged_rope_append(q, k_new, v_new, slots, k_pages, v_pages, positions, fr
     if v_new.shape != k_new.shape or not _same_layout(k_new, v_new):
         raise ValueError("k_new and v_new must have the same shape and strides")
     rot, axes, c_sections = _need_rope(positions, freqs, q_weight, k_weight, sections, B, S, D, dev)
-    _need_on(slots, "slots", torch.int32, 2, dev)
-    _need_shape(slots, "slots", (B, S))
+    _need_is(slots, "slots", torch.int32, (B, S), dev)
     if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in (torch.float16, torch.uint8):
         raise ValueError("k_pages must be a float16 or uint8 tensor")
-    _need_on(k_pages, "k_pages", k_pages.dtype, 4, dev)
-    _need_on(v_pages, "v_pages", k_pages.dtype, 4, dev)
+    dtype = k_pages.dtype
+    _need_on(k_pages, "k_pages", dtype, 4, dev)
     P, ps = k_pages.shape[:2]
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _need_shape(t, name, (P, ps, Hkv, D))
+    _need_shape(k_pages, "k_pages", (P, ps, Hkv, D))
+    _need_is(v_pages, "v_pages", dtype, (P, ps, Hkv, D), dev)
     if weights is not None:
-        _need_on(weights, "weights", torch.float32, 3, dev)
-        _need_shape(weights, "weights", (P, Hkv, ps))
+        _need_is(weights, "weights", torch.float32, (P, Hkv, ps), dev)
     if q_out is None:
-        q_out = _new_tensor((B, Hq, S, D), torch.float16, q.device, stream)
+        q_out = _maker(stream)((B, Hq, S, D), dtype=torch.float16, device=q.device)
     else:
         _need_view_on(q_out, "q_out", torch.float16, dev)
         _need_shape(q_out, "q_out", (B, Hq, S, D))
@@ -1044,7 +1050,7 @@ def kv_paged_rope_append(q, k_new, v_new, slots, k_pages, v_pages, positions, fr
         q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), slots.data_ptr(), _ptr(positions),
         _ptr(freqs), _ptr(q_weight), _ptr(k_weight), q_out.data_ptr(), k_pages.data_ptr(),
         v_pages.data_ptr(), _ptr(weights), B, Hq, Hkv, S, D, rot, 1 if interleaved else 0, axes,
-        c_sections, _strides(q), _strides(k_new), _strides(q_out), k_pages.element_size(), P, ps,
+        c_sections, _strides(q), _strides(k_new), _strides(q_out), 2 if dtype is torch.float16 else 1, P, ps,
         float(eps), float(rope_scale), float(k_scale), float(v_scale), _raw_stream(stream, dev))
     _check("kv_paged_rope_append", rc)
     return q_out
