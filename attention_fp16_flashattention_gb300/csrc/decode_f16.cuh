@@ -801,7 +801,9 @@ __device__ __forceinline__ uint32_t unit_steps(int rows, uint32_t tiles) {
 // where that can be had: with units of one length (`unit` steps, else 0) the same number of CTAs for each, else
 // the same whole number of steps (with few an even one where two sets of warps take them in turn).  A second unit
 // in a range costs O out and Q in, which pass the SM's port to memory beside the caches' stream (64 sequences behind
-// 32,768 tokens: 74 us, 66 without), and units of one KV head that begin together share their tiles in L2.
+// 32,768 tokens: 74 us, 66 without; 32 behind 1,024, six steps each, 24.1 and 18.7), and units of one KV head that begin
+// together share their tiles in L2.  Four steps and fewer a range are as well left as they fall (16 behind 4,096 on one
+// KV head 16.8 us, 17.9 with whole units).
 // Integers: two kernels have to come to the same numbers.
 struct PreSplit {
     uint32_t ctas, total;
@@ -815,7 +817,7 @@ __device__ __forceinline__ PreSplit prefix_split(uint32_t grid, uint32_t pre, ui
     uint32_t n = static_cast<uint32_t>((w * grid + all / 2) / all);
     n = min(max(n, 1u), most);
     uint32_t each = (pre + n - 1) / n;
-    if (each > 8 && unit > 0) {
+    if (each > 4 && unit > 0) {
         const uint32_t units = pre / unit;
         uint32_t k = (n + units / 2) / units;
         if (k * units > most) --k;
