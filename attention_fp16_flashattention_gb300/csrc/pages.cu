@@ -113,11 +113,11 @@ __device__ __forceinline__ int valid_count(const TableArgs& a, bool report) {
 
 __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const TableArgs a) {
     extern __shared__ int s_dyn[];
-    int* start = s_dyn;             // [B] tokens of the sequences before b
+    int* start = s_dyn;             // [B] places of the tokens of the sequences before b
     int* first = s_dyn + a.B;       // [B] pages that they take; kRefused: the stack has none for b
-    int* old = s_dyn + 2 * a.B;     // [B] cached tokens
+    int* old = s_dyn + 2 * a.B;     // [B] cached tokens; kRejected: the sequence's lengths were
     int* after = s_dyn + 3 * a.B;   // [B] and after the call
-    constexpr int kRefused = 0x7FFFFFFF;
+    constexpr int kRefused = 0x7FFFFFFF, kRejected = -1;
     __shared__ int s_taken;
     const int tid = threadIdx.x;
     const bool lead = blockIdx.x == 0;
@@ -126,32 +126,45 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const TableArgs a) 
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     if (tid == 0) s_taken = 0;
+    // Tokens end to end lie where whoever packed them by new_lens put them, so the tokens of a rejected sequence keep
+    // their places between the others' -- unless nothing can have been packed like that: a length that is negative or
+    // beyond the entries, or all of them together.  (In rows of their own nobody's places depend on the others.)
+    const int entries = a.slots && !a.row_tokens ? a.max_tokens : 0x7FFFFFFF;
     int tokens = 0, pages = 0;
     for (int b = b0; b < b1; ++b) {
-        const int n = a.kv_lens[b];
-        int m = a.other[b], need = 0;
+        const int n = a.kv_lens[b], m = a.other[b];
+        int places = m, need = 0, known = n;
         if (n < 0 || n > cap || m < 0 || m > cap - n || (a.row_tokens && m > a.row_tokens)) {
             if (lead) atomicOr(a.status, kDevBadLength);
-            m = 0;
+            if (a.row_tokens || m < 0 || m > entries) places = 0;
+            known = kRejected;
         } else {
             need = pages_of(n + m, a.page_bits) - pages_of(n, a.page_bits);
+            pages += need;
         }
-        start[b] = m;   // this thread's own entries; turned into the prefixes below
+        start[b] = places;   // this thread's own entries; turned into the prefixes below
         first[b] = need;
-        old[b] = n;
-        tokens = sat_add(tokens, m);
-        pages += need;
+        old[b] = known;
+        tokens = sat_add(tokens, places);
     }
     Sums at = block_scan(tokens, pages);
+    if (at.all_x > entries) {
+        tokens = 0;
+        for (int b = b0; b < b1; ++b) {
+            if (old[b] == kRejected) start[b] = 0;
+            tokens = sat_add(tokens, start[b]);
+        }
+        at = block_scan(tokens, pages);
+    }
     int taken = 0;
     for (int b = b0; b < b1; ++b) {
-        const int m = start[b], need = first[b];
+        const int places = start[b], need = first[b], n = old[b];
         const bool served = need == 0 || at.y + need <= stack;
         if (!served && lead) atomicOr(a.status, kDevNoPages);
-        after[b] = served ? old[b] + m : old[b];
+        after[b] = n == kRejected ? a.kv_lens[b] : served ? n + places : n;
         start[b] = at.x;
         first[b] = served ? at.y : kRefused;
-        at.x = sat_add(at.x, m);
+        at.x = sat_add(at.x, places);
         at.y += need;
         if (served && need) taken = at.y;
     }
@@ -196,8 +209,8 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const TableArgs a) 
                 b = find(start, a.B, static_cast<int>(i));
                 off = static_cast<int>(i) - start[b];
             }
-            if (first[b] == kRefused) continue;
             const int n = old[b], t = n + off;
+            if (n == kRejected || first[b] == kRefused) continue;
             const int fresh = (t >> a.page_bits) - pages_of(n, a.page_bits);
             // a token of the page that the old ones end in, or of a new one
             const int32_t* at_page = fresh < 0 ? a.table + static_cast<long long>(b) * a.max_pages + (t >> a.page_bits)

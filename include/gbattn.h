@@ -496,15 +496,18 @@ int attn_diff_prefill_fwd(const void* q, const void* k, const void* v, const flo
  *                    the sequences' new tokens lie end to end; with row_tokens = n > 0, token i of
  *                    sequence b has entry b * n + i, and max_tokens == B * n.  Entries without a token
  *                    are -1.  The pair is what kv_paged_rope_append takes.
- *   token_starts   : int32 [B + 1] or NULL: new tokens of the sequences before b, then of all (not
- *                    beyond 2^31 - 1)
+ *   token_starts   : int32 [B + 1] or NULL: places of the sequences before b among the tokens end to end
+ *                    (rows: their new tokens), then of all (not beyond 2^31 - 1)
  *   A sequence takes the pages that its new tokens need beyond the last one it holds, from the stack's
  *   top, in the order of the sequences; a page's slots are filled in order.  One whose need the stack
  *   cannot meet after all before it (GBATTN_DEV_NO_PAGES) takes none: its length stays, its tokens'
  *   entries are -1 (they keep their places between the others).  Sequences that need no page are not
  *   affected.  A sequence with kv_lens[b] outside [0, max_pages * page_size], or new_lens[b] outside
  *   [0, what is left of that] (or above row_tokens > 0), sets GBATTN_DEV_BAD_LENGTH, stays as it is and
- *   has no tokens.  A free_count outside [0, capacity] sets it too and counts as 0, and so do more
+ *   has no entries but -1.  With row_tokens = 0 its new_lens[b] tokens keep their places, so that the
+ *   others' are where a caller that packs by new_lens has them -- unless new_lens[b] is negative or above
+ *   max_tokens, or the places of all sequences together are (nothing can have been packed by
+ *   such lengths): then it has no places.  A free_count outside [0, capacity] sets it too and counts as 0, and so do more
  *   tokens than max_tokens (row_tokens = 0), of which the first are written.  A page outside
  *   [0, num_phys_pages) sets GBATTN_DEV_BAD_PAGE; its tokens have slot -1.
  *   B <= 4096; page_size a power of two >= 16; num_phys_pages * page_size < 2^31; max_pages * page_size,
