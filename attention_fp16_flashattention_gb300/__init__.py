@@ -823,7 +823,8 @@ def kv_paged_extend(page_table, kv_lens, new_lens, free_pages, free_count, page_
     max_tokens (the sequences' new tokens end to end) or row_tokens (every sequence's in a row of
     its own) asks for the tokens' positions and slots, int32 [max_tokens] or [B,row_tokens], -1
     where there is no token or its sequence is rejected or gets no pages (end to end, such a sequence
-    keeps its places between the others').  Returns (kv_lens_out [B], free_count_out [1], token_starts [B+1],
+    keeps its places between the others').  Tokens past max_tokens have no slot, and kv_lens_out does not
+    count them.  Returns (kv_lens_out [B], free_count_out [1], token_starts [B+1],
     positions, slots); each may be given, the first two as kv_lens and free_count themselves; the
     last three are None where neither max_tokens nor row_tokens asks for them."""
     import torch

@@ -118,14 +118,14 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const TableArgs a) 
     int* old = s_dyn + 2 * a.B;     // [B] cached tokens; kRejected: the sequence's lengths were
     int* after = s_dyn + 3 * a.B;   // [B] and after the call
     constexpr int kRefused = 0x7FFFFFFF, kRejected = -1;
-    __shared__ int s_taken;
+    __shared__ int s_taken, s_gone;
     const int tid = threadIdx.x;
     const bool lead = blockIdx.x == 0;
     const int cap = a.max_pages << a.page_bits;   // at most 2^30
     const int stack = valid_count(a, lead && tid == 0);
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
-    if (tid == 0) s_taken = 0;
+    if (tid == 0) s_taken = s_gone = 0;
     // Tokens end to end lie where whoever packed them by new_lens put them, so the tokens of a rejected sequence keep
     // their places between the others' -- unless nothing can have been packed like that: a length that is negative or
     // beyond the entries, or all of them together.  (In rows of their own nobody's places depend on the others.)
@@ -147,26 +147,45 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const TableArgs a) 
         old[b] = known;
         tokens = sat_add(tokens, places);
     }
-    Sums at = block_scan(tokens, pages);
-    if (at.all_x > entries) {
+    Sums at;
+#pragma unroll 1
+    for (bool again = false;; again = true) {
+        at = block_scan(tokens, pages);
+        if (__builtin_expect(at.all_x <= entries || again, 1)) break;
         tokens = 0;
+#pragma unroll 1
         for (int b = b0; b < b1; ++b) {
             if (old[b] == kRejected) start[b] = 0;
             tokens = sat_add(tokens, start[b]);
         }
-        at = block_scan(tokens, pages);
     }
     int taken = 0;
     for (int b = b0; b < b1; ++b) {
         const int places = start[b], need = first[b], n = old[b];
         const bool served = need == 0 || at.y + need <= stack;
         if (!served && lead) atomicOr(a.status, kDevNoPages);
-        after[b] = n == kRejected ? a.kv_lens[b] : served ? n + places : n;
+        after[b] = served ? n + places : n;
+        if (__builtin_expect(n == kRejected, 0)) after[b] = a.kv_lens[b];
         start[b] = at.x;
         first[b] = served ? at.y : kRefused;
         at.x = sat_add(at.x, places);
         at.y += need;
         if (served && need) taken = at.y;
+    }
+    // More tokens than entries: a token without a slot is not a cached one, and its page stays on the stack (though
+    // the row has it, behind what the sequence holds, where nobody reads).
+    const bool cut = at.all_x > entries;
+    if (__builtin_expect(cut, 0)) {
+        int gone = 0;
+#pragma unroll 1
+        for (int b = b0; b < b1; ++b) {
+            const int n = old[b];
+            if (n == kRejected || first[b] == kRefused) continue;
+            const int have = max(min(after[b] - n, entries - start[b]), 0);
+            after[b] = n + have;
+            if (have) gone = first[b] + pages_of(n + have, a.page_bits) - pages_of(n, a.page_bits);
+        }
+        if (gone) atomicMax(&s_gone, gone);
     }
     taken = __reduce_max_sync(0xffffffffu, taken);
     if ((tid & 31) == 0 && taken) atomicMax(&s_taken, taken);   // (set to 0 two barriers ago)
@@ -179,9 +198,9 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const TableArgs a) 
             if (a.starts) a.starts[b] = start[b];
         }
         if (tid == 0) {
-            *a.count_out = stack - taken;
+            *a.count_out = stack - (cut ? s_gone : taken);
             if (a.starts) a.starts[a.B] = at.all_x;
-            if (a.slots && !a.row_tokens && at.all_x > a.max_tokens) atomicOr(a.status, kDevBadLength);
+            if (cut) atomicOr(a.status, kDevBadLength);
         }
     }
     const int step = kThreads * gridDim.x, self = blockIdx.x * kThreads + tid;

@@ -487,8 +487,8 @@ int attn_diff_prefill_fwd(const void* q, const void* k, const void* v, const flo
  *   kv_lens        : int32 [B], cached tokens of every sequence; new_lens: int32 [B], how many come
  *   free_pages     : int32 [capacity], the pages that no sequence holds, a stack: its first
  *                    free_count[0] entries, the last of them on top.  Only read.
- *   kv_lens_out    : int32 [B], kv_lens + new_lens; free_count_out: int32 [1], what is left on the
- *                    stack.  Each may be the input itself (kv_lens_out == kv_lens, free_count_out ==
+ *   kv_lens_out    : int32 [B], kv_lens + new_lens (less where stated below); free_count_out: int32 [1],
+ *                    what is left on the stack.  Each may be the input itself (kv_lens_out == kv_lens, free_count_out ==
  *                    free_count): a captured step then carries its own state.
  *   positions,
  *   slots          : int32 [max_tokens] each, or both NULL: the place in its sequence of every new
@@ -506,10 +506,12 @@ int attn_diff_prefill_fwd(const void* q, const void* k, const void* v, const flo
  *   [0, what is left of that] (or above row_tokens > 0), sets GBATTN_DEV_BAD_LENGTH, stays as it is and
  *   has no entries but -1.  With row_tokens = 0 its new_lens[b] tokens keep their places, so that the
  *   others' are where a caller that packs by new_lens has them -- unless new_lens[b] is negative or above
- *   max_tokens, or the places of all sequences together are (nothing can have been packed by
- *   such lengths): then it has no places.  A free_count outside [0, capacity] sets it too and counts as 0, and so do more
- *   tokens than max_tokens (row_tokens = 0), of which the first are written.  A page outside
- *   [0, num_phys_pages) sets GBATTN_DEV_BAD_PAGE; its tokens have slot -1.
+ *   max_tokens, or the places of all sequences together are (nothing can have been packed by such
+ *   lengths): then it has no places.  More tokens than max_tokens (row_tokens = 0) set the flag too: the
+ *   first max_tokens have their entries, and lengths and free_count advance by those alone (table
+ *   entries past a new length may be written as well; no call reads them).  A free_count outside
+ *   [0, capacity] sets it and counts as 0.  A page outside [0, num_phys_pages) sets
+ *   GBATTN_DEV_BAD_PAGE; its tokens have slot -1.
  *   B <= 4096; page_size a power of two >= 16; num_phys_pages * page_size < 2^31; max_pages * page_size,
  *   B * max_pages <= 2^30.
  */

@@ -1,0 +1,74 @@
+"""Page tables where a batch brings more tokens than there are entries for their slots (kv_paged_extend):
+lengths and pages advance by the tokens that have slots alone."""
+
+import numpy as np
+import pytest
+
+from oracle import tables as OT
+from tests.test_gpu_tables import make, t
+
+pytestmark = pytest.mark.gpu
+
+
+def held(lens, page):
+    return [-(-n // page) for n in lens]
+
+
+def entries(new, tokens):
+    """Of each sequence's new tokens, those among the first `tokens` end to end."""
+    return [max(0, min(m, tokens - at)) for m, at in zip(new, np.cumsum([0] + list(new)))]
+
+
+def run_cut(gb, lens, new, page, width, spare, tokens, in_place, seed=1):
+    table, stack, pages, P = make(lens, page, spare, width, seed)
+    kept = entries(new, tokens)
+    rt, rl, rs, _, refused = OT.extend(table, lens, kept, stack, page)
+    _, _, _, toks, short = OT.extend(table, lens, new, stack, page)
+    assert not refused and not short
+    gt, gl, gc = t(table), t(lens), t([len(stack)])
+    kw = dict(kv_lens_out=gl, free_count_out=gc) if in_place else {}
+    out = gb.kv_paged_extend(gt, gl, t(new), t(pages), gc, page, P, max_tokens=tokens, **kw)
+    assert gb.device_status() == (gb.DEV_BAD_LENGTH if sum(new) > tokens else 0)
+    assert out[0].tolist() == rl and out[1].item() == len(rs)
+    got = gt.cpu().numpy()
+    for b, n in enumerate(held(rl, page)):
+        assert np.array_equal(got[b, :n], rt[b, :n]), b
+    pos, slots, starts = OT.packed(toks, tokens)
+    assert np.array_equal(out[3].cpu().numpy(), pos) and np.array_equal(out[4].cpu().numpy(), slots)
+    assert out[2].tolist() == starts.tolist()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_tokens_without_an_entry_are_not_cached(gb, in_place):
+    for tokens in (1, 6, 7, 99, 100, 101, 120, 150, 151, 209, 210):
+        run_cut(gb, [10, 20, 30], [100, 50, 60], 16, 20, 40, tokens, in_place)
+    # behind the last entry: a sequence that needs no page, one with no tokens
+    run_cut(gb, [0, 1, 32, 15], [20, 3, 0, 1], 16, 4, 9, 20, in_place)
+    rng = np.random.default_rng(4)
+    for B, top in ((4096, 9), (513, 200), (3, 40000)):
+        lens = [int(x) for x in rng.integers(0, 500, B)]
+        new = [int(x) for x in rng.integers(0, top + 1, B)]
+        for part in (0.1, 0.5, 0.99):
+            run_cut(gb, lens, new, 16, -(-(500 + top) // 16) + 1, sum(new) // 16 + B + 5,
+                    max(1, int(part * sum(new))), in_place, seed=B)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_the_rest_comes_with_the_next_call(gb, in_place):
+    """What had no entry is brought again: every page is held once, and all of them come back."""
+    lens, new, page, width = [10, 20, 30], [100, 50, 60], 16, 20
+    table, stack, pages, P = make(lens, page, 40, width, 7)
+    gt, gl, gp, gc = t(table), t(lens), t(pages), t([len(stack)])
+    left = list(new)
+    for tokens in (120, 45, 200):
+        kw = dict(kv_lens_out=gl, free_count_out=gc) if in_place else {}
+        gl, gc, *_ = gb.kv_paged_extend(gt, gl, t(left), gp, gc, page, P, max_tokens=tokens, **kw)
+        left = [m - k for m, k in zip(left, entries(left, tokens))]
+        assert gb.device_status() == (gb.DEV_BAD_LENGTH if sum(left) else 0)
+        assert gl.tolist() == [n + m - x for n, m, x in zip(lens, new, left)]
+        got = gt.cpu().numpy()
+        mine = [p for b, n in enumerate(held(gl.tolist(), page)) for p in got[b, :n].tolist()]
+        assert sorted(mine + gp.tolist()[:gc.item()]) == list(range(P))
+    assert left == [0, 0, 0]
+    gc = gb.kv_paged_release(gt, gl, gp, gc, page, P)
+    assert gb.device_status() == 0 and sorted(gp.tolist()[:gc.item()]) == list(range(P))
