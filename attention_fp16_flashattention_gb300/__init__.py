@@ -199,7 +199,8 @@ def set_wait_limit_ns(ns):
 
 def test_inject_fault(mode):
     """Test hook: 1 makes attention launches skip their query load, 2 stops their K/V loads
-    after two rounds of the ring (timeout paths, mid-stream for 2); 0 restores."""
+    after two rounds of the ring, or after one tile in the FP16 decodes' form for short caches
+    (timeout paths, mid-stream for 2); 0 restores."""
     _check("gbattn_test_inject_fault", load().gbattn_test_inject_fault(int(mode)))
 
 

@@ -62,7 +62,7 @@ struct DecodeF16Args {
     uint4* tiles;         // with scores: what the weights kernel needs to know of each tile
     uint32_t* status;
     uint64_t wait_limit;
-    int fault;   // test hook: 1 = no stage is loaded, 2 = loads stop after two ring rounds
+    int fault;   // test hook: 1 = no stage is loaded, 2 = loads stop after two ring rounds (kOne: one tile)
     int B, Hq, Hkv, nq, G, pairs, num_phys, ps, max_pages, max_kv;
     int side_bits, sets;  // row groups: `side` = 2^side_bits side by side in a CTA, `sets` such sets
     int maps;             // 1, or 2: row r is map r % 2 of query r / 2
@@ -318,9 +318,9 @@ __device__ __forceinline__ void decode_f16_body(const CUtensorMap& tk, const CUt
     };
 
     const uint32_t n_tiles = u_end - u_beg;
-    // test hook: the waits for stages never loaded run out (bounded) mid-range
+    // test hook: the waits for stages never loaded run out (bounded) mid-range (a cluster's warp has no two rounds)
     const uint32_t n_load = a.fault == 1 ? 0u
-                            : a.fault == 2 ? min(n_tiles, static_cast<uint32_t>(2 * C::kStages))
+                            : a.fault == 2 ? min(n_tiles, static_cast<uint32_t>(kOne ? 1 : 2 * C::kStages))
                                            : n_tiles;
     long long src_cur = tile_src(u_beg + lane);          // tiles 0..31 of the range, one per lane
     long long src_next = tile_src(u_beg + 32 + lane);    // tiles 32..63

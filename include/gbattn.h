@@ -133,7 +133,8 @@ uint64_t gbattn_launch_count(void);
  * the waits run out mid-stream with tensor-core work in flight (in the fused
  * paged prefill, the E4M3 converter warps' waits run out too).  In the paged
  * decode, mode 1 makes every warp load no stage and mode 2 stop after two
- * rounds of its own ring.  Either way the kernel records
+ * rounds of its own ring (after one tile where a short FP16 cache's decode runs
+ * in clusters, whose warps have no two rounds).  Either way the kernel records
  * GBATTN_DEV_WAIT_TIMEOUT, lets its copies and MMAs finish, frees its tensor
  * memory and returns (outputs are then undefined).  mode 0 (default) restores
  * normal operation.  Returns GBATTN_OK or GBATTN_ERR_SHAPE. */
