@@ -656,7 +656,8 @@ def kv_paged_evict(k_pages, v_pages, weights, page_table, kv_lens, budget, sink=
                    dst_table=None, max_kv_len=None, new_lens=None, kept=None, stream=None):
     """Evict the tokens of paged caches (FP16 or uint8 E4M3 pages) that received the least
     attention: every KV head keeps its first `sink` tokens, its last `recent` and the heaviest of
-    the rest, `budget` in all, in slots 0.. of dst_table's pages (None: in place).  Returns
+    the rest, `budget` in all, in slots 0.. of dst_table's pages (None: in place).  Rotated keys keep
+    their rotation, so positions of later tokens go on from the text, not from new_lens.  Returns
     (new_lens int32 [B], kept int32 [B,Hkv,budget]: old slots, -1 past the new length)."""
     import torch
     if not isinstance(k_pages, torch.Tensor) or k_pages.dtype not in (torch.float16, torch.uint8):
@@ -825,7 +826,8 @@ def kv_paged_extend(page_table, kv_lens, new_lens, free_pages, free_count, page_
     its own) asks for the tokens' positions and slots, int32 [max_tokens] or [B,row_tokens], -1
     where there is no token or its sequence is rejected or gets no pages (end to end, such a sequence
     keeps its places between the others').  Tokens past max_tokens have no slot, and kv_lens_out does not
-    count them.  Returns (kv_lens_out [B], free_count_out [1], token_starts [B+1],
+    count them.  A position is the token's place in the cache: after kv_paged_evict, what the sequence
+    has lost is to be added before queries and keys are rotated by it.  Returns (kv_lens_out [B], free_count_out [1], token_starts [B+1],
     positions, slots); each may be given, the first two as kv_lens and free_count themselves; the
     last three are None where neither max_tokens nor row_tokens asks for them."""
     import torch
@@ -1019,7 +1021,8 @@ def kv_paged_rope_append(q, k_new, v_new, slots, k_pages, v_pages, positions, fr
                          k_weight=None, eps=1e-6, interleaved=False, sections=None, rope_scale=1.0,
                          k_scale=1.0, v_scale=1.0, weights=None, q_out=None, stream=None):
     """qk_norm_rope_f16 on the way into a paged cache: q [B,Hq,S,D] goes to q_out, k_new [B,Hkv,S,D]
-    to its slots int32 [B,S] (kv_paged_extend; negative: padding) of k_pages [P,page,Hkv,D], and
+    to its slots int32 [B,S] (kv_paged_extend; negative: padding) of k_pages [P,page,Hkv,D], by its
+    position in the text (kv_paged_extend's, and what kv_paged_evict has taken from the sequence), and
     v_new, not rotated, to those of v_pages.  Pages are FP16, or uint8 E4M3 codes of value / scale
     (k_scale, v_scale).  weights FP32 [P,Hkv,page] gets zeros at the new slots.  Tokens packed end to
     end are B = 1 and S tokens.  Returns q_out."""

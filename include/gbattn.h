@@ -406,7 +406,8 @@ int attn_paged_decode_shared_f16_fwd(const void* q, const void* k_pages, const v
  *   for itself, its first `sink` tokens, its last `recent` and the heaviest of those between, up to
  *   budget in all; of equal weights the lower slot is kept, a NaN weighs less than any number.  The
  *   kept rows of K and V and their weights go to slots 0 .. new_lens[b] - 1 of dst_table's pages in
- *   their old order.  Everything else in the pool stays as it is.
+ *   their old order, keys as they are: a rotated one keeps the rotation of the place where it came
+ *   (positions of kv_paged_extend).  Everything else in the pool stays as it is.
  *   In place, a page that is moved in must belong to one sequence only.  With other pages, no page
  *   of dst_table may be read or written for another purpose by the same call (so shared pages can be
  *   evicted from, into fresh ones); of this a sequence's own page in the same place of both tables,
@@ -492,11 +493,14 @@ int attn_diff_prefill_fwd(const void* q, const void* k, const void* v, const flo
  *                    what is left on the stack.  Each may be the input itself (kv_lens_out == kv_lens, free_count_out ==
  *                    free_count): a captured step then carries its own state.
  *   positions,
- *   slots          : int32 [max_tokens] each, or both NULL: the place in its sequence of every new
- *                    token, and its slot page * page_size + offset in the pool.  With row_tokens = 0
+ *   slots          : int32 [max_tokens] each, or both NULL: the place of every new token in its
+ *                    sequence's cache, and its slot page * page_size + offset in the pool.  With row_tokens = 0
  *                    the sequences' new tokens lie end to end; with row_tokens = n > 0, token i of
  *                    sequence b has entry b * n + i, and max_tokens == B * n.  Entries without a token
- *                    are -1.  The pair is what kv_paged_rope_append takes.
+ *                    are -1.  The pair is what kv_paged_rope_append takes.  After an eviction the
+ *                    cache holds fewer tokens than have come, and keys that stay keep the rotation
+ *                    of the places where they came: the positions to rotate by are then these and
+ *                    what the sequence has lost (kv_lens[b] - new_lens[b] of its kv_paged_evict calls).
  *   token_starts   : int32 [B + 1] or NULL: places of the sequences before b among the tokens end to end
  *                    (rows: their new tokens), then of all (not beyond 2^31 - 1)
  *   A sequence takes the pages that its new tokens need beyond the last one it holds, from the stack's
@@ -557,7 +561,7 @@ int kv_paged_release(const int32_t* page_table, const int32_t* kv_lens, const in
  *   sections[i] (a host array, summing to rot / 2) of the pairs, one axis after the other, take
  *   their position from axis i; sections may be NULL with one axis.  FP32 throughout (angles to a
  *   2^-32 of a turn), rounded to FP16 once.
- *   A token with a negative position is padding: its rows of q_out and k_out are left as they are.
+ *   A token with a negative position (on any axis) is padding: its rows of q_out and k_out are left as they are.
  *   rot = 0: no rotation; positions (NULL, or for the padding alone), freqs, sections and rope_scale unused.
  *   In place: q_out == q with the same strides, k_out == k likewise.  q_out may also lie in one packed
  *   tensor with k (and k_out with q) where both have the same batch and row strides and their heads lie in
@@ -578,6 +582,7 @@ int qk_norm_rope_f16(const void* q, const void* k, const int32_t* positions, con
  * Cites: "Integrate FP32 v37 prefill and exact E4M3 bridge", Implementation (paged cache; E4M3 codes
  * with a scale).
  *   k_new, v_new : [B][Hkv][S][D] FP16 (they share kv_strides)
+ *   positions    : the tokens' places in their texts, kv_paged_extend's as long as nothing was evicted (there)
  *   slots        : int32 [B][S], where each token goes: page * page_size + offset (kv_paged_extend).  A
  *                  negative slot is padding, like a negative position: q_out and the pages stay as they are
  *                  for that token.  No two tokens of a call may have the same slot.
