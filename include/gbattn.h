@@ -536,6 +536,8 @@ int kv_paged_extend(int32_t* page_table, const int32_t* kv_lens, const int32_t* 
  *   The pages of tokens keep_lens[b] .. kv_lens[b] - 1 that hold none before keep_lens[b] go onto the
  *   stack, in the order of the sequences and of their rows.  page_table stays as it is (entries
  *   past a sequence's pages are not read by any call).  A page must not be given back twice.
+ *   A free_count outside [0, capacity] sets GBATTN_DEV_BAD_LENGTH and counts as 0, as in kv_paged_extend: what
+ *   was on the stack is lost, and free_pages is written from its first entry on.
  *   A sequence with kv_lens[b] outside [0, max_pages * page_size] or keep_lens[b] outside [0, kv_lens[b]]
  *   (GBATTN_DEV_BAD_LENGTH), with a page to be given back outside [0, num_phys_pages)
  *   (GBATTN_DEV_BAD_PAGE), or whose pages no longer fit on the stack (GBATTN_DEV_NO_PAGES; nor do
