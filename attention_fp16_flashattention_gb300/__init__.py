@@ -621,7 +621,9 @@ def attn_paged_decode_shared_f16_fwd(q, k_pages, v_pages, page_table, kv_lens, g
     group_starts[g+1]-1 (int32 [groups+1], from 0 to B) have their first prefix_lens[g] tokens (int32
     [groups], multiples of the page size) in the pages of the first of them, and those are read once.
     kv_lens counts prefix and own tokens.  max_prefix_len and max_own_len (what is behind the
-    prefix) default to max_pages * page_size."""
+    prefix) default to max_pages * page_size each; near the longest ones they let short caches run in
+    one kernel and keep the workspace small.  Prefixes of a few hundred tokens, or of few sequences, are
+    as quick with attn_paged_decode_f16_fwd."""
     import torch
     dev = _current_device(q, "q")
     _need_on(q, "q", torch.float16, 4, dev)

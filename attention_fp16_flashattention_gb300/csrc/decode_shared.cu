@@ -31,9 +31,15 @@
 //
 // Measured (graph replays): 64 sequences behind 16,384 tokens with 100 to 2,001 of their own, 32 on 8 heads of 128
 // (351 MB; 67 of them the prefix) 71 to 76 us, where the ordinary decode, to which that is 4.6 GB, takes 345; at D = 64 48;
-// 8 behind 131,072 (32 rows a KV head) 91 us, 0.87 of the measured copy; 64 behind as many (256 rows) 147 us, 490 TFLOP/s without the lo
-// halves, a step of 128 rows and 64 tokens in 1,030 cycles of which the tensor pipe has 900 to do.  8 behind 1,024 with
-// up to 300 of their own in the form for short caches 10.7 us (the ordinary decode 10.5).
+// 8 behind 131,072 (32 rows a KV head) 91 to 99 us, 0.80 to 0.87 of the measured copy; 64 behind as many (256 rows) 147 to 156 us,
+// 880 to 935 TFLOP/s without the lo halves, a step of 128 rows and 64 tokens in 1,030 cycles of which the tensor pipe has 900
+// to do.  8 behind 1,024 with up to 300 of their own in the form for short caches 10.7 us (the ordinary decode 10.5).
+//
+// Against the ordinary decode (one group with up to 300 own tokens each; this call's time first): the form for short
+// caches costs 0.2 to 0.7 us for the groups.  Beyond it, 32 on 8 heads of 128: 16 sequences behind 1,024 tokens 16.9 and
+// 17.2 us, 4 behind 4,096 16.2 and 16.8, 2 15.1 and 12.7; 6 on 1 of 256: 32 behind 1,024 15.8 and 16.4, 4 behind 4,096
+// 13.5 and 14.3, 2 13.2 and 12.4.  Prefixes of a tile or two are better read with the sequences' own tokens: 32 sequences
+// behind 64 on 8 heads of 128 36 and 15 us, since few CTAs then take several units each, one after the other.
 //
 // Every wait is bounded in time (WaitCtl): one that runs out records GBATTN_DEV_WAIT_TIMEOUT, the CTA stops,
 // waits a bounded time for its copies and MMAs in flight, frees tensor memory and exits.
@@ -136,7 +142,8 @@ __device__ __forceinline__ uint32_t block_sum(uint32_t x, uint32_t& all) {
 }
 
 // A shared-memory descriptor `bytes` further on: only the address field changes, and within 32 bits.  (Made anew
-// for every MMA, the descriptors took as long as the MMAs: 512 rows behind 131,072 tokens 160 us, so 145.)
+// for every MMA, the descriptors took as long as the MMAs: behind 131,072 tokens 256 rows on each of 8 KV heads took 170 us
+// and so 155, 512 on each of 4 167 and 150.)
 __device__ __forceinline__ uint64_t desc_at(uint64_t desc, int bytes) {
     return (desc & 0xFFFFFFFF00000000ull) | (static_cast<uint32_t>(desc) + static_cast<uint32_t>(bytes >> 4));
 }

@@ -14,7 +14,7 @@
 //
 // Bound by latency: the lengths, the stack's or the table's entries and the stores, one
 // behind the other; 8 bytes a token and 8 a page are nothing beside that.  Measured (graph replays): one
-// token for 64 sequences 4.0 us, 32 prompts of 131,000 tokens 4.6, drafted tokens of 64 sequences back 4.0,
+// token for 64 sequences 4.0 us, 32 prompts of 131,000 tokens 4.7, drafted tokens of 64 sequences back 4.0,
 // 100,000 pages back 7.3, 262,000 27 (a cluster of 16 CTAs looks at each of them; of eight 13.8 and 56, with 1024 threads
 // a CTA 9.5 and 34, but then 4.9 for the few).
 #include <cooperative_groups.h>

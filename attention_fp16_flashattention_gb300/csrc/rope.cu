@@ -33,7 +33,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxAxes = 3;
 // Blocks per SM (80 registers) and row steps under way in a warp: 3 and 4.  Video tokens, prompts, E4M3: 133, 86, 16.1
-// us; 3 and 2 144, 94, 15.1; 4 and 2 139, 95, 17.9; 2 and 4 147, 94, 15.3.
+// us; 3 and 2 144, 94, 15.1; 4 and 2 139, 95, 17.9; 2 and 4 147, 94, 15.3.  One pair for all stores, though E4M3 would be a
+// little quicker with two steps.  80 registers are not quite enough: 8 to 36 bytes are spilled for dense rows, 40 to 52 for
+// FP16 pages, 52 to 68 for E4M3.
 constexpr int kBlocks = 3, kAhead = 4;
 
 struct View {   // [B][H][S][D] rows
