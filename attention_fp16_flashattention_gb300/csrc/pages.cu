@@ -111,13 +111,49 @@ __device__ __forceinline__ int valid_count(const TableArgs& a, bool report) {
     return 0;
 }
 
+constexpr int kRefused = 0x7FFFFFFF, kRejected = -1;
+
+// What kv_extend_kernel does where there are more places than entries, out of its way (inlined, the code that calls
+// hardly ever take cost 0.1 us of 4).
+//
+// Beside a sequence by whose length nobody can have packed, places that are together beyond the entries are nobody's
+// either: then only the sound sequences have theirs.  The thread's own of those, or -1 where all stay.
+__device__ __noinline__ int drop_rejected(const int32_t* new_lens, int* start, const int* old, int b0, int b1, int most) {
+    bool wild = false;
+    int tokens = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        if (old[b] == kRejected) wild = wild || new_lens[b] < 0 || new_lens[b] > most;
+        else tokens = sat_add(tokens, start[b]);
+    }
+    if (!__syncthreads_or(wild)) return -1;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b)
+        if (old[b] == kRejected) start[b] = 0;
+    return tokens;
+}
+// A token without an entry is not a cached one, and its page stays on the stack (though the row has it, behind what
+// the sequence holds, where nobody reads).
+__device__ __noinline__ void cut_tokens(const int* start, const int* first, const int* old, int* after, int b0, int b1,
+                                        int entries, int page_bits, int* gone) {
+    int most = 0;
+#pragma unroll 1
+    for (int b = b0; b < b1; ++b) {
+        const int n = old[b];
+        if (n == kRejected || first[b] == kRefused) continue;
+        const int have = max(min(after[b] - n, entries - start[b]), 0);
+        after[b] = n + have;
+        if (have) most = first[b] + pages_of(n + have, page_bits) - pages_of(n, page_bits);
+    }
+    if (most) atomicMax(gone, most);
+}
+
 __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const TableArgs a) {
     extern __shared__ int s_dyn[];
     int* start = s_dyn;             // [B] places of the tokens of the sequences before b
     int* first = s_dyn + a.B;       // [B] pages that they take; kRefused: the stack has none for b
     int* old = s_dyn + 2 * a.B;     // [B] cached tokens; kRejected: the sequence's lengths were
     int* after = s_dyn + 3 * a.B;   // [B] and after the call
-    constexpr int kRefused = 0x7FFFFFFF, kRejected = -1;
     __shared__ int s_taken, s_gone;
     const int tid = threadIdx.x;
     const bool lead = blockIdx.x == 0;
@@ -127,16 +163,17 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const TableArgs a) 
     const int b0 = min(tid * per, a.B), b1 = min(b0 + per, a.B);
     if (tid == 0) s_taken = s_gone = 0;
     // Tokens end to end lie where whoever packed them by new_lens put them, so the tokens of a rejected sequence keep
-    // their places between the others' -- unless nothing can have been packed like that: a length that is negative or
-    // beyond the entries, or all of them together.  (In rows of their own nobody's places depend on the others.)
+    // their places between the others' -- unless nobody can have packed by its length: a negative one, or one that neither
+    // the entries nor a row could hold.  (In rows of their own nobody's places depend on the others.)
     const int entries = a.slots && !a.row_tokens ? a.max_tokens : 0x7FFFFFFF;
+    const int most = max(entries, cap);
     int tokens = 0, pages = 0;
     for (int b = b0; b < b1; ++b) {
         const int n = a.kv_lens[b], m = a.other[b];
         int places = m, need = 0, known = n;
         if (n < 0 || n > cap || m < 0 || m > cap - n || (a.row_tokens && m > a.row_tokens)) {
             if (lead) atomicOr(a.status, kDevBadLength);
-            if (a.row_tokens || m < 0 || m > entries) places = 0;
+            if (a.row_tokens || m < 0 || m > most) places = 0;
             known = kRejected;
         } else {
             need = pages_of(n + m, a.page_bits) - pages_of(n, a.page_bits);
@@ -151,42 +188,24 @@ __global__ void __launch_bounds__(kThreads) kv_extend_kernel(const TableArgs a) 
 #pragma unroll 1
     for (bool again = false;; again = true) {
         at = block_scan(tokens, pages);
-        if (__builtin_expect(at.all_x <= entries || again, 1)) break;
-        tokens = 0;
-#pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            if (old[b] == kRejected) start[b] = 0;
-            tokens = sat_add(tokens, start[b]);
-        }
+        if (at.all_x <= entries || again) break;
+        tokens = drop_rejected(a.other, start, old, b0, b1, most);
+        if (tokens < 0) break;
     }
     int taken = 0;
     for (int b = b0; b < b1; ++b) {
         const int places = start[b], need = first[b], n = old[b];
         const bool served = need == 0 || at.y + need <= stack;
         if (!served && lead) atomicOr(a.status, kDevNoPages);
-        after[b] = served ? n + places : n;
-        if (__builtin_expect(n == kRejected, 0)) after[b] = a.kv_lens[b];
+        after[b] = n == kRejected ? a.kv_lens[b] : served ? n + places : n;
         start[b] = at.x;
         first[b] = served ? at.y : kRefused;
         at.x = sat_add(at.x, places);
         at.y += need;
         if (served && need) taken = at.y;
     }
-    // More tokens than entries: a token without a slot is not a cached one, and its page stays on the stack (though
-    // the row has it, behind what the sequence holds, where nobody reads).
     const bool cut = at.all_x > entries;
-    if (__builtin_expect(cut, 0)) {
-        int gone = 0;
-#pragma unroll 1
-        for (int b = b0; b < b1; ++b) {
-            const int n = old[b];
-            if (n == kRejected || first[b] == kRefused) continue;
-            const int have = max(min(after[b] - n, entries - start[b]), 0);
-            after[b] = n + have;
-            if (have) gone = first[b] + pages_of(n + have, a.page_bits) - pages_of(n, a.page_bits);
-        }
-        if (gone) atomicMax(&s_gone, gone);
-    }
+    if (cut) cut_tokens(start, first, old, after, b0, b1, entries, a.page_bits, &s_gone);
     taken = __reduce_max_sync(0xffffffffu, taken);
     if ((tid & 31) == 0 && taken) atomicMax(&s_taken, taken);   // (set to 0 two barriers ago)
     if (a.in_place) cg::this_cluster().sync();   // every CTA has read the old lengths and count

@@ -511,8 +511,8 @@ int attn_diff_prefill_fwd(const void* q, const void* k, const void* v, const flo
  *   [0, what is left of that] (or above row_tokens > 0), sets GBATTN_DEV_BAD_LENGTH, stays as it is and
  *   has no entries but -1.  With row_tokens = 0 its new_lens[b] tokens keep their places, so that the
  *   others' are where a caller that packs by new_lens has them -- unless new_lens[b] is negative or above
- *   max_tokens, or the places of all sequences together are (nothing can have been packed by such
- *   lengths): then it has no places.  More tokens than max_tokens (row_tokens = 0) set the flag too: the
+ *   both max_tokens and max_pages * page_size, by which nothing can have been packed: then it has none,
+ *   and where all places are then still more than max_tokens no rejected sequence has any.  More tokens than max_tokens (row_tokens = 0) set the flag too: the
  *   first max_tokens have their entries, and lengths and free_count advance by those alone (table
  *   entries past a new length may be written as well; no call reads them).  A free_count outside
  *   [0, capacity] sets it and counts as 0.  A page outside [0, num_phys_pages) sets

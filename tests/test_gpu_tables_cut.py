@@ -54,6 +54,29 @@ def test_tokens_without_an_entry_are_not_cached(gb, in_place):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("tokens", [3, 4, 12, 13, 15, 17, 18])
+def test_rejected_sequences_keep_their_places_in_a_cut(gb, tokens, in_place):
+    """A request whose row is full in the middle: the others' tokens stay where they were packed."""
+    lens, new, page, width = [16, 160, 10], [4, 9, 5], 16, 10
+    table, stack, pages, P = make([16, 0, 10], page, 9, width, 8)
+    kept = entries(new, tokens)
+    good = [0, 2]
+    rt, rl, rs, _, _ = OT.extend(table[good], [16, 10], [kept[b] for b in good], stack, page)
+    _, _, _, toks, _ = OT.extend(table[good], [16, 10], [4, 5], stack, page)
+    gt, gl, gc = t(table), t(lens), t([len(stack)])
+    kw = dict(kv_lens_out=gl, free_count_out=gc) if in_place else {}
+    out = gb.kv_paged_extend(gt, gl, t(new), t(pages), gc, page, P, max_tokens=tokens, **kw)
+    assert gb.device_status() == gb.DEV_BAD_LENGTH
+    assert out[0].tolist() == [rl[0], 160, rl[1]] and out[1].item() == len(rs)
+    got = gt.cpu().numpy()
+    for row, b, n in zip(rt, good, held(rl, page)):
+        assert np.array_equal(got[b, :n], row[:n])
+    pos, slots, starts = OT.packed([toks[0], ([-1] * 9,) * 2, toks[1]], tokens)
+    assert out[2].tolist() == starts.tolist()
+    assert np.array_equal(out[3].cpu().numpy(), pos) and np.array_equal(out[4].cpu().numpy(), slots)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 def test_the_rest_comes_with_the_next_call(gb, in_place):
     """What had no entry is brought again: every page is held once, and all of them come back."""
     lens, new, page, width = [10, 20, 30], [100, 50, 60], 16, 20

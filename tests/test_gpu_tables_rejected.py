@@ -47,11 +47,12 @@ def test_rejected_sequences_keep_their_places(gb, in_place):
     run_rejected(gb, [0, 3, 0], [7, 200, 20], [1], 16, 10, 9, 250, in_place)
     # cached lengths out of range
     run_rejected(gb, [16, -1, 161, 2 ** 31 - 1, 9], [2, 3, 4, 5, 6], [1, 2, 3], 16, 10, 9, 20, in_place)
-    # nothing can have been packed by a negative length, or by one above the entries
+    # nothing can have been packed by a negative length, or by one that neither the entries nor a row could hold
     run_rejected(gb, [16, 30, 10, 7], [1, -3, 2 ** 31 - 1, 5], [1, 2], 16, 10, 9, 9, in_place,
                  places=[1, 0, 0, 5])
-    # nor by lengths whose sum is above them
-    run_rejected(gb, [16, 160, 10], [4, 9, 5], [1], 16, 10, 9, 17, in_place, places=[4, 0, 5])
+    # nor, beside such a one, by lengths whose sum is above them
+    run_rejected(gb, [16, 160, 10, 30], [4, 9, 5, -1], [1, 3], 16, 10, 9, 17, in_place, places=[4, 0, 5, 0])
+    run_rejected(gb, [16, 160, 10, 30], [4, 9, 5, 33], [1, 3], 16, 2, 9, 17, in_place, places=[4, 0, 5, 0])
 
 
 @pytest.mark.parametrize("in_place", [False, True])
