@@ -143,7 +143,8 @@ __device__ __noinline__ void cut_tokens(const int* start, const int* first, cons
         if (n == kRejected || first[b] == kRefused) continue;
         const int have = max(min(after[b] - n, entries - start[b]), 0);
         after[b] = n + have;
-        if (have) most = first[b] + pages_of(n + have, page_bits) - pages_of(n, page_bits);
+        const int pages = pages_of(n + have, page_bits) - pages_of(n, page_bits);
+        if (pages) most = first[b] + pages;   // (of one that needs none, first counts what others did not get)
     }
     if (most) atomicMax(gone, most);
 }

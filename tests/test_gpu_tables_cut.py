@@ -77,6 +77,25 @@ def test_rejected_sequences_keep_their_places_in_a_cut(gb, tokens, in_place):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+def test_too_few_pages_and_entries(gb, in_place):
+    """Behind a sequence that gets no pages, one that needs none, and the end of the entries."""
+    lens, new, page, width = [16, 0, 30, 8], [20, 60, 2, 7], 16, 8
+    table, stack, pages, P = make(lens, page, 20, width, 9, free=3)    # 2 pages taken, 4 not there
+    rt, rl, rs, toks, refused = OT.extend(table, lens, new, stack, page)
+    assert refused == [1] and len(rs) == 1
+    for tokens in (83, 85, 89):
+        gt, gl, gc = t(table), t(lens), t([len(stack)])
+        kw = dict(kv_lens_out=gl, free_count_out=gc) if in_place else {}
+        out = gb.kv_paged_extend(gt, gl, t(new), t(pages), gc, page, P, max_tokens=tokens, **kw)
+        assert gb.device_status() == gb.DEV_NO_PAGES | (gb.DEV_BAD_LENGTH if tokens < 89 else 0)
+        kept = entries(new, tokens)
+        assert out[0].tolist() == [36, 0, 30 + kept[2], 8 + kept[3]] and out[1].item() == len(rs)
+        pos, slots, starts = OT.packed(toks, tokens)
+        assert out[2].tolist() == starts.tolist() and np.array_equal(gt.cpu().numpy(), rt)
+        assert np.array_equal(out[3].cpu().numpy(), pos) and np.array_equal(out[4].cpu().numpy(), slots)
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 def test_the_rest_comes_with_the_next_call(gb, in_place):
     """What had no entry is brought again: every page is held once, and all of them come back."""
     lens, new, page, width = [10, 20, 30], [100, 50, 60], 16, 20
